@@ -19,7 +19,10 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_ep.s
 
 OK, EINVAL, ECAP, EDTYPE, EALIGN, EWORKSPACE, EHIP, ESCRATCH = 0, -1, -2, -3, -4, -5, -6, -7
 NOALLOC_SCRATCH_BYTES = 8 << 20
-BF16, F32 = 0, 1
+BF16, F32, E4M3 = 0, 1, 2
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "silu_gated": 3}
+SCALE_BLOCK = 128     # columns (and, in a weight matrix, rows) under one fp8 scale
 ERR_ID_RANGE, ERR_PICKS, ERR_ELOC, ERR_ROWCAP, ERR_CNT = 1, 2, 4, 8, 16
 MAX_PAYLOADS = 8
 
@@ -40,6 +43,10 @@ EXPORTED = (
     "moe_ep_combine_unpack_fused",
     "moe_ep_dispatch_pack_noalloc",
     "moe_ep_expert_batch_ranked",
+    "moe_ep_route_topk",
+    "moe_ep_expert_matmul",
+    "moe_ep_expert_matmul_fp8",
+    "moe_ep_matmul",
 )
 
 
@@ -61,6 +68,7 @@ class MoeEpError(RuntimeError):
 
 _lib = None
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+_F32 = ctypes.c_float
 
 
 def load(path: Optional[str] = None) -> ctypes.CDLL:
@@ -112,6 +120,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_ep_combine_unpack_fused.argtypes = [
         _P, _I64, _I32, _I64, _P, _I64, _I32, _I64, _I32, _P, _I64, _P, _P, _P,
         _I32, _I32, _P, _P]
+    lib.moe_ep_route_topk.argtypes = [
+        _P, _I64, _I32, _P, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _F32, _P, _P, _P]
+    lib.moe_ep_expert_matmul.argtypes = [
+        _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64, _I32, _P, _I64, _I32, _P]
+    lib.moe_ep_expert_matmul_fp8.argtypes = [
+        _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I64, _I64, _I64, _I32,
+        _P, _I64, _I32, _P, _I64, _P]
+    lib.moe_ep_matmul.argtypes = [
+        _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _I32, _P]
     for name in EXPORTED:
         if name != "moe_ep_status_string":
             getattr(lib, name).restype = ctypes.c_int
@@ -818,3 +835,194 @@ def moe_ep_combine_unpack_fused(back, token_slot, max_num_tokens, self_rank, exp
                                 stream=None) -> None:
     prepare_combine_unpack_fused(back, token_slot, max_num_tokens, self_rank, expert_out,
                                  self_eloc, self_w, self_row, e_local, K, out)(stream)
+
+
+# ---------------------------------------------------------------------------
+# The router's choice and the products
+# ---------------------------------------------------------------------------
+
+def _choice(table, name, what: str) -> int:
+    if name not in table:
+        raise ValueError(f"{what} must be one of {sorted(table)}, not {name!r}")
+    return table[name]
+
+
+def _rows_dense(t: torch.Tensor, first: int, name: str):
+    """The dims from `first` on are dense and each block before them starts
+    at or behind the end of the one before."""
+    _dense_from(t, first, name)
+    n = 1
+    for x in t.shape[first:]:
+        n *= x
+    if t.size(0) > 1 and first == 1 and t.stride(0) < n:
+        raise ValueError(f"{name}: blocks along dim 0 overlap")
+
+
+def _lead_stride(t: torch.Tensor) -> int:
+    """Elements between the blocks along dim 0 (a single block: its size, as
+    the stride of a dim of one may be anything)."""
+    if t.size(0) > 1:
+        return t.stride(0)
+    n = 1
+    for x in t.shape[1:]:
+        n *= x
+    return n
+
+
+def prepare_route_topk(logits: torch.Tensor, topk_ids: torch.Tensor,
+                       topk_weights: torch.Tensor, score: str = "softmax",
+                       bias: Optional[torch.Tensor] = None, n_group: int = 1,
+                       topk_group: int = 1, renormalize: bool = True,
+                       scale: float = 1.0) -> PreparedCall:
+    """logits: bf16 or fp32 [T, E] (token stride free); topk_ids int32 and
+    topk_weights fp32, [T, K] dense, as moe_ep_dispatch_pack takes them;
+    bias: fp32 [E]."""
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and topk_ids [T, K]")
+    T, E = logits.shape
+    K = topk_ids.size(1)
+    dtype = _dtype_code(logits)
+    _rows_dense(logits, 1, "logits")
+    _shape(topk_ids, (T, K), "topk_ids", _I32T)
+    _shape(topk_weights, (T, K), "topk_weights", _F32T)
+    _dense_from(topk_ids, 0, "topk_ids")
+    _dense_from(topk_weights, 0, "topk_weights")
+    if bias is not None:
+        _shape(bias, (E,), "bias", _F32T)
+        _dense_from(bias, 0, "bias")
+    args = (_ptr(logits), _lead_stride(logits), dtype, _ptr(bias), T, E, K,
+            _choice(SCORES, score, "score"), n_group, topk_group, int(bool(renormalize)),
+            float(scale), _ptr(topk_ids), _ptr(topk_weights))
+    return PreparedCall("moe_ep_route_topk", args, (logits, topk_ids, topk_weights, bias))
+
+
+def moe_ep_route_topk(logits, topk_ids, topk_weights, score="softmax", bias=None, n_group=1,
+                      topk_group=1, renormalize=True, scale=1.0, stream=None) -> None:
+    prepare_route_topk(logits, topk_ids, topk_weights, score, bias, n_group, topk_group,
+                       renormalize, scale)(stream)
+
+
+_CODE_T = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _product(x, w, out, act, bias, out_types):
+    """Shapes that the grouped products share; returns (e_local, rows, H, N,
+    act code)."""
+    if x.dim() != 3 or w.dim() != 3 or out.dim() != 3:
+        raise ValueError("x, w and out must be [e_local, ., .]")
+    e, rows, H = x.shape
+    N = out.size(2)
+    code = _choice(ACTS, act, "act")
+    nw = 2 * N if act == "silu_gated" else N
+    _shape(w, (e, nw, H), "w")
+    _shape(out, (e, rows, N), "out", out_types)
+    for t, n in ((x, "x"), (w, "w"), (out, "out")):
+        _rows_dense(t, 1, n)
+    if bias is not None:
+        _shape(bias, (e, nw), "bias", _F32T)
+        _rows_dense(bias, 1, "bias")
+    return e, rows, H, N, code
+
+
+def prepare_expert_matmul(x: torch.Tensor, w: torch.Tensor, expert_num_tokens: torch.Tensor,
+                          out: torch.Tensor, act: str = "none",
+                          bias: Optional[torch.Tensor] = None) -> PreparedCall:
+    """x: bf16 [e_local, rows, H] (the batched rows); w: bf16
+    [e_local, N, H] ([e_local, 2N, H] for silu_gated: gate rows, then up
+    rows); out: bf16 or fp32 [e_local, rows, N]; bias: fp32, one per row of
+    w. The expert stride of each is free, everything below it dense."""
+    e, rows, H, N, code = _product(x, w, out, act, bias, (torch.bfloat16, torch.float32))
+    for t, n in ((x, "x"), (w, "w")):
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{n} must be bfloat16")
+    _shape(expert_num_tokens, (e,), "expert_num_tokens", _I32T)
+    _dense_from(expert_num_tokens, 0, "expert_num_tokens")
+    args = (_ptr(x), _lead_stride(x), _ptr(w), _lead_stride(w), _ptr(bias),
+            0 if bias is None else _lead_stride(bias), _ptr(expert_num_tokens), e, rows, H, N,
+            code, _ptr(out), _lead_stride(out), _dtype_code(out))
+    return PreparedCall("moe_ep_expert_matmul", args, (x, w, expert_num_tokens, out, bias))
+
+
+def moe_ep_expert_matmul(x, w, expert_num_tokens, out, act="none", bias=None,
+                         stream=None) -> None:
+    prepare_expert_matmul(x, w, expert_num_tokens, out, act, bias)(stream)
+
+
+def prepare_expert_matmul_fp8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor,
+                              w_scale: torch.Tensor, expert_num_tokens: torch.Tensor,
+                              out: torch.Tensor, act: str = "none",
+                              bias: Optional[torch.Tensor] = None,
+                              out_scale: Optional[torch.Tensor] = None) -> PreparedCall:
+    """x, w: e4m3 codes (uint8 or float8_e4m3fn) shaped as for
+    prepare_expert_matmul; x_scale: fp32 [e_local, rows, scale_pitch(H, 128)];
+    w_scale: fp32 [e_local, ceil(N / 128), H / 128] (twice the blocks for
+    silu_gated); out: bf16, fp32, or e4m3 codes with out_scale fp32
+    [e_local, rows, scale_pitch(N, 128)]."""
+    e, rows, H, N, code = _product(x, w, out, act, bias,
+                                   (torch.bfloat16, torch.float32) + _CODE_T)
+    for t, n in ((x, "x"), (w, "w")):
+        if t.dtype not in _CODE_T:
+            raise ValueError(f"{n} must hold e4m3 codes (uint8 or float8_e4m3fn)")
+    if H % SCALE_BLOCK:
+        raise ValueError(f"x: {H} columns, a multiple of {SCALE_BLOCK} expected")
+    blocks = -(-N // SCALE_BLOCK) * (2 if act == "silu_gated" else 1)
+    _shape(x_scale, (e, rows, scale_pitch(H, SCALE_BLOCK)), "x_scale", _F32T)
+    _shape(w_scale, (e, blocks, H // SCALE_BLOCK), "w_scale", _F32T)
+    _rows_dense(x_scale, 1, "x_scale")
+    _rows_dense(w_scale, 1, "w_scale")
+    codes = out.dtype in _CODE_T
+    if codes != (out_scale is not None):
+        raise ValueError("out_scale goes with e4m3 codes in out")
+    if codes:
+        _shape(out_scale, (e, rows, scale_pitch(N, SCALE_BLOCK)), "out_scale", _F32T)
+        _rows_dense(out_scale, 1, "out_scale")
+    _shape(expert_num_tokens, (e,), "expert_num_tokens", _I32T)
+    _dense_from(expert_num_tokens, 0, "expert_num_tokens")
+    args = (_ptr(x), _lead_stride(x), _ptr(x_scale), _lead_stride(x_scale),
+            _ptr(w), _lead_stride(w), _ptr(w_scale), _lead_stride(w_scale), _ptr(bias),
+            0 if bias is None else _lead_stride(bias), _ptr(expert_num_tokens), e, rows, H, N,
+            code, _ptr(out), _lead_stride(out), E4M3 if codes else _dtype_code(out),
+            _ptr(out_scale), _lead_stride(out_scale) if codes else 0)
+    return PreparedCall("moe_ep_expert_matmul_fp8", args,
+                        (x, x_scale, w, w_scale, expert_num_tokens, out, bias, out_scale))
+
+
+def moe_ep_expert_matmul_fp8(x, x_scale, w, w_scale, expert_num_tokens, out, act="none",
+                             bias=None, out_scale=None, stream=None) -> None:
+    prepare_expert_matmul_fp8(x, x_scale, w, w_scale, expert_num_tokens, out, act, bias,
+                              out_scale)(stream)
+
+
+def prepare_matmul(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, act: str = "none",
+                   bias: Optional[torch.Tensor] = None,
+                   residual: Optional[torch.Tensor] = None) -> PreparedCall:
+    """x: bf16 [T, H]; w: bf16 [N, H] ([2N, H] for silu_gated); out: bf16 or
+    fp32 [T, N]; bias: fp32, one per row of w; residual: like out, may be
+    out. The row stride of each is free."""
+    for t, n in ((x, "x"), (w, "w"), (out, "out")):
+        if t.dim() != 2:
+            raise ValueError(f"{n} must have two dims")
+        _rows_dense(t, 1, n)
+    for t, n in ((x, "x"), (w, "w")):
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{n} must be bfloat16")
+    T, H = x.shape
+    N = out.size(1)
+    code = _choice(ACTS, act, "act")
+    nw = 2 * N if act == "silu_gated" else N
+    _shape(w, (nw, H), "w")
+    _shape(out, (T, N), "out", (torch.bfloat16, torch.float32))
+    if bias is not None:
+        _shape(bias, (nw,), "bias", _F32T)
+        _dense_from(bias, 0, "bias")
+    if residual is not None:
+        _shape(residual, (T, N), "residual", (out.dtype,))
+        _rows_dense(residual, 1, "residual")
+    args = (_ptr(x), _lead_stride(x), _ptr(w), _lead_stride(w), _ptr(bias), T, H, N, code,
+            _ptr(residual), 0 if residual is None else _lead_stride(residual), _ptr(out),
+            _lead_stride(out), _dtype_code(out))
+    return PreparedCall("moe_ep_matmul", args, (x, w, out, bias, residual))
+
+
+def moe_ep_matmul(x, w, out, act="none", bias=None, residual=None, stream=None) -> None:
+    prepare_matmul(x, w, out, act, bias, residual)(stream)

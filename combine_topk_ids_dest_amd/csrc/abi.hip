@@ -265,7 +265,7 @@ const char* moe_ep_status_string(int status) {
         case MOE_EP_OK: return "ok";
         case MOE_EP_EINVAL: return "invalid argument";
         case MOE_EP_ECAP: return "more tokens than max_num_tokens";
-        case MOE_EP_EDTYPE: return "unsupported combine data type";
+        case MOE_EP_EDTYPE: return "unsupported data type";
         case MOE_EP_EALIGN: return "pointer, stride or row not 16-byte aligned";
         case MOE_EP_EWORKSPACE: return "workspace missing or too small";
         case MOE_EP_EHIP: return "HIP kernel launch failed";

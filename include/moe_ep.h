@@ -62,7 +62,7 @@ extern "C" {
 #define MOE_EP_OK          0
 #define MOE_EP_EINVAL     -1   /* bad pointer, size, stride or limit      */
 #define MOE_EP_ECAP       -2   /* T > max_num_tokens                       */
-#define MOE_EP_EDTYPE     -3   /* combine data type not supported          */
+#define MOE_EP_EDTYPE     -3   /* data type not supported                  */
 #define MOE_EP_EALIGN     -4   /* pointer, stride or row not 16-B aligned  */
 #define MOE_EP_EWORKSPACE -5   /* workspace missing or too small           */
 #define MOE_EP_EHIP       -6   /* a kernel launch failed                    */
@@ -72,6 +72,19 @@ extern "C" {
 /* Combine data types (expert outputs, partials and token outputs). */
 #define MOE_EP_BF16 0
 #define MOE_EP_F32  1
+/* Output of moe_ep_expert_matmul_fp8 only: OCP fp8 E4M3 codes and scales. */
+#define MOE_EP_E4M3 2
+
+/* Router scores. */
+#define MOE_EP_SOFTMAX 0
+#define MOE_EP_SIGMOID 1
+
+/* Activations of the products. */
+#define MOE_EP_ACT_NONE       0
+#define MOE_EP_ACT_SILU       1   /* v * sigmoid(v)                          */
+#define MOE_EP_ACT_GELU       2   /* v * (1 + erf(v / sqrt 2)) / 2           */
+#define MOE_EP_ACT_SILU_GATED 3   /* w holds N gate rows, then N up rows:
+                                     silu(gate) * up                         */
 
 /* err_flags bits. */
 #define MOE_EP_ERR_ID_RANGE 1u  /* topk id >= E: the entry is dropped       */
@@ -85,6 +98,8 @@ extern "C" {
 #define MOE_EP_MAX_WORLD        64
 #define MOE_EP_MAX_LOCAL_EXPERTS 1024
 #define MOE_EP_MAX_SLOTS        64
+#define MOE_EP_MAX_ROUTE_EXPERTS 1024   /* experts of moe_ep_route_topk      */
+#define MOE_EP_MAX_WIDTH (1 << 20)      /* columns of x and out of a product */
 
 /* Device scratch that moe_ep_dispatch_pack_noalloc uses, per GPU. */
 #define MOE_EP_NOALLOC_SCRATCH_BYTES (8u << 20)
@@ -498,6 +513,125 @@ MOE_EP_API int moe_ep_combine_unpack_fused(const void* back, int64_t back_rank_s
                           int64_t expert_stride, const int32_t* self_eloc,
                           const float* self_w, const int32_t* self_row,
                           int32_t e_local, int32_t K, void* out, void* stream);
+
+/*
+ * The router's choice of experts for each token: topk_ids and topk_weights as
+ * moe_ep_dispatch_pack takes them. For a token's logits x[e], e in [0, E):
+ *   score   p[e] = softmax(x)[e] (MOE_EP_SOFTMAX) or sigmoid(x[e])
+ *           (MOE_EP_SIGMOID), computed in fp64.
+ *   choice  c[e] = fp32(p[e]) + bias[e] (no bias: fp32(p[e])).
+ *   groups  with n_group > 1 the experts are n_group equal runs; a run counts
+ *           its best choice value (with a bias: the sum of its two best, or
+ *           its only one), and experts outside the topk_group best runs are
+ *           not picked.
+ *   picks   the K largest c, largest first; equal values (of experts and of
+ *           runs) go to the lower index.
+ *   weights w = p[pick], with renormalize divided by the picks' sum (0 when
+ *           the sum is 0), times scale, in fp64, rounded once.
+ * An expert whose logit is -inf or NaN, or whose choice value is -inf or NaN,
+ * is never picked and takes no part in the softmax (a -inf or NaN logit); a
+ * logit of +inf counts as the largest fp32 value. Picks that find no expert
+ * left get id -1 and weight +0.0, which the pack takes for padding: a token
+ * whose logits are all -inf is a padding token.
+ *
+ *   logits        [T, E] of dtype (MOE_EP_BF16 or MOE_EP_F32); logits_stride
+ *                 elements between tokens (>= E). Aligned to their type.
+ *   bias          fp32 [E], nullable.
+ *   K             1 <= K <= min(64, E).
+ *   n_group       1 <= n_group <= 64, E % n_group == 0; 1 <= topk_group <=
+ *                 n_group and K <= topk_group * (E / n_group).
+ *   topk_ids      int32 [T, K] out.   topk_weights  fp32 [T, K] out.
+ * Limits: E <= 1024, T * K < 2^31.
+ */
+MOE_EP_API int moe_ep_route_topk(const void* logits, int64_t logits_stride, int32_t dtype,
+                                 const float* bias, int64_t T, int32_t E, int32_t K,
+                                 int32_t score, int32_t n_group, int32_t topk_group,
+                                 int32_t renormalize, float scale, int32_t* topk_ids,
+                                 float* topk_weights, void* stream);
+
+/*
+ * The experts' product over the batched rows of moe_ep_expert_batch, one
+ * weight matrix per local expert, ragged row counts read on the device:
+ *   out[e, r, n] = act(sum_h x[e, r, h] * w[e, n, h] + bias[e, n])
+ * for r < expert_num_tokens[e]. Products and sums are fp32 (in the matrix
+ * cores, over h in an order that does not depend on the counts of other
+ * experts), the activation fp32, the result rounded once. Rows from the count
+ * on are not written, and what x holds there has no effect.
+ *
+ *   x             bf16 [e_local, rows, H], expert e at x + e * x_stride
+ *                 (elements, >= rows * H); rows dense. For the batched rows
+ *                 rows = expert_cap.
+ *   w             bf16 [e_local, Nw, H], expert e at w + e * w_stride
+ *                 (>= Nw * H); Nw = N, or 2 N for MOE_EP_ACT_SILU_GATED.
+ *   bias          fp32 [e_local, Nw], nullable; bias_stride elements between
+ *                 experts (>= Nw).
+ *   expert_num_tokens  int32 [e_local]; a count outside [0, rows] is clamped.
+ *   out           bf16 or fp32 (out_dtype) [e_local, rows, N], expert e at
+ *                 out + e * out_stride (>= rows * N). Must not overlap x or w.
+ * Rows of x, w and out, their strides, bias and its stride are multiples of
+ * 16 bytes (EALIGN). Limits: H, N <= MOE_EP_MAX_WIDTH, Nw * H * 2 < 2^31
+ * bytes, e_local <= 1024, rows <= INT_MAX and e_local * ceil(rows / 16) *
+ * ceil(N / 8) < 2^31.
+ */
+MOE_EP_API int moe_ep_expert_matmul(const void* x, int64_t x_stride, const void* w,
+                                    int64_t w_stride, const float* bias, int64_t bias_stride,
+                                    const int32_t* expert_num_tokens, int32_t e_local,
+                                    int64_t rows, int64_t H, int64_t N, int32_t act, void* out,
+                                    int64_t out_stride, int32_t out_dtype, void* stream);
+
+/*
+ * moe_ep_expert_matmul on OCP fp8 E4M3 codes: rows as moe_ep_dispatch_pack_fp8
+ * (group 128) sends and moe_ep_expert_batch batches them, weights with one
+ * scale per 128 x 128 block. With S the sum of the products of 128 columns'
+ * codes, sums add (x_scale * w_scale) * S in ascending column order.
+ *
+ *   x             codes [e_local, rows, H] (one byte; x_stride bytes between
+ *                 experts), H % 128 == 0.
+ *   x_scale       fp32 [e_local, rows, Hp], Hp = H / 128 rounded up to 4;
+ *                 x_scale_stride elements between experts (>= rows * Hp).
+ *   w             codes [e_local, Nw, H] (w_stride bytes between experts).
+ *   w_scale       fp32 [e_local, Bn, H / 128] with Bn = ceil(N / 128), or
+ *                 2 * ceil(N / 128) for MOE_EP_ACT_SILU_GATED (the gate rows'
+ *                 blocks, then the up rows'); w_scale_stride elements between
+ *                 experts (>= Bn * H / 128).
+ *   out           bf16, fp32, or with MOE_EP_E4M3 codes (N % 128 == 0;
+ *                 out_stride bytes) quantised as moe_ep_dispatch_pack_fp8
+ *                 quantises 128 columns, from the fp32 results, with
+ *   out_scale     fp32 [e_local, rows, Np], Np = N / 128 rounded up to 4, its
+ *                 padding written +0.0; out_scale_stride elements between
+ *                 experts (>= rows * Np). NULL for the other types.
+ * Everything else as moe_ep_expert_matmul. EDTYPE for another out_dtype.
+ */
+MOE_EP_API int moe_ep_expert_matmul_fp8(const void* x, int64_t x_stride, const float* x_scale,
+                                        int64_t x_scale_stride, const void* w, int64_t w_stride,
+                                        const float* w_scale, int64_t w_scale_stride,
+                                        const float* bias, int64_t bias_stride,
+                                        const int32_t* expert_num_tokens, int32_t e_local,
+                                        int64_t rows, int64_t H, int64_t N, int32_t act,
+                                        void* out, int64_t out_stride, int32_t out_dtype,
+                                        float* out_scale, int64_t out_scale_stride,
+                                        void* stream);
+
+/*
+ * The product over all tokens of a rank: the router's logits, or an expert
+ * that every token passes through, added to the combine's output.
+ *   out[t, n] = act(sum_h x[t, h] * w[n, h] + bias[n]) + residual[t, n]
+ * with fp32 sums, one rounding at the end.
+ *
+ *   x             bf16 [T, H], x_stride elements between tokens (>= H).
+ *   w             bf16 [Nw, H], w_stride elements between rows (>= H).
+ *   bias          fp32 [Nw], nullable.
+ *   residual      [T, N] of out_dtype, nullable; residual_stride elements
+ *                 between tokens (>= N). May be out itself (same stride).
+ *   out           bf16 or fp32 [T, N], out_stride elements between tokens.
+ * Rows, strides and pointers are multiples of 16 bytes (EALIGN). Strides of
+ * x are below 2^23 bytes; limits as for moe_ep_expert_matmul (Nw * w_stride
+ * * 2 < 2^31 bytes).
+ */
+MOE_EP_API int moe_ep_matmul(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                             const float* bias, int64_t T, int64_t H, int64_t N, int32_t act,
+                             const void* residual, int64_t residual_stride, void* out,
+                             int64_t out_stride, int32_t out_dtype, void* stream);
 
 #ifdef __cplusplus
 }
