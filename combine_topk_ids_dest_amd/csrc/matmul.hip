@@ -31,6 +31,9 @@ struct Frag {
     u32x4 v[2];
 };
 
+// A value that every lane of the wave has, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 template <int EB>
 __device__ __forceinline__ f32x4 mma(const Frag& w, const Frag& x, f32x4 acc) {
     if constexpr (EB == 2) {
@@ -299,46 +302,264 @@ __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, i
     __syncthreads();   // the next tile writes lds again
 }
 
-// Tiles in front of each group, and in all (LDS, pre[groups]).
+// ---------------------------------------------------------------------
+// Big tiles: 256 rows of x by 256 rows of w. Eight waves in two rows of four,
+// each with 128 x 64 of the sums in registers. Slabs of 128 bytes of k go
+// from memory straight into LDS (no register is spent on a load in flight),
+// one slab ahead of the one being multiplied; fragments are read from LDS
+// half a slab ahead, so that the reads of one half run under the products
+// of the other.
+//
+// LDS: row r of a slab holds its eight 16-byte chunks with chunk c at place
+// c ^ ((r >> 1) & 7), so the 16 rows of a fragment's read fall on different
+// banks. The load that fills LDS writes a wave's 64 x 16 bytes in lane order,
+// so the permutation is applied to the addresses that the lanes read.
+// ---------------------------------------------------------------------
+constexpr int kBig = 256;
+constexpr int kBigSlab = kBig * kSlab;           // bytes of one operand's slab
+constexpr int kBigLds = 4 * kBigSlab;            // two slabs of both operands
+
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// The buffer resource of row_rsrc as four scalar registers.
+__device__ __forceinline__ i32x4 row_rsrc4(const uint8_t* p, int64_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    i32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)at);
+    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32) & 0xFFFF);
+    r[2] = __builtin_amdgcn_readfirstlane((int)(bytes < INT32_MAX ? bytes : INT32_MAX));
+    r[3] = 0x00020000;
+    return r;
+}
+
+// 16 bytes per lane from memory into LDS, lane l's at dst + 16 l (dst is
+// uniform, in M0). Written out so that the compiler does not count it among
+// the loads that an LDS read has to wait for: with its own form of this
+// instruction it waits for every load in flight before the next LDS read,
+// whatever that reads. The instruction has no output register; what it
+// writes is ordered by the waits and barriers below.
+__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t dst, uint32_t off, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(dst), "v"(off), "s"(r), "s"(soff)
+                 : "m0");
+}
+
+// Waits for this wave's loads into LDS and its LDS reads, then for the block.
+__device__ __forceinline__ void wait_all_and_barrier() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <bool GATED>
+__device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
+                                         uint8_t* lds) {
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    const int wm = wave >> 2, wn = wave & 3;
+    const int kb = a.row_bytes;
+    const int nslab = (kb + kSlab - 1) / kSlab;
+    const int left = rows - m0;
+    const int nw = GATED ? 2 * a.N : a.N;
+    const i32x4 rx = row_rsrc4(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
+                               (int64_t)(left - 1) * a.x_row + kb);
+    const i32x4 rw = row_rsrc4(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
+        (int)(uint32_t)(uintptr_t)(lds_byte*)lds + wave * 1024);
+
+    // a wave's instruction i fills rows (i * 8 + wave) * 8 .. + 7
+    const int sub = lane >> 3;
+    const int chunk = (lane & 7) ^ ((((wave & 1) << 3 | sub) >> 1) & 7);
+    uint32_t vx[4], vw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (i * 8 + wave) * 8 + sub;
+        vx[i] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk * 16 : kOutside;
+        int n;
+        const int q = wrow<GATED>(r, n0, a.N, n);
+        vw[i] = n < a.N ? (uint32_t)q * (uint32_t)a.w_row + chunk * 16 : kOutside;
+    }
+    // the last slab may be short: its chunks past the end of k load zeros
+    const int last = (kb - chunk * 16 + kSlab - 1) / kSlab;
+    auto fetch = [&](int s) {
+        const uint32_t none = s < last ? 0u : kOutside;
+        const uint32_t d = lds0 + (s & 1) * 2 * kBigSlab;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_to_lds(rx, d + i * 8192, vx[i] | none, s * kSlab);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            load_to_lds(rw, d + kBigSlab + i * 8192, vw[i] | none, s * kSlab);
+    };
+
+    const int rd = (lane & 15) * kSlab + ((((lane >> 4) * 2) ^ ((lane >> 1) & 7)) * 16);
+    const uint8_t* rdx = lds + wm * 128 * kSlab;
+    const uint8_t* rdw = lds + kBigSlab + wn * 64 * kSlab;
+    u32x4 fx[2][8], fw[2][4];
+    auto read = [&](int s, int h, u32x4 (&x)[8], u32x4 (&w)[4]) {
+        const int o = (s & 1) * 2 * kBigSlab + (rd ^ (h * 16));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = *reinterpret_cast<const u32x4*>(rdw + o + i * 16 * kSlab);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = *reinterpret_cast<const u32x4*>(rdx + o + j * 16 * kSlab);
+    };
+    f32x4 acc[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const u32x4 (&x)[8], const u32x4 (&w)[4]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, w[i]), __builtin_bit_cast(bf16x8, x[j]), acc[i][j],
+                    0, 0, 0);
+    };
+
+    fetch(0);
+    fetch(1);       // a slab past the last loads zeros
+    asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
+    read(0, 0, fx[0], fw[0]);
+    // the reads of the half after, one to every two or three products
+    auto spread = [&]() {
+#pragma unroll
+        for (int i = 0; i < 12; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // MFMA
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+    };
+    for (int s = 0; s < nslab; ++s) {
+        read(s, 1, fx[1], fw[1]);
+        multiply(fx[0], fw[0]);
+        spread();
+        // slab s is read; slab s + 1 has arrived
+        wait_all_and_barrier();
+        fetch(s + 2);
+        read(s + 1, 0, fx[0], fw[0]);
+        multiply(fx[1], fw[1]);
+        spread();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_all_and_barrier();   // LDS is free for the next tile
+
+#pragma unroll
+    for (int i = 0; i < 4; i += GATED ? 2 : 1) {
+        const int r = wn * 64 + i * 16 + (lane >> 4) * 4;
+        int n;
+        wrow<GATED>(r, n0, a.N, n);
+        if (n >= a.N) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int m = wm * 128 + j * 16 + (lane & 15);
+            if (m >= left) continue;
+            const f32x4 y = finish<GATED>(a, g, n, acc[i][j], acc[GATED ? i + 1 : i][j]);
+            store_out(a, g, m0 + m, n, y);
+        }
+    }
+}
+
+// The work list: big tiles of every group, then small ones. A group's rows
+// are cut into runs of 256; what is left is a big tile too where it has more
+// than `big_from` rows, else small tiles.
+struct Plan {
+    int32_t big[MOE_EP_MAX_LOCAL_EXPERTS + 1];      // tiles in front of a group
+    int32_t small[MOE_EP_MAX_LOCAL_EXPERTS + 1];
+};
+
+__device__ __forceinline__ int big_runs(int rows, int big_from) {
+    return rows / kBig + (rows % kBig > big_from ? 1 : 0);
+}
+
 template <int BM>
-__device__ __forceinline__ void plan(const MatmulArgs& a, int nt, int32_t* pre) {
+__device__ __forceinline__ void make_plan(const MatmulArgs& a, int big_from, int nt_big,
+                                          int nt_small, Plan* p) {
     if (threadIdx.x < 64) {
-        int32_t run = 0;
+        int32_t run_b = 0, run_s = 0;
         for (int g0 = 0; g0 < a.groups; g0 += 64) {
             const int g = g0 + (int)threadIdx.x;
-            const int32_t t = g < a.groups ? (group_rows(a, g) + BM - 1) / BM * nt : 0;
-            const int32_t inc = wave_inclusive_scan(t);
-            if (g < a.groups) pre[g] = run + inc - t;
-            run += __shfl(inc, 63, 64);
+            const int rows = g < a.groups ? group_rows(a, g) : 0;
+            const int b = big_from < kBig ? big_runs(rows, big_from) : 0;
+            const int rest = rows - b * kBig;
+            const int32_t tb = b * nt_big;
+            const int32_t ts = rest > 0 ? (rest + BM - 1) / BM * nt_small : 0;
+            const int32_t ib = wave_inclusive_scan(tb), is = wave_inclusive_scan(ts);
+            if (g < a.groups) {
+                p->big[g] = run_b + ib - tb;
+                p->small[g] = run_s + is - ts;
+            }
+            run_b += __shfl(ib, 63, 64);
+            run_s += __shfl(is, 63, 64);
         }
-        if (threadIdx.x == 0) pre[a.groups] = run;
+        if (threadIdx.x == 0) {
+            p->big[a.groups] = run_b;
+            p->small[a.groups] = run_s;
+        }
     }
     __syncthreads();
 }
 
-template <int EB, bool GATED, int BM, int BN, int DEPTH>
-__global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a) {
-    __shared__ float lds[kWaves * BM * (BN + 4)];
-    __shared__ int32_t pre[MOE_EP_MAX_LOCAL_EXPERTS + 1];
+// Tile of block b in a round of `left` tiles over the grid, -1 for none.
+// Blocks go to the eight XCDs in turn, so each XCD (with an L2 of its own)
+// gets a run of neighbouring tiles, which share rows of x and w.
+__device__ __forceinline__ int tile_of(int b, int grid, int left) {
+    const int r = left < grid ? left : grid;
+    const int per = (r + 7) / 8;
+    const int slot = b >> 3;
+    const int t = (b & 7) * per + slot;
+    return slot < per && t < r ? t : -1;
+}
+
+template <int EB, bool GATED, int BM, int BN, int DEPTH, bool BIG>
+__global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a, int big_from) {
+    constexpr int kSmallLds = kWaves * BM * (BN + 4) * 4;
+    __shared__ __align__(1024) uint8_t lds[BIG && kBigLds > kSmallLds ? kBigLds : kSmallLds];
+    __shared__ Plan p;
     constexpr int BO = GATED ? BN / 2 : BN;
-    const int nt = (a.N + BO - 1) / BO;
-    plan<BM>(a, nt, pre);
-    const int total = pre[a.groups];
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        const int g = find_source(pre, a.groups, t);
-        const int rows = group_rows(a, g);
-        const int mt = (rows + BM - 1) / BM;
-        const int l = t - pre[g];
-        small_tile<EB, GATED, BM, BN, DEPTH>(a, g, l % mt * BM, rows, l / mt * BO, lds);
+    constexpr int BB = GATED ? kBig / 2 : kBig;
+    const int nt = (a.N + BO - 1) / BO, ntb = (a.N + BB - 1) / BB;
+    make_plan<BM>(a, BIG ? big_from : kBig, ntb, nt, &p);
+    const int nbig = BIG ? uniform(p.big[a.groups]) : 0;
+    const int total = nbig + uniform(p.small[a.groups]);
+    for (int t0 = 0; t0 < total; t0 += gridDim.x) {
+        const int at = tile_of(blockIdx.x, gridDim.x, total - t0);
+        if (at < 0) break;      // a last, partial round
+        const int t = t0 + at;
+        if constexpr (BIG) {
+            if (t < nbig) {
+                const int g = uniform(find_source(p.big, a.groups, t));
+                const int rows = uniform(group_rows(a, g));
+                const int mt = big_runs(rows, big_from);
+                // eight runs of rows at a time, over all columns
+                const int l = t - uniform(p.big[g]);
+                const int m8 = l / (8 * ntb) * 8;
+                const int wide = mt - m8 < 8 ? mt - m8 : 8;
+                const int in = l - m8 * ntb;
+                big_tile<GATED>(a, g, (m8 + in % wide) * kBig, rows, in / wide * BB, lds);
+                continue;
+            }
+        }
+        const int l0 = t - nbig;
+        const int g = uniform(find_source(p.small, a.groups, l0));
+        const int rows = uniform(group_rows(a, g));
+        const int from = BIG ? big_runs(rows, big_from) * kBig : 0;
+        const int mt = (rows - from + BM - 1) / BM;
+        const int l = l0 - uniform(p.small[g]);
+        small_tile<EB, GATED, BM, BN, DEPTH>(a, g, from + l % mt * BM, rows, l / mt * BO,
+                                             reinterpret_cast<float*>(lds));
     }
 }
 
-template <int EB, bool GATED, int BM, int BN, int DEPTH>
+template <int EB, bool GATED, int BM, int BN, int DEPTH, bool BIG = false>
 hipError_t launch(const MatmulArgs& a, hipStream_t st) {
     constexpr int BO = GATED ? BN / 2 : BN;
     const int64_t most = (int64_t)a.groups * ((a.rows + BM - 1) / BM) * ((a.N + BO - 1) / BO);
-    const unsigned grid = (unsigned)(most < 1024 ? most : 1024);
-    matmul_kernel<EB, GATED, BM, BN, DEPTH><<<grid, kThreads, 0, st>>>(a);
+    const int64_t grid = most < 256 ? (most + 7) / 8 * 8 : 256;
+    matmul_kernel<EB, GATED, BM, BN, DEPTH, BIG>
+        <<<(unsigned)grid, kThreads, 0, st>>>(a, BIG ? 128 : kBig);
     return hipGetLastError();
 }
 
@@ -351,6 +572,9 @@ hipError_t launch_matmul(const MatmulArgs& a, hipStream_t st) {
             return gated ? launch<1, true, 16, 256, 1>(a, st) : launch<1, false, 16, 128, 2>(a, st);
         return gated ? launch<1, true, 64, 64, 1>(a, st) : launch<1, false, 64, 64, 1>(a, st);
     }
+    if (a.rows > 128)
+        return gated ? launch<2, true, 64, 64, 1, true>(a, st)
+                     : launch<2, false, 64, 64, 1, true>(a, st);
     return gated ? launch<2, true, 64, 64, 1>(a, st) : launch<2, false, 64, 64, 1>(a, st);
 }
 
