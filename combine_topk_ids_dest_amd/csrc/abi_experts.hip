@@ -192,11 +192,12 @@ int moe_ep_matmul(const void* x, int64_t x_stride, const void* w, int64_t w_stri
     if (rc) return rc;
     const int ob = out_bytes(out_dtype, false);
     if (ob == 0) return MOE_EP_EDTYPE;
-    if (x_stride < H || x_stride >= (1 << 22) || w_stride < H || out_stride < N ||
-        out_stride > INT64_MAX / ob / (T > 0 ? T : 1))
+    // a tile's rows are addressed by 32-bit offsets
+    const int64_t most = 1 << 23;
+    if (x_stride < H || x_stride >= most / 2 || w_stride < H || out_stride < N ||
+        out_stride >= most / ob)
         return MOE_EP_EINVAL;
-    if (residual && (residual_stride < N || residual_stride > INT64_MAX / ob / (T > 0 ? T : 1)))
-        return MOE_EP_EINVAL;
+    if (residual && (residual_stride < N || residual_stride >= most / ob)) return MOE_EP_EINVAL;
     if (residual == out && residual && residual_stride != out_stride) return MOE_EP_EINVAL;
     if (T > 0 && (!x || !w || !out)) return MOE_EP_EINVAL;
     if (H * 2 % 16 || N * ob % 16 || x_stride * 2 % 16 || w_stride * 2 % 16 ||

@@ -5,62 +5,77 @@
 // so both operands of an MFMA load the same way: a lane of a 16-row fragment
 // takes 32 consecutive bytes of row lane % 16 from every 128-byte slab of k
 // (any assignment of k to lanes gives the same sum as long as both operands
-// share it). w is the A operand: a lane's four accumulators are four
-// consecutive output columns of one row, so the epilogue works on vectors.
+// share it). w is the A operand: a lane's accumulators are consecutive output
+// columns of one row of x, so the epilogue works on vectors.
 //
-// silu_gated: w holds N gate rows, then N up rows. Fragments alternate between
-// the two, so gate and up of an output meet in one tile (wrow()).
+// silu_gated: w holds N gate rows, then N up rows; a tile takes both rows of
+// each of its output columns.
 //
 // fp8: a slab of 128 codes is one scale block: acc += (sx * sw) * slab sum.
+// The fp8 matrix instruction drops product bits below 2^-13 of the largest
+// product it adds (measured: 1.4e-5 of the result over 7168 columns, against
+// 4e-7 in bf16). That vanishes under the rounding of a bf16 result (2^-8), so
+// bf16 outputs use it; for fp32 and e4m3 outputs, whose scales are fp32, the
+// codes are widened to bf16 (exactly) and multiplied there (`WIDE`).
 #include "experts.h"
 
 namespace moe_ep {
 namespace {
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kSlab = 128;                       // bytes of k per step
 constexpr uint32_t kOutside = 0x80000000u;       // past every buffer's range
 
+// A value that every lane of the wave has, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // 32 bytes of k of one row: a lane's share of a fragment.
 struct Frag {
     u32x4 v[2];
 };
 
-// A value that every lane of the wave has, in a scalar register.
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
-template <int EB>
-__device__ __forceinline__ f32x4 mma(const Frag& w, const Frag& x, f32x4 acc) {
-    if constexpr (EB == 2) {
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v[0]),
-                                                      __builtin_bit_cast(bf16x8, x.v[0]), acc,
-                                                      0, 0, 0);
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w.v[1]),
-                                                       __builtin_bit_cast(bf16x8, x.v[1]), acc,
-                                                       0, 0, 0);
-    } else {
-        // e4m3 x e4m3 with the blocks' exponents at 1.0 (127)
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            __builtin_bit_cast(i32x8, w), __builtin_bit_cast(i32x8, x), acc, 0, 0, 0,
-            0x7F7F7F7F, 0, 0x7F7F7F7F);
-    }
+__device__ __forceinline__ f32x4 mma_bf16(const u32x4& w, const u32x4& x, f32x4 acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
+                                                   __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
 }
 
-// Row of w behind row r of a tile whose first output column is n0; its
-// output column in n (columns n >= N do not exist).
-template <bool GATED>
-__device__ __forceinline__ int wrow(int r, int n0, int N, int& n) {
-    if (!GATED) {
-        n = n0 + r;
-        return n;
+// e4m3 x e4m3 with the blocks' exponents at 1.0 (127)
+__device__ __forceinline__ f32x4 mma_fp8(const Frag& w, const Frag& x, f32x4 acc) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        __builtin_bit_cast(i32x8, w), __builtin_bit_cast(i32x8, x), acc, 0, 0, 0, 0x7F7F7F7F, 0,
+        0x7F7F7F7F);
+}
+
+// 32 e4m3 codes as bf16, in code order.
+struct Wide {
+    u32x4 v[4];
+};
+
+__device__ __forceinline__ Wide widen(const Frag& f) {
+    Wide r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t c = f.v[i >> 2][i & 3];
+        r.v[i >> 1][(i & 1) * 2] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+        r.v[i >> 1][(i & 1) * 2 + 1] = __builtin_bit_cast(
+            uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
     }
-    n = n0 + (r >> 5) * 16 + (r & 15);
-    return (r & 16) ? N + n : n;
+    return r;
+}
+
+__device__ __forceinline__ f32x4 mma_wide(const Wide& w, const Wide& x, f32x4 acc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc = mma_bf16(w.v[i], x.v[i], acc);
+    return acc;
 }
 
 __device__ __forceinline__ float apply_act(float v, int act) {
@@ -73,42 +88,11 @@ __device__ __forceinline__ float silu_gated(float gate, float up) {
     return gate / (1.0f + expf(-gate)) * up;
 }
 
-// Four output columns n..n+3 of row m, from their sums.
-template <bool GATED>
-__device__ __forceinline__ f32x4 finish(const MatmulArgs& a, int g, int n, f32x4 v, f32x4 up) {
-    if (a.bias) {
-        const float* b = a.bias + (int64_t)g * a.bias_stride + n;
-        v += *reinterpret_cast<const f32x4*>(b);
-        if (GATED) up += *reinterpret_cast<const f32x4*>(b + a.N);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = GATED ? silu_gated(v[i], up[i]) : apply_act(v[i], a.act);
-    return v;
-}
-
 __device__ __forceinline__ u32x2 pack_bf16(f32x4 v) {
     u32x2 o;
     o[0] = to_bf16_rne(v[0]) | (to_bf16_rne(v[1]) << 16);
     o[1] = to_bf16_rne(v[2]) | (to_bf16_rne(v[3]) << 16);
     return o;
-}
-
-__device__ __forceinline__ void store_out(const MatmulArgs& a, int g, int64_t m, int n, f32x4 v) {
-    const int64_t col = (int64_t)n * (a.out_dtype == MOE_EP_F32 ? 4 : 2);
-    uint8_t* o = a.out + g * a.out_stride + m * a.out_row + col;
-    if (a.out_dtype == MOE_EP_F32) {
-        if (a.res) v += *reinterpret_cast<const f32x4*>(a.res + m * a.res_row + col);
-        *reinterpret_cast<f32x4*>(o) = v;
-    } else {
-        if (a.res) {
-            const u32x2 r = *reinterpret_cast<const u32x2*>(a.res + m * a.res_row + col);
-            v[0] += bf16_lo(r[0]);
-            v[1] += bf16_hi(r[0]);
-            v[2] += bf16_lo(r[1]);
-            v[3] += bf16_hi(r[1]);
-        }
-        *reinterpret_cast<u32x2*>(o) = pack_bf16(v);
-    }
 }
 
 // max(m, |x|) where a NaN x leaves m as it is
@@ -123,7 +107,7 @@ __device__ __forceinline__ uint32_t codes4(f32x4 v, float s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = v[i] / s;
     const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-    uint32_t c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+    const uint32_t c = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
     uint32_t sign = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) sign |= (__float_as_uint(v[i]) >> 31) << (8 * i + 7);
@@ -137,205 +121,168 @@ __device__ __forceinline__ int group_rows(const MatmulArgs& a, int g) {
 }
 
 // ---------------------------------------------------------------------
-// Small tiles: BM rows of x by BN rows of w, the slabs of k dealt to the
-// block's waves in turn (so that a tile alone already keeps eight waves'
-// loads in flight and the block reads 1 KB runs of each row), fragments
-// loaded straight into registers, the waves' sums added in wave order.
+// Small tiles, for a few rows: 16 rows of x by 16 rows of w (gated: 8 gate
+// rows and their 8 up rows). Bound by the weights' bytes, so what counts is
+// loads in flight: the slabs of k are dealt to the block's eight waves in
+// turn (the block reads 1 KB runs of each row), each keeps four slabs of both
+// operands on their way to registers, and the waves' sums are added in wave
+// order through LDS.
 // ---------------------------------------------------------------------
-template <int EB, bool GATED, int BM, int BN, int DEPTH>
-__device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, int rows,
-                                           int n0, float* lds) {
-    constexpr int FM = BM / 16, FN = BN / 16;
-    constexpr int PITCH = BN + 4;
+constexpr int kSmall = 16;
+constexpr int kSmallPitch = kSmall + 4;
+constexpr int kSmallLds = kWaves * kSmall * kSmallPitch * 4;
+constexpr int kSmallDepth = 4;
+
+template <int EB, bool WIDE, bool GATED>
+__device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
+                                           float* lds) {
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
     const int kb = a.row_bytes;
     const int nslab = (kb + kSlab - 1) / kSlab;
     const int left = rows - m0;
-
     const int nw = GATED ? 2 * a.N : a.N;
-    const uint8_t* xb = a.x + g * a.x_stride + (int64_t)m0 * a.x_row;
-    const uint8_t* wb = a.w + g * a.w_stride;
-    const auto rx = row_rsrc(xb, (int64_t)(left - 1) * a.x_row + kb);
-    const auto rw = row_rsrc(wb, (int64_t)(nw - 1) * a.w_row + kb);
+    const auto rx = row_rsrc(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
+                             (int64_t)(left - 1) * a.x_row + kb);
+    const auto rw = row_rsrc(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
+    const int r = lane & 15;
     const uint32_t kin = (uint32_t)(lane >> 4) * 32u;
-    uint32_t vx[FM], vw[FN];
-#pragma unroll
-    for (int f = 0; f < FM; ++f) {
-        const int m = f * 16 + (lane & 15);
-        vx[f] = m < left ? (uint32_t)m * (uint32_t)a.x_row : kOutside;
-    }
-#pragma unroll
-    for (int f = 0; f < FN; ++f) {
-        int n;
-        const int r = wrow<GATED>(f * 16 + (lane & 15), n0, a.N, n);
-        vw[f] = n < a.N ? (uint32_t)r * (uint32_t)a.w_row : kOutside;
-    }
+    const uint32_t vx = r < left ? (uint32_t)r * (uint32_t)a.x_row : kOutside;
+    const int wn = GATED ? n0 + (r & 7) : n0 + r;
+    const uint32_t vw =
+        wn < a.N ? (uint32_t)(GATED && r >= 8 ? a.N + wn : wn) * (uint32_t)a.w_row : kOutside;
 
-    const float* xs[FM];
-    const float* ws[FN];
+    const float* xs = nullptr;
+    const float* ws = nullptr;
     if constexpr (EB == 1) {
-#pragma unroll
-        for (int f = 0; f < FM; ++f) {
-            int m = f * 16 + (lane & 15);
-            m = m < left ? m : left - 1;
-            xs[f] = a.xs + g * a.xs_stride + (int64_t)(m0 + m) * a.xs_pitch;
-        }
+        xs = a.xs + g * a.xs_stride + (int64_t)(m0 + (r < left ? r : left - 1)) * a.xs_pitch;
+        // the rows of w behind a lane's sums (4 * (lane / 16) on) share a block
         const int per = (a.N + kScaleBlock - 1) / kScaleBlock;
-#pragma unroll
-        for (int f = 0; f < FN; ++f) {
-            int n = GATED ? n0 + (f >> 1) * 16 : n0 + f * 16;
-            n = n < a.N ? n : a.N - 1;
-            const int blk = n / kScaleBlock + (GATED && (f & 1) ? per : 0);
-            ws[f] = a.ws + g * a.ws_stride + (int64_t)blk * nslab;
-        }
+        const int blk = n0 / kScaleBlock + (GATED && lane >= 32 ? per : 0);
+        ws = a.ws + g * a.ws_stride + (int64_t)blk * nslab;
     }
 
-    f32x4 acc[FN][FM];
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    Frag fx[DEPTH][FM], fw[DEPTH][FN];
-    float sx[DEPTH][FM], sw[DEPTH][FN];
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    Frag fx[kSmallDepth], fw[kSmallDepth];
+    float sc[kSmallDepth];
     // A slab past the last loads nothing but zeros (the buffers' range check).
     auto load = [&](int d, int s) {
         const uint32_t k0 = (uint32_t)s * kSlab + kin;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t k = k0 + 16 * h;
-            const uint32_t add = k < (uint32_t)kb ? k : kOutside;
-#pragma unroll
-            for (int f = 0; f < FN; ++f)
-                fw[d][f].v[h] = ld_row_buf<false>(rw, (vw[f] | (add & kOutside)) + (add & ~kOutside));
-#pragma unroll
-            for (int f = 0; f < FM; ++f)
-                fx[d][f].v[h] = ld_row_buf<false>(rx, (vx[f] | (add & kOutside)) + (add & ~kOutside));
+            const bool in = k < (uint32_t)kb;
+            fw[d].v[h] = ld_row_buf<false>(rw, in ? vw + k : kOutside);
+            fx[d].v[h] = ld_row_buf<false>(rx, in ? vx + k : kOutside);
         }
         if constexpr (EB == 1) {
-            const int sc = s < nslab ? s : nslab - 1;
-#pragma unroll
-            for (int f = 0; f < FM; ++f) sx[d][f] = xs[f][sc];
-#pragma unroll
-            for (int f = 0; f < FN; ++f) sw[d][f] = ws[f][sc];
+            const int c = s < nslab ? s : nslab - 1;
+            sc[d] = xs[c] * ws[c];
         }
     };
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(d, wave + d * kWaves);
-    for (int s = wave; s < nslab; s += kWaves * DEPTH) {
+    for (int d = 0; d < kSmallDepth; ++d) load(d, wave + d * kWaves);
+    for (int s = wave; s < nslab; s += kWaves * kSmallDepth) {
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
+        for (int d = 0; d < kSmallDepth; ++d) {
+            if constexpr (EB == 2) {
+                acc = mma_bf16(fw[d].v[0], fx[d].v[0], acc);
+                acc = mma_bf16(fw[d].v[1], fx[d].v[1], acc);
+            } else {
+                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                const f32x4 t = WIDE ? mma_wide(widen(fw[d]), widen(fx[d]), zero)
+                                     : mma_fp8(fw[d], fx[d], zero);
 #pragma unroll
-            for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int j = 0; j < FM; ++j) {
-                    if constexpr (EB == 2) {
-                        acc[i][j] = mma<EB>(fw[d][i], fx[d][j], acc[i][j]);
-                    } else {
-                        const f32x4 t = mma<EB>(fw[d][i], fx[d][j], f32x4{0.f, 0.f, 0.f, 0.f});
-                        const float sc = sw[d][i] * sx[d][j];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            acc[i][j][q] = __builtin_fmaf(t[q], sc, acc[i][j][q]);
-                    }
-                }
-            load(d, s + (d + DEPTH) * kWaves);
+                for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(t[q], sc[d], acc[q]);
+            }
+            load(d, s + (d + kSmallDepth) * kWaves);
         }
     }
 
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j)
-            *reinterpret_cast<f32x4*>(lds + ((wave * BM + j * 16 + (lane & 15)) * PITCH + i * 16 +
-                                             (lane >> 4) * 4)) = acc[i][j];
+    *reinterpret_cast<f32x4*>(lds + ((wave * kSmall + r) * kSmallPitch + (lane >> 4) * 4)) = acc;
     __syncthreads();
-    auto sum = [&](int m, int r) {
-        f32x4 v = *reinterpret_cast<const f32x4*>(lds + (m * PITCH + r));
+    constexpr int BO = GATED ? kSmall / 2 : kSmall;
+    const int o = threadIdx.x % BO, m = threadIdx.x / BO;
+    const int n = n0 + o;
+    if (m < kSmall && m < left && n < a.N) {
+        float v = 0.f, up = 0.f;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w)
-            v += *reinterpret_cast<const f32x4*>(lds + ((w * BM + m) * PITCH + r));
-        return v;
-    };
-    constexpr int BO = GATED ? BN / 2 : BN;       // output columns
-    constexpr int QUADS = BO / 4;
-    const bool quant = EB == 1 && a.out_dtype == MOE_EP_E4M3;
-    for (int q = threadIdx.x; q < BM * QUADS; q += kThreads) {
-        const int m = q / QUADS;
-        const int o = q % QUADS * 4;
-        const int r = GATED ? (o >> 4) * 32 + (o & 15) : o;
-        const f32x4 v = sum(m, r);
-        const f32x4 up = GATED ? sum(m, r + 16) : v;
-        const int n = n0 + o;
-        const bool in = m < left && n < a.N;
-        f32x4 y = {0.f, 0.f, 0.f, 0.f};
-        if (in) y = finish<GATED>(a, g, n, v, up);
-        if constexpr (BO == kScaleBlock) {
-            if (quant) {
-                // 32 consecutive lanes hold the 128 columns of a row's group
-                float mx = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx = abs_max(mx, y[i]);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) mx = abs_max(mx, __shfl_xor(mx, off, 32));
-                const float s = mx > 0.f ? mx / 448.0f : 1.0f;
-                if (in) {
-                    *reinterpret_cast<uint32_t*>(a.out + g * a.out_stride +
-                                                 (int64_t)(m0 + m) * a.out_row + n) = codes4(y, s);
-                    if (o == 0)
-                        a.os[g * a.os_stride + (int64_t)(m0 + m) * a.os_pitch + n / kScaleBlock] = s;
-                }
-                continue;
-            }
+        for (int w = 0; w < kWaves; ++w) {
+            v += lds[(w * kSmall + m) * kSmallPitch + o];
+            if (GATED) up += lds[(w * kSmall + m) * kSmallPitch + o + 8];
         }
-        if (in && !quant) store_out(a, g, m0 + m, n, y);
-    }
-    // the scale row's padding, by the blocks of its last group
-    if (quant && BO == kScaleBlock && n0 + BO >= a.N) {
-        const int groups = a.N / kScaleBlock;
-        const int pad = (int)a.os_pitch - groups;
-        for (int q = threadIdx.x; q < BM * pad; q += kThreads)
-            if (q / pad < left)
-                a.os[g * a.os_stride + (int64_t)(m0 + q / pad) * a.os_pitch + groups + q % pad] = 0.f;
+        if (a.bias) {
+            const float* b = a.bias + g * a.bias_stride + n;
+            v += b[0];
+            if (GATED) up += b[a.N];
+        }
+        v = GATED ? silu_gated(v, up) : apply_act(v, a.act);
+        const bool f32 = EB == 1 ? WIDE : a.out_dtype == MOE_EP_F32;
+        const int64_t row = m0 + m;
+        if (a.res) {
+            const uint8_t* q = a.res + row * a.res_row;
+            v += f32 ? reinterpret_cast<const float*>(q)[n]
+                     : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(q)[n] << 16);
+        }
+        uint8_t* p = a.out + g * a.out_stride + row * a.out_row;
+        if (f32) reinterpret_cast<float*>(p)[n] = v;
+        else reinterpret_cast<uint16_t*>(p)[n] = (uint16_t)to_bf16_rne(v);
     }
     __syncthreads();   // the next tile writes lds again
 }
 
 // ---------------------------------------------------------------------
-// Big tiles: 256 rows of x by 256 rows of w. Eight waves in two rows of four,
-// each with 128 x 64 of the sums in registers. Slabs of 128 bytes of k go
-// from memory straight into LDS (no register is spent on a load in flight),
-// one slab ahead of the one being multiplied; fragments are read from LDS
-// half a slab ahead, so that the reads of one half run under the products
-// of the other.
+// Big tiles: BM (256, 128 or 64) rows of x by 256 rows of w. Eight waves in
+// two rows of four, each with BM / 2 x 64 of the sums in registers. Slabs of
+// 128 bytes of k go from memory straight into LDS (no register is spent on a
+// load in flight), STAGES - 1 slabs ahead of the one being multiplied.
 //
 // LDS: row r of a slab holds its eight 16-byte chunks with chunk c at place
 // c ^ ((r >> 1) & 7), so the 16 rows of a fragment's read fall on different
 // banks. The load that fills LDS writes a wave's 64 x 16 bytes in lane order,
 // so the permutation is applied to the addresses that the lanes read.
+//
+// The 64 rows of w of a wave are permuted so that a lane's sums are 16
+// consecutive output columns (gated: 8): see wrow().
 // ---------------------------------------------------------------------
-constexpr int kBig = 256;
-constexpr int kBigSlab = kBig * kSlab;           // bytes of one operand's slab
-constexpr int kBigLds = 4 * kBigSlab;            // two slabs of both operands
+constexpr int kBig = 256;                        // rows of w
+constexpr int kBigSlab = kBig * kSlab;
+constexpr int kBigLds = 4 * kBigSlab;            // two slabs of 256 + 256 rows
+constexpr int kScaleLds = 2 * (kBig * 16 + 256); // two sets of scales of four slabs
 
-typedef __attribute__((address_space(3))) uint8_t lds_byte;
-typedef int i32x4 __attribute__((ext_vector_type(4)));
+template <int BM>
+constexpr int kStages = BM == 256 || BM == 128 ? 2 : 3;
+
+// Row of w behind row r of a tile whose first output column is n0, and its
+// output column n (columns n >= N do not exist). A fragment's row 4 q + t
+// becomes the sums t of the lanes 16 q ..: fragment i of a wave holds the
+// columns 16 q + 4 i + t, gated fragments 2 p + h the gate (h = 0) and up
+// rows of the columns 8 q + 4 p + t.
+template <bool GATED>
+__device__ __forceinline__ int wrow(int r, int n0, int N, int& n) {
+    const int i = (r >> 4) & 3, q = (r >> 2) & 3, t = r & 3;
+    if (!GATED) {
+        n = n0 + (r & ~63) + q * 16 + i * 4 + t;
+        return n;
+    }
+    n = n0 + (r >> 6) * 32 + q * 8 + (i >> 1) * 4 + t;
+    return (i & 1) ? N + n : n;
+}
 
 // The buffer resource of row_rsrc as four scalar registers.
 __device__ __forceinline__ i32x4 row_rsrc4(const uint8_t* p, int64_t bytes) {
     const uint64_t at = reinterpret_cast<uint64_t>(p);
     i32x4 r;
-    r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)at);
-    r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(at >> 32) & 0xFFFF);
-    r[2] = __builtin_amdgcn_readfirstlane((int)(bytes < INT32_MAX ? bytes : INT32_MAX));
+    r[0] = uniform((int)(uint32_t)at);
+    r[1] = uniform((int)(uint32_t)(at >> 32) & 0xFFFF);
+    r[2] = uniform((int)(bytes < INT32_MAX ? bytes : INT32_MAX));
     r[3] = 0x00020000;
     return r;
 }
 
-// 16 bytes per lane from memory into LDS, lane l's at dst + 16 l (dst is
-// uniform, in M0). Written out so that the compiler does not count it among
-// the loads that an LDS read has to wait for: with its own form of this
+// 16 (or 4) bytes per lane from memory into LDS, lane l's at dst + 16 l (4 l);
+// dst is uniform, in M0. Written out so that the compiler does not count it
+// among the loads that an LDS read has to wait for: with its own form of this
 // instruction it waits for every load in flight before the next LDS read,
 // whatever that reads. The instruction has no output register; what it
 // writes is ordered by the waits and barriers below.
@@ -345,17 +292,44 @@ __device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t dst, uint32_t off,
                  : "s"(dst), "v"(off), "s"(r), "s"(soff)
                  : "m0");
 }
-
-// Waits for this wave's loads into LDS and its LDS reads, then for the block.
-__device__ __forceinline__ void wait_all_and_barrier() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+__device__ __forceinline__ void load4_to_lds(i32x4 r, uint32_t dst, uint32_t off, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :
+                 : "s"(dst), "v"(off), "s"(r), "s"(soff)
+                 : "m0");
 }
 
+// Waits until at most LEFT of this wave's loads are in flight and for its LDS
+// reads, then for the block.
+template <int LEFT>
+__device__ __forceinline__ void wait_and_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+}
+
+// The four output columns n..n+3 (a quad) of a lane: act(v + b), gated with up.
 template <bool GATED>
+__device__ __forceinline__ f32x4 activate(f32x4 v, f32x4 up, int act) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = GATED ? silu_gated(v[i], up[i]) : apply_act(v[i], act);
+    return v;
+}
+
+__device__ __forceinline__ f32x4 load_f32x4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(f32x4, ld_row_buf<false>(r, off));
+}
+
+template <int EB, bool WIDE, bool GATED, int BM>
 __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
                                          uint8_t* lds) {
+    constexpr int JF = BM / 32;                   // fragments of x of a wave
+    constexpr int ST = kStages<BM>;
+    constexpr int SLAB_X = BM * kSlab;
+    constexpr int STAGE = SLAB_X + kBigSlab;
+    constexpr int FX = BM / 64;                   // loads of x of a wave and slab
+    constexpr int FETCH = FX + 4;
+    static_assert(ST * STAGE <= kBigLds, "");
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
+    const int wave = uniform(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int kb = a.row_bytes;
     const int nslab = (kb + kSlab - 1) / kSlab;
@@ -364,142 +338,377 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
     const i32x4 rx = row_rsrc4(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
                                (int64_t)(left - 1) * a.x_row + kb);
     const i32x4 rw = row_rsrc4(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
-        (int)(uint32_t)(uintptr_t)(lds_byte*)lds + wave * 1024);
+    const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
 
-    // a wave's instruction i fills rows (i * 8 + wave) * 8 .. + 7
+    // a wave's load i fills rows (i * 8 + wave) * 8 .. + 7
     const int sub = lane >> 3;
     const int chunk = (lane & 7) ^ ((((wave & 1) << 3 | sub) >> 1) & 7);
-    uint32_t vx[4], vw[4];
+    uint32_t vx[FX], vw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (i * 8 + wave) * 8 + sub;
-        vx[i] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk * 16 : kOutside;
+        if (i < FX) vx[i] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk * 16 : kOutside;
         int n;
         const int q = wrow<GATED>(r, n0, a.N, n);
         vw[i] = n < a.N ? (uint32_t)q * (uint32_t)a.w_row + chunk * 16 : kOutside;
     }
-    // the last slab may be short: its chunks past the end of k load zeros
+    // the last slab may be short: its chunks past the end of k load zeros, and
+    // so do slabs past the last
     const int last = (kb - chunk * 16 + kSlab - 1) / kSlab;
-    auto fetch = [&](int s) {
+    auto fetch = [&](int s, int stage) {
         const uint32_t none = s < last ? 0u : kOutside;
-        const uint32_t d = lds0 + (s & 1) * 2 * kBigSlab;
+        const uint32_t k = s < nslab ? s * kSlab : 0;   // stays within the range
+        const uint32_t d = lds0 + stage * STAGE + wave * 1024;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_to_lds(rx, d + i * 8192, vx[i] | none, s * kSlab);
+        for (int i = 0; i < FX; ++i) load_to_lds(rx, d + i * 8192, vx[i] | none, k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            load_to_lds(rw, d + kBigSlab + i * 8192, vw[i] | none, s * kSlab);
+        for (int i = 0; i < 4; ++i) load_to_lds(rw, d + SLAB_X + i * 8192, vw[i] | none, k);
+    };
+
+    // fp8: the scales of four slabs at a time, 16 bytes per row of x, and 4
+    // bytes per block of w and slab (at most 4 blocks); slab s's set is s/4 & 1
+    constexpr int SCALES = kBig * 16 + 256;
+    uint32_t vxs = kOutside, vws = kOutside;
+    i32x4 rxs = rx, rws = rw;
+    if constexpr (EB == 1) {
+        const int row = wave * 64 + lane;
+        if (row < BM && row < left) vxs = (uint32_t)row * (uint32_t)a.xs_pitch * 4;
+        rxs = row_rsrc4(reinterpret_cast<const uint8_t*>(a.xs + g * a.xs_stride +
+                                                         (int64_t)m0 * a.xs_pitch),
+                        (int64_t)left * a.xs_pitch * 4);
+        // block b of the tile: two runs of 128 columns, gated: gate and up
+        const int per = (a.N + kScaleBlock - 1) / kScaleBlock;
+        const int b = lane >> 2;
+        const int n = n0 + (GATED ? 0 : b * kScaleBlock);
+        if (b < 2 && n < a.N)
+            vws = ((uint32_t)(n / kScaleBlock + (GATED ? b * per : 0)) * (uint32_t)nslab +
+                   (lane & 3)) * 4;
+        rws = row_rsrc4(reinterpret_cast<const uint8_t*>(a.ws + g * a.ws_stride),
+                        (int64_t)(GATED ? 2 : 1) * per * nslab * 4);
+    }
+    const uint32_t scales0 = lds0 + kBigLds;
+    auto fetch_scales = [&](int s) {              // s a multiple of 4
+        const uint32_t d = scales0 + ((s >> 2) & 1) * SCALES;
+        const uint32_t none = s < nslab ? 0u : kOutside;
+        const uint32_t k = s < nslab ? s * 4 : 0;
+        if (wave * 64 < BM) load_to_lds(rxs, d + wave * 1024, vxs | none, k);
+        if (wave == kWaves - 1)
+            load4_to_lds(rws, d + kBig * 16, s + (lane & 3) < nslab ? vws : kOutside, k);
     };
 
     const int rd = (lane & 15) * kSlab + ((((lane >> 4) * 2) ^ ((lane >> 1) & 7)) * 16);
-    const uint8_t* rdx = lds + wm * 128 * kSlab;
-    const uint8_t* rdw = lds + kBigSlab + wn * 64 * kSlab;
-    u32x4 fx[2][8], fw[2][4];
-    auto read = [&](int s, int h, u32x4 (&x)[8], u32x4 (&w)[4]) {
-        const int o = (s & 1) * 2 * kBigSlab + (rd ^ (h * 16));
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = *reinterpret_cast<const u32x4*>(rdw + o + i * 16 * kSlab);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            x[j] = *reinterpret_cast<const u32x4*>(rdx + o + j * 16 * kSlab);
-    };
-    f32x4 acc[4][8];
+    const uint8_t* rdx = lds + wm * (BM / 2) * kSlab;
+    const uint8_t* rdw = lds + SLAB_X + wn * 64 * kSlab;
+    f32x4 acc[4][JF];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](const u32x4 (&x)[8], const u32x4 (&w)[4]) {
+        for (int j = 0; j < JF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if constexpr (EB == 1) fetch_scales(0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+    for (int s = 0; s < ST - 1; ++s) fetch(s, s);
+
+    if constexpr (EB == 2) {
+        // Fragments are read half a slab ahead, so that the reads of one half
+        // run under the products of the other.
+        u32x4 fx[2][JF], fw[2][4];
+        auto read = [&](int stage, int h, u32x4 (&x)[JF], u32x4 (&w)[4]) {
+            const int o = stage * STAGE + (rd ^ (h * 16));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8, w[i]), __builtin_bit_cast(bf16x8, x[j]), acc[i][j],
-                    0, 0, 0);
-    };
-
-    fetch(0);
-    fetch(1);       // a slab past the last loads zeros
-    asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
-    read(0, 0, fx[0], fw[0]);
-    // the reads of the half after, one to every two or three products
-    auto spread = [&]() {
+                w[i] = *reinterpret_cast<const u32x4*>(rdw + o + i * 16 * kSlab);
 #pragma unroll
-        for (int i = 0; i < 12; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
-            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // MFMA
+            for (int j = 0; j < JF; ++j)
+                x[j] = *reinterpret_cast<const u32x4*>(rdx + o + j * 16 * kSlab);
+        };
+        auto multiply = [&](const u32x4 (&x)[JF], const u32x4 (&w)[4]) {
+#pragma unroll
+            for (int j = 0; j < JF; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][j] = mma_bf16(w[i], x[j], acc[i][j]);
+        };
+        // the reads of the half after, one to every one or two products
+        auto spread = [&]() {
+#pragma unroll
+            for (int i = 0; i < 4 + JF; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);              // LDS read
+                __builtin_amdgcn_sched_group_barrier(0x008, JF > 4 ? 2 : 1, 0);   // MFMA
+            }
+        };
+        fetch(ST - 1, ST - 1);
+        wait_and_barrier<(ST - 1) * FETCH>();
+        read(0, 0, fx[0], fw[0]);
+        int now = 0, next = 1;                    // stages of slabs s and s + 1
+        for (int s = 0; s < nslab; ++s) {
+            read(now, 1, fx[1], fw[1]);
+            multiply(fx[0], fw[0]);
+            spread();
+            // slab s is read; slab s + 1 has arrived
+            wait_and_barrier<(ST - 2) * FETCH>();
+            fetch(s + ST, now);
+            read(next, 0, fx[0], fw[0]);
+            multiply(fx[1], fw[1]);
+            spread();
+            __builtin_amdgcn_sched_barrier(0);
+            now = next;
+            next = next + 1 < ST ? next + 1 : 0;
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
-    };
-    for (int s = 0; s < nslab; ++s) {
-        read(s, 1, fx[1], fw[1]);
-        multiply(fx[0], fw[0]);
-        spread();
-        // slab s is read; slab s + 1 has arrived
-        wait_all_and_barrier();
-        fetch(s + 2);
-        read(s + 1, 0, fx[0], fw[0]);
-        multiply(fx[1], fw[1]);
-        spread();
-        __builtin_amdgcn_sched_barrier(0);
+    } else {
+        // Slab by slab: the sums of a slab are complete before they are
+        // scaled, so the halves cannot be taken apart.
+        const int bw = GATED ? 0 : wn >> 1;       // the wave's block (gated: both)
+        int now = 0;
+        for (int s = 0; s < nslab; ++s) {
+            // slab s and its scales (older than the loads that may still be
+            // in flight) have arrived; slab s - 1 is read
+            wait_and_barrier<(ST - 2) * FETCH>();
+            const int to = now == 0 ? ST - 1 : now - 1;
+            fetch(s + ST - 1, to);
+            if ((s & 3) == 2) fetch_scales((s & ~3) + 4);
+            const float* sc = reinterpret_cast<const float*>(lds + kBigLds + ((s >> 2) & 1) * SCALES);
+            const float sg = sc[kBig * 4 + bw * 4 + (s & 3)];
+            const float su = GATED ? sc[kBig * 4 + 4 + (s & 3)] : sg;
+            const int o = now * STAGE + rd;
+            auto frag = [&](const uint8_t* p) {
+                Frag f;
+                f.v[0] = *reinterpret_cast<const u32x4*>(p + o);
+                f.v[1] = *reinterpret_cast<const u32x4*>(p + (o ^ 16));
+                return f;
+            };
+            auto scale = [&](int i, int j, f32x4 t, float sx) {
+                const float f = sx * (GATED && (i & 1) ? su : sg);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(t[q], f, acc[i][j][q]);
+            };
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (WIDE) {
+                Wide w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = widen(frag(rdw + i * 16 * kSlab));
+#pragma unroll
+                for (int j = 0; j < JF; ++j) {
+                    const Wide x = widen(frag(rdx + j * 16 * kSlab));
+                    const float sx = sc[(wm * (BM / 2) + j * 16 + (lane & 15)) * 4 + (s & 3)];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) scale(i, j, mma_wide(w[i], x, zero), sx);
+                }
+            } else {
+                Frag w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = frag(rdw + i * 16 * kSlab);
+#pragma unroll
+                for (int j = 0; j < JF; ++j) {
+                    const Frag x = frag(rdx + j * 16 * kSlab);
+                    const float sx = sc[(wm * (BM / 2) + j * 16 + (lane & 15)) * 4 + (s & 3)];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) scale(i, j, mma_fp8(w[i], x, zero), sx);
+                }
+            }
+            now = now + 1 < ST ? now + 1 : 0;
+        }
     }
-    wait_all_and_barrier();   // LDS is free for the next tile
+    wait_and_barrier<0>();   // LDS is free for what follows
 
+    // Epilogue. A lane has QN quads of consecutive columns from n on, of rows
+    // wm * BM / 2 + 16 j + lane % 16. Rows and columns that do not exist are
+    // outside the buffers' ranges: their loads give 0, their stores nothing.
+    constexpr int QN = GATED ? 2 : 4;
+    const int n = n0 + (GATED ? wn * 32 + (lane >> 4) * 8 : wn * 64 + (lane >> 4) * 16);
+    if (a.bias) {
+        const auto rb = row_rsrc(reinterpret_cast<const uint8_t*>(a.bias + g * a.bias_stride),
+                                 (int64_t)nw * 4);
 #pragma unroll
-    for (int i = 0; i < 4; i += GATED ? 2 : 1) {
-        const int r = wn * 64 + i * 16 + (lane >> 4) * 4;
-        int n;
-        wrow<GATED>(r, n0, a.N, n);
-        if (n >= a.N) continue;
+        for (int q = 0; q < QN; ++q) {
+            const uint32_t at = n + q * 4 < a.N ? (uint32_t)(n + q * 4) * 4 : kOutside;
+            const f32x4 b = load_f32x4(rb, at);
+            const f32x4 bu = GATED ? load_f32x4(rb, at + (uint32_t)a.N * 4) : b;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int m = wm * 128 + j * 16 + (lane & 15);
-            if (m >= left) continue;
-            const f32x4 y = finish<GATED>(a, g, n, acc[i][j], acc[GATED ? i + 1 : i][j]);
-            store_out(a, g, m0 + m, n, y);
+            for (int j = 0; j < JF; ++j) {
+                acc[GATED ? 2 * q : q][j] += b;
+                if (GATED) acc[2 * q + 1][j] += bu;
+            }
         }
+    }
+    auto value = [&](int q, int j) {
+        return activate<GATED>(acc[GATED ? 2 * q : q][j], acc[GATED ? 2 * q + 1 : q][j], a.act);
+    };
+    uint8_t* const out = a.out + g * a.out_stride + (int64_t)m0 * a.out_row;
+    const int mrow = wm * (BM / 2) + (lane & 15);
+
+    if constexpr (EB == 1 && WIDE) {
+        if (a.out_dtype == MOE_EP_E4M3) {
+            // a row's 128 columns lie in 4 (gated) or 2 waves, 4 lanes each
+            constexpr int WG = GATED ? 4 : 2;
+            float* part = reinterpret_cast<float*>(lds);            // [BM][4]
+            f32x4 y[QN][JF];
+#pragma unroll
+            for (int j = 0; j < JF; ++j) {
+                float mx = 0.f;
+#pragma unroll
+                for (int q = 0; q < QN; ++q) {
+                    y[q][j] = value(q, j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx = abs_max(mx, y[q][j][e]);
+                }
+                mx = abs_max(mx, __shfl_xor(mx, 16, 64));
+                mx = abs_max(mx, __shfl_xor(mx, 32, 64));
+                if (lane < 16) part[(mrow + j * 16) * 4 + wn] = mx;
+            }
+            __syncthreads();
+            const int groups = a.N / kScaleBlock;
+#pragma unroll
+            for (int j = 0; j < JF; ++j) {
+                const int m = mrow + j * 16;
+                float mx = 0.f;
+#pragma unroll
+                for (int w = 0; w < WG; ++w) mx = abs_max(mx, part[m * 4 + (GATED ? 0 : wn & 2) + w]);
+                const float s = mx > 0.f ? mx / 448.0f : 1.0f;
+                if (m < left && n < a.N) {
+                    uint32_t* o = reinterpret_cast<uint32_t*>(out + (int64_t)m * a.out_row + n);
+#pragma unroll
+                    for (int q = 0; q < QN; ++q) o[q] = codes4(y[q][j], s);
+                    float* os = a.os + g * a.os_stride + (int64_t)(m0 + m) * a.os_pitch;
+                    if (lane < 16 && wn % WG == 0) {
+                        os[n / kScaleBlock] = s;
+                        // the last group's wave also writes the padding
+                        if (n / kScaleBlock == groups - 1)
+                            for (int p = groups; p < (int)a.os_pitch; ++p) os[p] = 0.f;
+                    }
+                }
+            }
+            __syncthreads();   // the next tile writes lds again
+            return;
+        }
+    }
+
+    const bool f32 = EB == 1 ? WIDE : a.out_dtype == MOE_EP_F32;
+    const int eb = f32 ? 4 : 2;
+    const auto ro = row_rsrc(out, (int64_t)(left - 1) * a.out_row + (int64_t)a.N * eb);
+    const auto rr = row_rsrc(a.res ? a.res + (int64_t)m0 * a.res_row : out,
+                             a.res ? (int64_t)(left - 1) * a.res_row + (int64_t)a.N * eb : 0);
+    auto at = [&](int j, int q, int64_t row) {
+        const int m = mrow + j * 16, c = n + q * 4;
+        return m < left && c < a.N ? (uint32_t)m * (uint32_t)row + (uint32_t)(c * eb) : kOutside;
+    };
+    if (f32) {
+#pragma unroll
+        for (int j = 0; j < JF; ++j) {
+            f32x4 r[QN];
+            if (a.res) {
+#pragma unroll
+                for (int q = 0; q < QN; ++q) r[q] = load_f32x4(rr, at(j, q, a.res_row));
+            }
+#pragma unroll
+            for (int q = 0; q < QN; ++q) {
+                f32x4 y = value(q, j);
+                if (a.res) y += r[q];
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), ro,
+                                                       at(j, q, a.out_row), 0, 0);
+            }
+        }
+        return;
+    }
+    // bf16: N is a multiple of 8, so eight columns exist together; the
+    // residuals of four rows are on their way at once
+    constexpr int JB = JF < 4 ? JF : 4;
+#pragma unroll
+    for (int j0 = 0; j0 < JF; j0 += JB) {
+        u32x4 r[JB][QN / 2];
+        if (a.res) {
+#pragma unroll
+            for (int j = 0; j < JB; ++j)
+#pragma unroll
+                for (int q = 0; q < QN / 2; ++q)
+                    r[j][q] = ld_row_buf<false>(rr, at(j0 + j, 2 * q, a.res_row));
+        }
+#pragma unroll
+        for (int j = 0; j < JB; ++j)
+#pragma unroll
+            for (int q = 0; q < QN / 2; ++q) {
+                f32x4 lo = value(2 * q, j0 + j), hi = value(2 * q + 1, j0 + j);
+                if (a.res) {
+                    const u32x4 v = r[j][q];
+                    lo += f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+                    hi += f32x4{bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3])};
+                }
+                const u32x2 l = pack_bf16(lo), h = pack_bf16(hi);
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{l[0], l[1], h[0], h[1]}, ro,
+                                                       at(j0 + j, 2 * q, a.out_row), 0, 0);
+            }
     }
 }
 
-// The work list: big tiles of every group, then small ones. A group's rows
-// are cut into runs of 256; what is left is a big tile too where it has more
-// than `big_from` rows, else small tiles.
+// ---------------------------------------------------------------------
+// The work list. A group's rows are cut into runs of 256; what is left into
+// 128, 64 and, up to small_to rows, small tiles. Tiles are dealt out largest
+// first. With few tiles in all, runs are 64 rows (see make_plan).
+// ---------------------------------------------------------------------
+constexpr int kKinds = 4;                        // 256, 128, 64 rows, small
+
 struct Plan {
-    int32_t big[MOE_EP_MAX_LOCAL_EXPERTS + 1];      // tiles in front of a group
-    int32_t small[MOE_EP_MAX_LOCAL_EXPERTS + 1];
+    int32_t pre[kKinds][MOE_EP_MAX_LOCAL_EXPERTS + 1];   // tiles in front of a group
 };
 
-__device__ __forceinline__ int big_runs(int rows, int big_from) {
-    return rows / kBig + (rows % kBig > big_from ? 1 : 0);
-}
+struct Cut {
+    int n[kKinds];                               // runs of rows of each kind
+};
 
-template <int BM>
-__device__ __forceinline__ void make_plan(const MatmulArgs& a, int big_from, int nt_big,
-                                          int nt_small, Plan* p) {
-    if (threadIdx.x < 64) {
-        int32_t run_b = 0, run_s = 0;
-        for (int g0 = 0; g0 < a.groups; g0 += 64) {
-            const int g = g0 + (int)threadIdx.x;
-            const int rows = g < a.groups ? group_rows(a, g) : 0;
-            const int b = big_from < kBig ? big_runs(rows, big_from) : 0;
-            const int rest = rows - b * kBig;
-            const int32_t tb = b * nt_big;
-            const int32_t ts = rest > 0 ? (rest + BM - 1) / BM * nt_small : 0;
-            const int32_t ib = wave_inclusive_scan(tb), is = wave_inclusive_scan(ts);
-            if (g < a.groups) {
-                p->big[g] = run_b + ib - tb;
-                p->small[g] = run_s + is - ts;
-            }
-            run_b += __shfl(ib, 63, 64);
-            run_s += __shfl(is, 63, 64);
-        }
-        if (threadIdx.x == 0) {
-            p->big[a.groups] = run_b;
-            p->small[a.groups] = run_s;
+__device__ __forceinline__ Cut cut_rows(int rows, int largest, int small_to) {
+    Cut c = {};
+    if (largest == 0) {
+        c.n[3] = (rows + kSmall - 1) / kSmall;
+        return c;
+    }
+    int r = rows;
+    if (largest == 256) {
+        c.n[0] = r / 256;
+        r %= 256;
+        if (r > 192) {
+            ++c.n[0];
+            r = 0;
+        } else if (r > 64) {
+            c.n[1] = 1;
+            r = r > 128 ? r - 128 : 0;
         }
     }
+    c.n[2] = r / 64;
+    r %= 64;
+    if (r > small_to) ++c.n[2];
+    else c.n[3] = (r + kSmall - 1) / kSmall;
+    return c;
+}
+
+// Returns the largest run. Runs of 256 rows leave most of the chip idle when
+// there are fewer than half as many tiles as CUs; 64-row runs then spread the
+// weights' loads over more of it (two runs of an expert read the same weights
+// at the same time, from one L2).
+__device__ __forceinline__ int make_plan(const MatmulArgs& a, int largest, int small_to,
+                                         int nt_big, int nt_small, int cus, Plan* p) {
+    __shared__ int32_t chosen;
+    if (threadIdx.x < 64) {
+        for (;;) {
+            int32_t run[kKinds] = {};
+            for (int g0 = 0; g0 < a.groups; g0 += 64) {
+                const int g = g0 + (int)threadIdx.x;
+                Cut c = {};
+                if (g < a.groups) c = cut_rows(group_rows(a, g), largest, small_to);
+#pragma unroll
+                for (int k = 0; k < kKinds; ++k) {
+                    const int32_t t = c.n[k] * (k == 3 ? nt_small : nt_big);
+                    const int32_t inc = wave_inclusive_scan(t);
+                    if (g < a.groups) p->pre[k][g] = run[k] + inc - t;
+                    run[k] += __shfl(inc, 63, 64);
+                }
+            }
+            if (threadIdx.x < kKinds) p->pre[threadIdx.x][a.groups] = run[threadIdx.x];
+            if (largest != 256 || run[0] + run[1] + run[2] > cus / 2) break;
+            largest = 64;
+        }
+        if (threadIdx.x == 0) chosen = largest;
+    }
     __syncthreads();
+    return uniform(chosen);
 }
 
 // Tile of block b in a round of `left` tiles over the grid, -1 for none.
@@ -513,53 +722,73 @@ __device__ __forceinline__ int tile_of(int b, int grid, int left) {
     return slot < per && t < r ? t : -1;
 }
 
-template <int EB, bool GATED, int BM, int BN, int DEPTH, bool BIG>
-__global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a, int big_from) {
-    constexpr int kSmallLds = kWaves * BM * (BN + 4) * 4;
-    __shared__ __align__(1024) uint8_t lds[BIG && kBigLds > kSmallLds ? kBigLds : kSmallLds];
+template <int EB, bool WIDE, bool GATED, bool BIG>
+__global__ __launch_bounds__(kThreads, BIG ? 2 : 4) void matmul_kernel(const MatmulArgs a,
+                                                                       int small_to) {
+    __shared__ __align__(1024) uint8_t
+        lds[BIG ? kBigLds + (EB == 1 ? kScaleLds : 0) : kSmallLds];
     __shared__ Plan p;
-    constexpr int BO = GATED ? BN / 2 : BN;
+    constexpr int BO = GATED ? kSmall / 2 : kSmall;
     constexpr int BB = GATED ? kBig / 2 : kBig;
     const int nt = (a.N + BO - 1) / BO, ntb = (a.N + BB - 1) / BB;
-    make_plan<BM>(a, BIG ? big_from : kBig, ntb, nt, &p);
-    const int nbig = BIG ? uniform(p.big[a.groups]) : 0;
-    const int total = nbig + uniform(p.small[a.groups]);
+    const int largest = make_plan(a, BIG ? 256 : 0, small_to, ntb, nt, gridDim.x, &p);
+    int total = 0;
+#pragma unroll
+    for (int k = BIG ? 0 : 3; k < kKinds; ++k) total += uniform(p.pre[k][a.groups]);
     for (int t0 = 0; t0 < total; t0 += gridDim.x) {
-        const int at = tile_of(blockIdx.x, gridDim.x, total - t0);
-        if (at < 0) break;      // a last, partial round
-        const int t = t0 + at;
+        int t = tile_of(blockIdx.x, gridDim.x, total - t0);
+        if (t < 0) break;       // a last, partial round
+        t += t0;
+        int kind = BIG ? 0 : 3;
+        while (kind < 3 && t >= uniform(p.pre[kind][a.groups]))
+            t -= uniform(p.pre[kind++][a.groups]);
+        const int g = uniform(find_source(p.pre[kind], a.groups, t));
+        const int rows = uniform(group_rows(a, g));
+        const Cut c = cut_rows(rows, largest, small_to);
+        const int l = t - uniform(p.pre[kind][g]);
+        if (kind == 3) {
+            const int from = c.n[0] * 256 + c.n[1] * 128 + c.n[2] * 64;
+            const int mt = c.n[3];
+            small_tile<EB, WIDE, GATED>(a, g, from + l % mt * kSmall, rows, l / mt * BO,
+                                        reinterpret_cast<float*>(lds));
+            continue;
+        }
         if constexpr (BIG) {
-            if (t < nbig) {
-                const int g = uniform(find_source(p.big, a.groups, t));
-                const int rows = uniform(group_rows(a, g));
-                const int mt = big_runs(rows, big_from);
+            if (kind == 0) {
                 // eight runs of rows at a time, over all columns
-                const int l = t - uniform(p.big[g]);
                 const int m8 = l / (8 * ntb) * 8;
-                const int wide = mt - m8 < 8 ? mt - m8 : 8;
+                const int wide = c.n[0] - m8 < 8 ? c.n[0] - m8 : 8;
                 const int in = l - m8 * ntb;
-                big_tile<GATED>(a, g, (m8 + in % wide) * kBig, rows, in / wide * BB, lds);
-                continue;
+                big_tile<EB, WIDE, GATED, 256>(a, g, (m8 + in % wide) * 256, rows, in / wide * BB,
+                                               lds);
+            } else if (kind == 1) {
+                big_tile<EB, WIDE, GATED, 128>(a, g, c.n[0] * 256, rows, l * BB, lds);
+            } else {
+                const int from = c.n[0] * 256 + c.n[1] * 128;
+                big_tile<EB, WIDE, GATED, 64>(a, g, from + l % c.n[2] * 64, rows,
+                                              l / c.n[2] * BB, lds);
             }
         }
-        const int l0 = t - nbig;
-        const int g = uniform(find_source(p.small, a.groups, l0));
-        const int rows = uniform(group_rows(a, g));
-        const int from = BIG ? big_runs(rows, big_from) * kBig : 0;
-        const int mt = (rows - from + BM - 1) / BM;
-        const int l = l0 - uniform(p.small[g]);
-        small_tile<EB, GATED, BM, BN, DEPTH>(a, g, from + l % mt * BM, rows, l / mt * BO,
-                                             reinterpret_cast<float*>(lds));
     }
 }
 
-template <int EB, bool GATED, int BM, int BN, int DEPTH, bool BIG = false>
+template <int EB, bool WIDE, bool GATED>
 hipError_t launch(const MatmulArgs& a, hipStream_t st) {
-    constexpr int BO = GATED ? BN / 2 : BN;
-    const int64_t most = (int64_t)a.groups * ((a.rows + BM - 1) / BM) * ((a.N + BO - 1) / BO);
-    const int64_t grid = most < 256 ? (most + 7) / 8 * 8 : 256;
-    matmul_kernel<EB, GATED, BM, BN, DEPTH, BIG>
-        <<<(unsigned)grid, kThreads, 0, st>>>(a, BIG ? 128 : kBig);
+    constexpr int BO = GATED ? kSmall / 2 : kSmall;
+    constexpr int BB = GATED ? kBig / 2 : kBig;
+    const int64_t small =
+        (int64_t)a.groups * ((a.rows + kSmall - 1) / kSmall) * ((a.N + BO - 1) / BO);
+    const int64_t runs = (int64_t)a.groups * ((a.rows + 63) / 64) * ((a.N + BB - 1) / BB);
+    const bool e4m3 = a.out_dtype == MOE_EP_E4M3;
+    const bool few = !e4m3 && (a.counts ? a.rows <= 2 * kSmall : a.rows <= kSmall || runs < 64);
+    if (few) {
+        const int64_t grid = small < 512 ? (small + 7) / 8 * 8 : 512;
+        matmul_kernel<EB, WIDE, GATED, false>
+            <<<(unsigned)grid, kThreads, 0, st>>>(a, a.rows);
+    } else {
+        matmul_kernel<EB, WIDE, GATED, true>
+            <<<256, kThreads, 0, st>>>(a, e4m3 ? 0 : kSmall);
+    }
     return hipGetLastError();
 }
 
@@ -567,15 +796,10 @@ hipError_t launch(const MatmulArgs& a, hipStream_t st) {
 
 hipError_t launch_matmul(const MatmulArgs& a, hipStream_t st) {
     const bool gated = a.act == MOE_EP_ACT_SILU_GATED;
-    if (a.fp8) {
-        if (a.out_dtype == MOE_EP_E4M3)
-            return gated ? launch<1, true, 16, 256, 1>(a, st) : launch<1, false, 16, 128, 2>(a, st);
-        return gated ? launch<1, true, 64, 64, 1>(a, st) : launch<1, false, 64, 64, 1>(a, st);
-    }
-    if (a.rows > 128)
-        return gated ? launch<2, true, 64, 64, 1, true>(a, st)
-                     : launch<2, false, 64, 64, 1, true>(a, st);
-    return gated ? launch<2, true, 64, 64, 1>(a, st) : launch<2, false, 64, 64, 1>(a, st);
+    if (!a.fp8) return gated ? launch<2, false, true>(a, st) : launch<2, false, false>(a, st);
+    if (a.out_dtype == MOE_EP_BF16)
+        return gated ? launch<1, false, true>(a, st) : launch<1, false, false>(a, st);
+    return gated ? launch<1, true, true>(a, st) : launch<1, true, false>(a, st);
 }
 
 }  // namespace moe_ep

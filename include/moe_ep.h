@@ -625,8 +625,8 @@ MOE_EP_API int moe_ep_expert_matmul_fp8(const void* x, int64_t x_stride, const f
  *                 between tokens (>= N). May be out itself (same stride).
  *   out           bf16 or fp32 [T, N], out_stride elements between tokens.
  * Rows, strides and pointers are multiples of 16 bytes (EALIGN). Strides of
- * x are below 2^23 bytes; limits as for moe_ep_expert_matmul (Nw * w_stride
- * * 2 < 2^31 bytes).
+ * x, residual and out are below 2^23 bytes; limits as for
+ * moe_ep_expert_matmul (Nw * w_stride * 2 < 2^31 bytes).
  */
 MOE_EP_API int moe_ep_matmul(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
                              const float* bias, int64_t T, int64_t H, int64_t N, int32_t act,
