@@ -148,7 +148,7 @@ def _check(name: str, status: int):
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -160,6 +160,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _dense_from(t: torch.Tensor, first: int, name: str):
     """Checks that dims >= first of t are dense (row-major, no gaps)."""
+    if t.is_contiguous():
+        return
     exp = 1
     for ax in range(t.dim() - 1, first - 1, -1):
         if t.size(ax) > 1 and t.stride(ax) != exp:
@@ -247,7 +249,7 @@ def _lead_at_least(t: torch.Tensor, mins: Sequence[int], name: str):
 def _shape(t: Optional[torch.Tensor], shape: Sequence[int], name: str, dtypes=None):
     if t is None:
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtypes is not None and t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype} not in {dtypes}")
@@ -351,13 +353,13 @@ class PreparedCall:
     the stream of a call must belong to that GPU."""
 
     def __init__(self, name: str, args: tuple, keep: tuple):
-        devices = {t.device for t in _tensors(keep)}
-        if any(d.type != "cuda" for d in devices) or len(devices) > 1:
+        devices = {t.get_device() for t in _tensors(keep)}      # -1: not a GPU
+        if len(devices) > 1 or -1 in devices:
             raise ValueError(f"{name}: every tensor must be on one GPU, got "
-                             f"{sorted(str(d) for d in devices)}")
-        self.device = devices.pop().index if devices else None
+                             f"{sorted({str(t.device) for t in _tensors(keep)})}")
+        self.device = devices.pop() if devices else None
         self.name = name
-        self.fn = getattr(load(), name)
+        self.fn = getattr(_lib or load(), name)
         self.args = args
         self.keep = keep
 
@@ -371,13 +373,15 @@ class PreparedCall:
         _check(self.name, self.fn(*self.args, _stream(stream)))
 
 
-def _tensors(x):
+def _tensors(x) -> list:
     """The tensors in a nest of tuples and lists."""
-    if isinstance(x, torch.Tensor):
-        yield x
-    elif isinstance(x, (tuple, list)):
-        for y in x:
-            yield from _tensors(y)
+    found = []
+    for y in x:
+        if isinstance(y, torch.Tensor):
+            found.append(y)
+        elif isinstance(y, (tuple, list)):
+            found += _tensors(y)
+    return found
 
 
 def _ws_bytes(workspace: torch.Tensor) -> int:
@@ -850,6 +854,8 @@ def _choice(table, name, what: str) -> int:
 def _rows_dense(t: torch.Tensor, first: int, name: str):
     """The dims from `first` on are dense and each block before them starts
     at or behind the end of the one before."""
+    if t.is_contiguous():
+        return
     _dense_from(t, first, name)
     n = 1
     for x in t.shape[first:]:
