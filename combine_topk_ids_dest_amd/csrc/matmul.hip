@@ -17,6 +17,8 @@
 // 4e-7 in bf16). That vanishes under the rounding of a bf16 result (2^-8), so
 // bf16 outputs use it; for fp32 and e4m3 outputs, whose scales are fp32, the
 // codes are widened to bf16 (exactly) and multiplied there (`WIDE`).
+#include <type_traits>
+
 #include "experts.h"
 
 namespace moe_ep {
@@ -29,7 +31,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;                    // of a block of big tiles
 constexpr int kWaves = kThreads / 64;
 constexpr int kSlab = 128;                       // bytes of k per step
 constexpr uint32_t kOutside = 0x80000000u;       // past every buffer's range
@@ -123,17 +125,18 @@ __device__ __forceinline__ int group_rows(const MatmulArgs& a, int g) {
 // ---------------------------------------------------------------------
 // Small tiles, for a few rows: 16 rows of x by 16 rows of w (gated: 8 gate
 // rows and their 8 up rows). Bound by the weights' bytes, so what counts is
-// loads in flight: the slabs of k are dealt to the block's eight waves in
-// turn (the block reads 1 KB runs of each row), each keeps four slabs of both
+// loads in flight: the slabs of k are dealt to the block's waves in turn (the
+// block reads runs of 1 or 2 KB of each row), each keeps four slabs of both
 // operands on their way to registers, and the waves' sums are added in wave
 // order through LDS.
 // ---------------------------------------------------------------------
 constexpr int kSmall = 16;
 constexpr int kSmallPitch = kSmall + 4;
-constexpr int kSmallLds = kWaves * kSmall * kSmallPitch * 4;
+template <int WAVES>
+constexpr int kSmallLds = WAVES * kSmall * kSmallPitch * 4;
 constexpr int kSmallDepth = 4;
 
-template <int EB, bool WIDE, bool GATED>
+template <int EB, bool WIDE, bool GATED, int WAVES>
 __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
                                            float* lds) {
     const int lane = threadIdx.x & 63;
@@ -181,8 +184,8 @@ __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, i
         }
     };
 #pragma unroll
-    for (int d = 0; d < kSmallDepth; ++d) load(d, wave + d * kWaves);
-    for (int s = wave; s < nslab; s += kWaves * kSmallDepth) {
+    for (int d = 0; d < kSmallDepth; ++d) load(d, wave + d * WAVES);
+    for (int s = wave; s < nslab; s += WAVES * kSmallDepth) {
 #pragma unroll
         for (int d = 0; d < kSmallDepth; ++d) {
             if constexpr (EB == 2) {
@@ -195,7 +198,7 @@ __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, i
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(t[q], sc[d], acc[q]);
             }
-            load(d, s + (d + kSmallDepth) * kWaves);
+            load(d, s + (d + kSmallDepth) * WAVES);
         }
     }
 
@@ -207,7 +210,7 @@ __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, i
     if (m < kSmall && m < left && n < a.N) {
         float v = 0.f, up = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             v += lds[(w * kSmall + m) * kSmallPitch + o];
             if (GATED) up += lds[(w * kSmall + m) * kSmallPitch + o + 8];
         }
@@ -238,9 +241,13 @@ __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, i
 // load in flight), STAGES - 1 slabs ahead of the one being multiplied.
 //
 // LDS: row r of a slab holds its eight 16-byte chunks with chunk c at place
-// c ^ ((r >> 1) & 7), so the 16 rows of a fragment's read fall on different
-// banks. The load that fills LDS writes a wave's 64 x 16 bytes in lane order,
-// so the permutation is applied to the addresses that the lanes read.
+// c ^ ((r >> 1) & 7), and lane l of a fragment takes the chunks l / 16 and
+// l / 16 + 4 of row l % 16. A 16-byte read is served 16 lanes at a time,
+// lanes 0-3, 12-15, 20-27 first and 4-11, 16-19, 28-31 next (then the same of
+// the upper half): both sets fall on all 64 banks. (With chunks 2 (l / 16) and
+// the one after, every read met a conflict: 8 cycles instead of 4.) The load
+// that fills LDS writes a wave's 64 x 16 bytes in lane order, so the
+// permutation is applied to the addresses that the lanes read.
 //
 // The 64 rows of w of a wave are permuted so that a lane's sums are 16
 // consecutive output columns (gated: 8): see wrow().
@@ -396,7 +403,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
             load4_to_lds(rws, d + kBig * 16, s + (lane & 3) < nslab ? vws : kOutside, k);
     };
 
-    const int rd = (lane & 15) * kSlab + ((((lane >> 4) * 2) ^ ((lane >> 1) & 7)) * 16);
+    const int rd = (lane & 15) * kSlab + (((lane >> 4) ^ ((lane >> 1) & 7)) * 16);
     const uint8_t* rdx = lds + wm * (BM / 2) * kSlab;
     const uint8_t* rdw = lds + SLAB_X + wn * 64 * kSlab;
     f32x4 acc[4][JF];
@@ -413,44 +420,48 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
         // Fragments are read half a slab ahead, so that the reads of one half
         // run under the products of the other.
         u32x4 fx[2][JF], fw[2][4];
-        auto read = [&](int stage, int h, u32x4 (&x)[JF], u32x4 (&w)[4]) {
-            const int o = stage * STAGE + (rd ^ (h * 16));
+        // Multiplies one half while reading another, and with FETCHES loads
+        // slab f into its stage, all in small steps: a wave issues in order, so
+        // eight loads in a row would hold up the products behind them until the
+        // address unit has taken the loads of all eight waves.
+        auto step = [&](const u32x4 (&x)[JF], const u32x4 (&w)[4], int stage, int h,
+                        u32x4 (&nx)[JF], u32x4 (&nwf)[4], auto fetches, int f, int to) {
+            const int o = stage * STAGE + (rd ^ (h * 64));
+            const uint32_t none = f < last ? 0u : kOutside;
+            const uint32_t k = f < nslab ? f * kSlab : 0;
+            const uint32_t d = lds0 + to * STAGE + wave * 1024;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = *reinterpret_cast<const u32x4*>(rdw + o + i * 16 * kSlab);
+            for (int j = 0; j < JF; ++j) {
+                if constexpr (decltype(fetches)::value) {
 #pragma unroll
-            for (int j = 0; j < JF; ++j)
-                x[j] = *reinterpret_cast<const u32x4*>(rdx + o + j * 16 * kSlab);
-        };
-        auto multiply = [&](const u32x4 (&x)[JF], const u32x4 (&w)[4]) {
+                    for (int i = j * FETCH / JF; i < (j + 1) * FETCH / JF; ++i) {
+                        if (i < FX) load_to_lds(rx, d + i * 8192, vx[i < FX ? i : 0] | none, k);
+                        else load_to_lds(rw, d + SLAB_X + (i - FX) * 8192, vw[i < FX ? 0 : i - FX] | none, k);
+                    }
+                }
 #pragma unroll
-            for (int j = 0; j < JF; ++j)
+                for (int i = j * 4 / JF; i < (j + 1) * 4 / JF; ++i)
+                    nwf[i] = *reinterpret_cast<const u32x4*>(rdw + o + i * 16 * kSlab);
+                nx[j] = *reinterpret_cast<const u32x4*>(rdx + o + j * 16 * kSlab);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[i][j] = mma_bf16(w[i], x[j], acc[i][j]);
-        };
-        // the reads of the half after, one to every one or two products
-        auto spread = [&]() {
-#pragma unroll
-            for (int i = 0; i < 4 + JF; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);              // LDS read
-                __builtin_amdgcn_sched_group_barrier(0x008, JF > 4 ? 2 : 1, 0);   // MFMA
+                __builtin_amdgcn_sched_barrier(0);
             }
         };
         fetch(ST - 1, ST - 1);
         wait_and_barrier<(ST - 1) * FETCH>();
-        read(0, 0, fx[0], fw[0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            fw[0][i] = *reinterpret_cast<const u32x4*>(rdw + rd + i * 16 * kSlab);
+#pragma unroll
+        for (int j = 0; j < JF; ++j)
+            fx[0][j] = *reinterpret_cast<const u32x4*>(rdx + rd + j * 16 * kSlab);
         int now = 0, next = 1;                    // stages of slabs s and s + 1
         for (int s = 0; s < nslab; ++s) {
-            read(now, 1, fx[1], fw[1]);
-            multiply(fx[0], fw[0]);
-            spread();
+            step(fx[0], fw[0], now, 1, fx[1], fw[1], std::false_type{}, 0, 0);
             // slab s is read; slab s + 1 has arrived
             wait_and_barrier<(ST - 2) * FETCH>();
-            fetch(s + ST, now);
-            read(next, 0, fx[0], fw[0]);
-            multiply(fx[1], fw[1]);
-            spread();
-            __builtin_amdgcn_sched_barrier(0);
+            step(fx[1], fw[1], next, 0, fx[0], fw[0], std::true_type{}, s + ST, now);
             now = next;
             next = next + 1 < ST ? next + 1 : 0;
         }
@@ -473,7 +484,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
             auto frag = [&](const uint8_t* p) {
                 Frag f;
                 f.v[0] = *reinterpret_cast<const u32x4*>(p + o);
-                f.v[1] = *reinterpret_cast<const u32x4*>(p + (o ^ 16));
+                f.v[1] = *reinterpret_cast<const u32x4*>(p + (o ^ 64));
                 return f;
             };
             auto scale = [&](int i, int j, f32x4 t, float sx) {
@@ -641,36 +652,35 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
 
 // ---------------------------------------------------------------------
 // The work list. A group's rows are cut into runs of 256; what is left into
-// 128, 64 and, up to small_to rows, small tiles. Tiles are dealt out largest
-// first. With few tiles in all, runs are 64 rows (see make_plan).
+// runs of 128 and 64 rows and, up to small_to rows, small tiles. One block per
+// CU works through its share, which every block computes for itself from the
+// counts (there is no queue, so nothing to clear and no order left to chance).
 // ---------------------------------------------------------------------
-constexpr int kKinds = 4;                        // 256, 128, 64 rows, small
+constexpr int kKinds = 4;                        // runs of 256, 128, 64 rows, small
+constexpr int kGrid = 256;                       // blocks of the big kernel
+constexpr int kGroup = 8;                        // runs of 256 rows side by side
 
 struct Plan {
     int32_t pre[kKinds][MOE_EP_MAX_LOCAL_EXPERTS + 1];   // tiles in front of a group
+    // shares: whole rounds of 256-row tiles, then of the rest this block's
+    // tiles of 256 rows (0 or 1), and its runs of the 128-row and 64-row tiles
+    int32_t rounds, big, half0, halves, quarter0, quarters, small_to;
 };
 
 struct Cut {
     int n[kKinds];                               // runs of rows of each kind
 };
 
-__device__ __forceinline__ Cut cut_rows(int rows, int largest, int small_to) {
+__device__ __forceinline__ Cut cut_rows(int rows, int small_to) {
     Cut c = {};
-    if (largest == 0) {
-        c.n[3] = (rows + kSmall - 1) / kSmall;
-        return c;
-    }
-    int r = rows;
-    if (largest == 256) {
-        c.n[0] = r / 256;
-        r %= 256;
-        if (r > 192) {
-            ++c.n[0];
-            r = 0;
-        } else if (r > 64) {
-            c.n[1] = 1;
-            r = r > 128 ? r - 128 : 0;
-        }
+    c.n[0] = rows / 256;
+    int r = rows % 256;
+    if (r > 192) {
+        ++c.n[0];
+        r = 0;
+    } else if (r > 64 + small_to) {
+        c.n[1] = 1;
+        r = r > 128 ? r - 128 : 0;
     }
     c.n[2] = r / 64;
     r %= 64;
@@ -679,36 +689,29 @@ __device__ __forceinline__ Cut cut_rows(int rows, int largest, int small_to) {
     return c;
 }
 
-// Returns the largest run. Runs of 256 rows leave most of the chip idle when
-// there are fewer than half as many tiles as CUs; 64-row runs then spread the
-// weights' loads over more of it (two runs of an expert read the same weights
-// at the same time, from one L2).
-__device__ __forceinline__ int make_plan(const MatmulArgs& a, int largest, int small_to,
-                                         int nt_big, int nt_small, int cus, Plan* p) {
-    __shared__ int32_t chosen;
-    if (threadIdx.x < 64) {
-        for (;;) {
-            int32_t run[kKinds] = {};
-            for (int g0 = 0; g0 < a.groups; g0 += 64) {
-                const int g = g0 + (int)threadIdx.x;
-                Cut c = {};
-                if (g < a.groups) c = cut_rows(group_rows(a, g), largest, small_to);
+// Tile counts of each kind, and the tiles in front of each group (a wave).
+__device__ __forceinline__ void count_tiles(const MatmulArgs& a, int small_to, int nt_big,
+                                            int nt_small, Plan* p, int (&total)[kKinds]) {
 #pragma unroll
-                for (int k = 0; k < kKinds; ++k) {
-                    const int32_t t = c.n[k] * (k == 3 ? nt_small : nt_big);
-                    const int32_t inc = wave_inclusive_scan(t);
-                    if (g < a.groups) p->pre[k][g] = run[k] + inc - t;
-                    run[k] += __shfl(inc, 63, 64);
-                }
-            }
-            if (threadIdx.x < kKinds) p->pre[threadIdx.x][a.groups] = run[threadIdx.x];
-            if (largest != 256 || run[0] + run[1] + run[2] > cus / 2) break;
-            largest = 64;
+    for (int k = 0; k < kKinds; ++k) total[k] = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += 64) {
+        const int g = g0 + (int)threadIdx.x;
+        Cut c = {};
+        if (g < a.groups) c = cut_rows(group_rows(a, g), small_to);
+#pragma unroll
+        for (int k = 0; k < kKinds; ++k) {
+            const int32_t t = c.n[k] * (k == 3 ? nt_small : nt_big);
+            const int32_t inc = wave_inclusive_scan(t);
+            if (g < a.groups) p->pre[k][g] = total[k] + inc - t;
+            total[k] += __shfl(inc, 63, 64);
         }
-        if (threadIdx.x == 0) chosen = largest;
     }
-    __syncthreads();
-    return uniform(chosen);
+    if (threadIdx.x < kKinds) {
+        int32_t v = 0;
+#pragma unroll
+        for (int k = 0; k < kKinds; ++k) v = (int)threadIdx.x == k ? total[k] : v;
+        p->pre[threadIdx.x][a.groups] = v;
+    }
 }
 
 // Tile of block b in a round of `left` tiles over the grid, -1 for none.
@@ -722,53 +725,201 @@ __device__ __forceinline__ int tile_of(int b, int grid, int left) {
     return slot < per && t < r ? t : -1;
 }
 
-template <int EB, bool WIDE, bool GATED, bool BIG>
-__global__ __launch_bounds__(kThreads, BIG ? 2 : 4) void matmul_kernel(const MatmulArgs a,
-                                                                       int small_to) {
-    __shared__ __align__(1024) uint8_t
-        lds[BIG ? kBigLds + (EB == 1 ? kScaleLds : 0) : kSmallLds];
+// The block's share. Rounds of 256-row tiles come first, one per block. What
+// is left, in units of a 64-row tile, would fill `high` units of each block: it
+// is laid out in columns of that height, largest tiles first. With less than a
+// 256-row tile's height the 256-row tiles left are cut in two, with a single
+// unit everything is cut into 64-row tiles (and these are spread over the
+// XCDs): 3.5 rounds then take 3.5 tiles' time and not 4, and a few rows an
+// expert, bound by the weights' bytes, are read by all CUs.
+__device__ __forceinline__ void make_plan(const MatmulArgs& a, int small_to, int nt_big,
+                                          int nt_small, int pos, Plan* p) {
+    if (threadIdx.x < 64) {
+        int n[kKinds];
+        count_tiles(a, small_to, nt_big, nt_small, p, n);
+        auto units = [&]() { return 4 * (n[0] % kGrid) + 2 * n[1] + n[2]; };
+        if (small_to && n[0] * 4 + n[1] * 2 + n[2] > kGrid) {
+            // small tiles beside so much else cost more than part-filled ones
+            small_to = 0;
+            count_tiles(a, 0, nt_big, nt_small, p, n);
+        }
+        const int u = units();
+        int high = (u + kGrid - 1) / kGrid;
+        int big = n[0] % kGrid, half = n[1], quarter = n[2];
+        if (high == 1) {
+            quarter += 2 * half + 4 * big;
+            big = half = 0;
+        } else if (high < 4) {
+            half += 2 * big;
+            big = 0;
+        }
+        // a column holds high / 2 halves, beside a 256-row tile (high - 4) / 2
+        while ((kGrid - big) * (high / 2) + big * (high >= 4 ? (high - 4) / 2 : 0) < half) ++high;
+        const int hc = high / 2, hb = high >= 4 ? (high - 4) / 2 : 0;
+        const int over = half - (kGrid - big) * hc;
+        int h0[4], hn[4], rem[4], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = (int)threadIdx.x * 4 + i;
+            const bool b = c < big;
+            const int at = b ? c * hb : (c - big) * hc;
+            const int most = b ? hb : hc;
+            int m = (b ? over : half) - at;
+            m = m < 0 ? 0 : m > most ? most : m;
+            h0[i] = (b ? (kGrid - big) * hc : 0) + at;
+            hn[i] = m;
+            rem[i] = high - (b ? 4 : 0) - 2 * m;
+            sum += rem[i];
+        }
+        int q = wave_inclusive_scan(sum) - sum;
+        if ((int)threadIdx.x == pos / 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i == pos % 4) {
+                    p->rounds = n[0] / kGrid;
+                    p->big = pos < big ? 1 : 0;
+                    p->half0 = h0[i];
+                    p->halves = hn[i];
+                    const int left = quarter - q;
+                    p->quarter0 = q;
+                    p->quarters = left < 0 ? 0 : left > rem[i] ? rem[i] : left;
+                    p->small_to = small_to;
+                }
+                q += rem[i];
+            }
+            if (high == 1) {
+                const int t = tile_of(blockIdx.x, kGrid, quarter);
+                p->quarter0 = t;
+                p->quarters = t < 0 ? 0 : 1;
+            }
+        }
+    }
+    __syncthreads();
+}
+
+template <int EB, bool WIDE, bool GATED>
+__global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a, int small_to_) {
+    __shared__ __align__(1024) uint8_t lds[kBigLds + (EB == 1 ? kScaleLds : 0)];
     __shared__ Plan p;
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
     constexpr int BB = GATED ? kBig / 2 : kBig;
     const int nt = (a.N + BO - 1) / BO, ntb = (a.N + BB - 1) / BB;
-    const int largest = make_plan(a, BIG ? 256 : 0, small_to, ntb, nt, gridDim.x, &p);
-    int total = 0;
-#pragma unroll
-    for (int k = BIG ? 0 : 3; k < kKinds; ++k) total += uniform(p.pre[k][a.groups]);
-    for (int t0 = 0; t0 < total; t0 += gridDim.x) {
-        int t = tile_of(blockIdx.x, gridDim.x, total - t0);
-        if (t < 0) break;       // a last, partial round
-        t += t0;
-        int kind = BIG ? 0 : 3;
-        while (kind < 3 && t >= uniform(p.pre[kind][a.groups]))
-            t -= uniform(p.pre[kind++][a.groups]);
-        const int g = uniform(find_source(p.pre[kind], a.groups, t));
-        const int rows = uniform(group_rows(a, g));
-        const Cut c = cut_rows(rows, largest, small_to);
-        const int l = t - uniform(p.pre[kind][g]);
-        if (kind == 3) {
-            const int from = c.n[0] * 256 + c.n[1] * 128 + c.n[2] * 64;
-            const int mt = c.n[3];
-            small_tile<EB, WIDE, GATED>(a, g, from + l % mt * kSmall, rows, l / mt * BO,
-                                        reinterpret_cast<float*>(lds));
-            continue;
-        }
-        if constexpr (BIG) {
-            if (kind == 0) {
-                // eight runs of rows at a time, over all columns
-                const int m8 = l / (8 * ntb) * 8;
-                const int wide = c.n[0] - m8 < 8 ? c.n[0] - m8 : 8;
-                const int in = l - m8 * ntb;
-                big_tile<EB, WIDE, GATED, 256>(a, g, (m8 + in % wide) * 256, rows, in / wide * BB,
-                                               lds);
-            } else if (kind == 1) {
-                big_tile<EB, WIDE, GATED, 128>(a, g, c.n[0] * 256, rows, l * BB, lds);
-            } else {
-                const int from = c.n[0] * 256 + c.n[1] * 128;
-                big_tile<EB, WIDE, GATED, 64>(a, g, from + l % c.n[2] * 64, rows,
-                                              l / c.n[2] * BB, lds);
+    // blocks go to the eight XCDs in turn: neighbouring tiles, which share rows
+    // of x and w, to the blocks of one XCD (with an L2 of its own)
+    const int pos = (blockIdx.x & 7) * (kGrid / 8) + (blockIdx.x >> 3);
+    make_plan(a, small_to_, ntb, nt, pos, &p);
+    const int small_to = uniform(p.small_to);
+    const int rounds = uniform(p.rounds), big = uniform(p.big);
+    const int halves = uniform(p.halves), quarters = uniform(p.quarters);
+    const int nbig = uniform(p.pre[0][a.groups]), nhalf = uniform(p.pre[1][a.groups]);
+    const int nquarter = uniform(p.pre[2][a.groups]), nsmall = uniform(p.pre[3][a.groups]);
+    const int whole = nbig / kGrid * kGrid;       // tiles of whole rounds
+    const int items = rounds + big + halves + quarters;
+    for (int i = 0; i < items; ++i) {
+        int kind, t, from = 0, sub = 0;          // a tile of kind `from`, its part `sub`
+        int l = i - rounds;
+        if (l < big) {
+            kind = 0;
+            t = l < 0 ? i * kGrid + pos : whole + pos;
+        } else if ((l -= big) < halves) {
+            kind = from = 1;
+            t = uniform(p.half0) + l;
+            if (t >= nhalf) {
+                from = 0;
+                sub = (t - nhalf) % 2;
+                t = whole + (t - nhalf) / 2;
+            }
+        } else {
+            kind = from = 2;
+            t = uniform(p.quarter0) + l - halves;
+            if (t >= nquarter + 2 * nhalf) {
+                from = 0;
+                t -= nquarter + 2 * nhalf;
+                sub = t % 4;
+                t = whole + t / 4;
+            } else if (t >= nquarter) {
+                from = 1;
+                t -= nquarter;
+                sub = t % 2;
+                t /= 2;
             }
         }
+        const int g = uniform(find_source(p.pre[from], a.groups, t));
+        const int rows = uniform(group_rows(a, g));
+        const Cut c = cut_rows(rows, small_to);
+        l = t - uniform(p.pre[from][g]);
+        int m0, n0;
+        if (from == 0) {
+            // kGroup runs of rows at a time, over all columns
+            const int m8 = l / (kGroup * ntb) * kGroup;
+            const int wide = c.n[0] - m8 < kGroup ? c.n[0] - m8 : kGroup;
+            const int in = l - m8 * ntb;
+            m0 = (m8 + in % wide) * 256;
+            n0 = in / wide;
+        } else if (from == 1) {
+            m0 = c.n[0] * 256;
+            n0 = l;
+        } else {
+            m0 = c.n[0] * 256 + c.n[1] * 128 + l % c.n[2] * 64;
+            n0 = l / c.n[2];
+        }
+        n0 *= BB;
+        m0 += sub * (kind == 1 ? 128 : 64);
+        if (kind == 0) big_tile<EB, WIDE, GATED, 256>(a, g, m0, rows, n0, lds);
+        else if (kind == 1) big_tile<EB, WIDE, GATED, 128>(a, g, m0, rows, n0, lds);
+        else big_tile<EB, WIDE, GATED, 64>(a, g, m0, rows, n0, lds);
+    }
+    for (int t0 = 0; t0 < nsmall; t0 += kGrid) {
+        int t = tile_of(blockIdx.x, kGrid, nsmall - t0);
+        if (t < 0) break;       // a last, partial round
+        t += t0;
+        const int g = uniform(find_source(p.pre[3], a.groups, t));
+        const int rows = uniform(group_rows(a, g));
+        const Cut c = cut_rows(rows, small_to);
+        const int l = t - uniform(p.pre[3][g]);
+        const int from = c.n[0] * 256 + c.n[1] * 128 + c.n[2] * 64;
+        small_tile<EB, WIDE, GATED, kWaves>(a, g, from + l % c.n[3] * kSmall, rows,
+                                            l / c.n[3] * BO, reinterpret_cast<float*>(lds));
+    }
+}
+
+// Small tiles alone, where the host knows that there are few rows.
+template <int EB, bool WIDE, bool GATED, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 4) void small_kernel(const MatmulArgs a) {
+    __shared__ __align__(16) uint8_t lds[kSmallLds<WAVES>];
+    __shared__ int32_t pre[MOE_EP_MAX_LOCAL_EXPERTS + 1];
+    constexpr int BO = GATED ? kSmall / 2 : kSmall;
+    const int nt = (a.N + BO - 1) / BO;
+    int total = (a.rows + kSmall - 1) / kSmall * nt;
+    if (a.counts) {
+        if (threadIdx.x < 64) {
+            int32_t run = 0;
+            for (int g0 = 0; g0 < a.groups; g0 += 64) {
+                const int g = g0 + (int)threadIdx.x;
+                const int32_t t =
+                    g < a.groups ? (group_rows(a, g) + kSmall - 1) / kSmall * nt : 0;
+                const int32_t inc = wave_inclusive_scan(t);
+                if (g < a.groups) pre[g] = run + inc - t;
+                run += __shfl(inc, 63, 64);
+            }
+            if (threadIdx.x == 0) pre[a.groups] = run;
+        }
+        __syncthreads();
+        total = uniform(pre[a.groups]);
+    }
+    for (int t0 = 0; t0 < total; t0 += gridDim.x) {
+        int l = tile_of(blockIdx.x, gridDim.x, total - t0);
+        if (l < 0) break;       // a last, partial round
+        l += t0;
+        int g = 0, rows = a.rows;
+        if (a.counts) {
+            g = uniform(find_source(pre, a.groups, l));
+            rows = uniform(group_rows(a, g));
+            l -= uniform(pre[g]);
+        }
+        const int mt = (rows + kSmall - 1) / kSmall;
+        small_tile<EB, WIDE, GATED, WAVES>(a, g, l % mt * kSmall, rows, l / mt * BO,
+                                           reinterpret_cast<float*>(lds));
     }
 }
 
@@ -781,13 +932,15 @@ hipError_t launch(const MatmulArgs& a, hipStream_t st) {
     const int64_t runs = (int64_t)a.groups * ((a.rows + 63) / 64) * ((a.N + BB - 1) / BB);
     const bool e4m3 = a.out_dtype == MOE_EP_E4M3;
     const bool few = !e4m3 && (a.counts ? a.rows <= 2 * kSmall : a.rows <= kSmall || runs < 64);
-    if (few) {
-        const int64_t grid = small < 512 ? (small + 7) / 8 * 8 : 512;
-        matmul_kernel<EB, WIDE, GATED, false>
-            <<<(unsigned)grid, kThreads, 0, st>>>(a, a.rows);
+    if (!few) {
+        matmul_kernel<EB, WIDE, GATED>
+            <<<kGrid, kThreads, 0, st>>>(a, e4m3 || !a.counts ? 0 : kSmall);
+    } else if (small <= 256) {
+        // a block of sixteen waves per CU reads a tile in half the steps
+        small_kernel<EB, WIDE, GATED, 16><<<(unsigned)((small + 7) / 8 * 8), 1024, 0, st>>>(a);
     } else {
-        matmul_kernel<EB, WIDE, GATED, true>
-            <<<256, kThreads, 0, st>>>(a, e4m3 ? 0 : kSmall);
+        const int64_t grid = small < 512 ? (small + 7) / 8 * 8 : 512;
+        small_kernel<EB, WIDE, GATED, 8><<<(unsigned)grid, 512, 0, st>>>(a);
     }
     return hipGetLastError();
 }
