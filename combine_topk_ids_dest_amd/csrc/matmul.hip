@@ -80,14 +80,20 @@ __device__ __forceinline__ f32x4 mma_wide(const Wide& w, const Wide& x, f32x4 ac
     return acc;
 }
 
+// v * sigmoid(v). The hardware's reciprocal is within an ulp; a division would
+// be most of an epilogue's instructions.
+__device__ __forceinline__ float silu(float v) {
+    return v * __builtin_amdgcn_rcpf(1.0f + expf(-v));
+}
+
 __device__ __forceinline__ float apply_act(float v, int act) {
-    if (act == MOE_EP_ACT_SILU) return v / (1.0f + expf(-v));
+    if (act == MOE_EP_ACT_SILU) return silu(v);
     if (act == MOE_EP_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
     return v;
 }
 
 __device__ __forceinline__ float silu_gated(float gate, float up) {
-    return gate / (1.0f + expf(-gate)) * up;
+    return silu(gate) * up;
 }
 
 __device__ __forceinline__ u32x2 pack_bf16(f32x4 v) {
@@ -149,7 +155,9 @@ __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, i
                              (int64_t)(left - 1) * a.x_row + kb);
     const auto rw = row_rsrc(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
     const int r = lane & 15;
-    const uint32_t kin = (uint32_t)(lane >> 4) * 32u;
+    // lane l has the chunks l / 16 and l / 16 + 4 of a slab: a load takes 64
+    // consecutive bytes of each of 16 rows
+    const uint32_t kin = (uint32_t)(lane >> 4) * 16u;
     const uint32_t vx = r < left ? (uint32_t)r * (uint32_t)a.x_row : kOutside;
     const int wn = GATED ? n0 + (r & 7) : n0 + r;
     const uint32_t vw =
@@ -173,7 +181,7 @@ __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, i
         const uint32_t k0 = (uint32_t)s * kSlab + kin;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t k = k0 + 16 * h;
+            const uint32_t k = k0 + 64 * h;
             const bool in = k < (uint32_t)kb;
             fw[d].v[h] = ld_row_buf<false>(rw, in ? vw + k : kOutside);
             fx[d].v[h] = ld_row_buf<false>(rx, in ? vx + k : kOutside);
@@ -238,7 +246,7 @@ __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, i
 // Big tiles: BM (256, 128 or 64) rows of x by 256 rows of w. Eight waves in
 // two rows of four, each with BM / 2 x 64 of the sums in registers. Slabs of
 // 128 bytes of k go from memory straight into LDS (no register is spent on a
-// load in flight), STAGES - 1 slabs ahead of the one being multiplied.
+// load in flight), one to three slabs ahead of the one being multiplied.
 //
 // LDS: row r of a slab holds its eight 16-byte chunks with chunk c at place
 // c ^ ((r >> 1) & 7), and lane l of a fragment takes the chunks l / 16 and
@@ -254,11 +262,18 @@ __device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, i
 // ---------------------------------------------------------------------
 constexpr int kBig = 256;                        // rows of w
 constexpr int kBigSlab = kBig * kSlab;
-constexpr int kBigLds = 4 * kBigSlab;            // two slabs of 256 + 256 rows
-constexpr int kScaleLds = 2 * (kBig * 16 + 256); // two sets of scales of four slabs
+constexpr int kLds = 160 << 10;                  // all of a CU's
+constexpr int kScaleLds = 2 * (kBig * 16 + 256); // fp8: two sets of scales of four slabs
+constexpr int kScaleAt = kLds - kScaleLds;
 
-template <int BM>
-constexpr int kStages = BM == 256 || BM == 128 ? 2 : 3;
+// Slabs of x and of w in LDS: as many as fit. Weights of experts come from
+// HBM, x more often from L2, so where one of the two can be deeper it is w.
+// (256 rows: with two slabs of each, a slab's time is below HBM's loaded
+// latency of about 2 us, and the products wait for the weights.)
+template <int EB, int BM>
+constexpr int kStagesX = EB == 2 ? (BM == 256 ? 2 : BM == 128 ? 3 : 4) : (BM == 256 ? 2 : 3);
+template <int EB, int BM>
+constexpr int kStagesW = EB == 2 ? (BM == 64 ? 4 : 3) : (BM == 256 ? 2 : 3);
 
 // Row of w behind row r of a tile whose first output column is n0, and its
 // output column n (columns n >= N do not exist). A fragment's row 4 q + t
@@ -329,12 +344,12 @@ template <int EB, bool WIDE, bool GATED, int BM>
 __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
                                          uint8_t* lds) {
     constexpr int JF = BM / 32;                   // fragments of x of a wave
-    constexpr int ST = kStages<BM>;
+    constexpr int XS = kStagesX<EB, BM>, WS = kStagesW<EB, BM>;
     constexpr int SLAB_X = BM * kSlab;
-    constexpr int STAGE = SLAB_X + kBigSlab;
+    constexpr int AT_W = XS * SLAB_X;             // slabs of w behind those of x
     constexpr int FX = BM / 64;                   // loads of x of a wave and slab
     constexpr int FETCH = FX + 4;
-    static_assert(ST * STAGE <= kBigLds, "");
+    static_assert(XS <= WS && AT_W + WS * kBigSlab <= (EB == 1 ? kScaleAt : kLds), "");
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
@@ -362,14 +377,13 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
     // the last slab may be short: its chunks past the end of k load zeros, and
     // so do slabs past the last
     const int last = (kb - chunk * 16 + kSlab - 1) / kSlab;
-    auto fetch = [&](int s, int stage) {
-        const uint32_t none = s < last ? 0u : kOutside;
-        const uint32_t k = s < nslab ? s * kSlab : 0;   // stays within the range
-        const uint32_t d = lds0 + stage * STAGE + wave * 1024;
-#pragma unroll
-        for (int i = 0; i < FX; ++i) load_to_lds(rx, d + i * 8192, vx[i] | none, k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) load_to_lds(rw, d + SLAB_X + i * 8192, vw[i] | none, k);
+    auto fetch_x = [&](int i, int s, int stage) {
+        load_to_lds(rx, lds0 + stage * SLAB_X + wave * 1024 + i * 8192,
+                    vx[i] | (s < last ? 0u : kOutside), s < nslab ? s * kSlab : 0);
+    };
+    auto fetch_w = [&](int i, int s, int stage) {
+        load_to_lds(rw, lds0 + AT_W + stage * kBigSlab + wave * 1024 + i * 8192,
+                    vw[i] | (s < last ? 0u : kOutside), s < nslab ? s * kSlab : 0);
     };
 
     // fp8: the scales of four slabs at a time, 16 bytes per row of x, and 4
@@ -393,7 +407,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
         rws = row_rsrc4(reinterpret_cast<const uint8_t*>(a.ws + g * a.ws_stride),
                         (int64_t)(GATED ? 2 : 1) * per * nslab * 4);
     }
-    const uint32_t scales0 = lds0 + kBigLds;
+    const uint32_t scales0 = lds0 + kScaleAt;
     auto fetch_scales = [&](int s) {              // s a multiple of 4
         const uint32_t d = scales0 + ((s >> 2) & 1) * SCALES;
         const uint32_t none = s < nslab ? 0u : kOutside;
@@ -405,88 +419,100 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
 
     const int rd = (lane & 15) * kSlab + (((lane >> 4) ^ ((lane >> 1) & 7)) * 16);
     const uint8_t* rdx = lds + wm * (BM / 2) * kSlab;
-    const uint8_t* rdw = lds + SLAB_X + wn * 64 * kSlab;
+    const uint8_t* rdw = lds + AT_W + wn * 64 * kSlab;
     f32x4 acc[4][JF];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < JF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    // The order of the loads is that of a loop started WS slabs early: step v
+    // loads slab v + XS of x, then slab v + WS of w.
     if constexpr (EB == 1) fetch_scales(0);
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s) fetch(s, s);
+    for (int v = -WS; v < (EB == 2 ? 0 : -1); ++v) {
+#pragma unroll
+        for (int i = 0; i < FX; ++i)
+            if (v + XS >= 0) fetch_x(i, v + XS, v + XS);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fetch_w(i, v + WS, v + WS);
+    }
+    // Loads behind those of slab s + 1 when step s waits for it.
+    constexpr int LEFT = (XS - 2) * FETCH + (WS > XS ? 4 : 0);
 
     if constexpr (EB == 2) {
         // Fragments are read half a slab ahead, so that the reads of one half
         // run under the products of the other.
         u32x4 fx[2][JF], fw[2][4];
-        // Multiplies one half while reading another, and with FETCHES loads
-        // slab f into its stage, all in small steps: a wave issues in order, so
-        // eight loads in a row would hold up the products behind them until the
-        // address unit has taken the loads of all eight waves.
-        auto step = [&](const u32x4 (&x)[JF], const u32x4 (&w)[4], int stage, int h,
-                        u32x4 (&nx)[JF], u32x4 (&nwf)[4], auto fetches, int f, int to) {
-            const int o = stage * STAGE + (rd ^ (h * 64));
-            const uint32_t none = f < last ? 0u : kOutside;
-            const uint32_t k = f < nslab ? f * kSlab : 0;
-            const uint32_t d = lds0 + to * STAGE + wave * 1024;
+        // Multiplies one half while reading half h of the slab at stages ix
+        // and iw, and with FETCHES does step f's loads, in small steps: a wave
+        // issues in order.
+        auto step = [&](const u32x4 (&x)[JF], const u32x4 (&w)[4], int ix, int iw, int h,
+                        u32x4 (&nx)[JF], u32x4 (&nwf)[4], auto fetches, int f, int tx, int tw) {
+            const int o = rd ^ (h * 64);
 #pragma unroll
             for (int j = 0; j < JF; ++j) {
                 if constexpr (decltype(fetches)::value) {
 #pragma unroll
                     for (int i = j * FETCH / JF; i < (j + 1) * FETCH / JF; ++i) {
-                        if (i < FX) load_to_lds(rx, d + i * 8192, vx[i < FX ? i : 0] | none, k);
-                        else load_to_lds(rw, d + SLAB_X + (i - FX) * 8192, vw[i < FX ? 0 : i - FX] | none, k);
+                        if (i < FX) fetch_x(i, f + XS, tx);
+                        else fetch_w(i - FX, f + WS, tw);
                     }
                 }
 #pragma unroll
                 for (int i = j * 4 / JF; i < (j + 1) * 4 / JF; ++i)
-                    nwf[i] = *reinterpret_cast<const u32x4*>(rdw + o + i * 16 * kSlab);
-                nx[j] = *reinterpret_cast<const u32x4*>(rdx + o + j * 16 * kSlab);
+                    nwf[i] = *reinterpret_cast<const u32x4*>(rdw + iw * kBigSlab + o + i * 16 * kSlab);
+                nx[j] = *reinterpret_cast<const u32x4*>(rdx + ix * SLAB_X + o + j * 16 * kSlab);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[i][j] = mma_bf16(w[i], x[j], acc[i][j]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        fetch(ST - 1, ST - 1);
-        wait_and_barrier<(ST - 1) * FETCH>();
+        wait_and_barrier<LEFT + FETCH>();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             fw[0][i] = *reinterpret_cast<const u32x4*>(rdw + rd + i * 16 * kSlab);
 #pragma unroll
         for (int j = 0; j < JF; ++j)
             fx[0][j] = *reinterpret_cast<const u32x4*>(rdx + rd + j * 16 * kSlab);
-        int now = 0, next = 1;                    // stages of slabs s and s + 1
+        int ix = 0, iw = 0;                       // stages of slab s
         for (int s = 0; s < nslab; ++s) {
-            step(fx[0], fw[0], now, 1, fx[1], fw[1], std::false_type{}, 0, 0);
+            step(fx[0], fw[0], ix, iw, 1, fx[1], fw[1], std::false_type{}, 0, 0, 0);
             // slab s is read; slab s + 1 has arrived
-            wait_and_barrier<(ST - 2) * FETCH>();
-            step(fx[1], fw[1], next, 0, fx[0], fw[0], std::true_type{}, s + ST, now);
-            now = next;
-            next = next + 1 < ST ? next + 1 : 0;
+            wait_and_barrier<LEFT>();
+            const int nix = ix + 1 < XS ? ix + 1 : 0, niw = iw + 1 < WS ? iw + 1 : 0;
+            step(fx[1], fw[1], nix, niw, 0, fx[0], fw[0], std::true_type{}, s, ix, iw);
+            ix = nix;
+            iw = niw;
         }
     } else {
         // Slab by slab: the sums of a slab are complete before they are
         // scaled, so the halves cannot be taken apart.
         const int bw = GATED ? 0 : wn >> 1;       // the wave's block (gated: both)
+        static_assert(XS == WS, "");
         int now = 0;
         for (int s = 0; s < nslab; ++s) {
             // slab s and its scales (older than the loads that may still be
             // in flight) have arrived; slab s - 1 is read
-            wait_and_barrier<(ST - 2) * FETCH>();
-            const int to = now == 0 ? ST - 1 : now - 1;
-            fetch(s + ST - 1, to);
+            wait_and_barrier<LEFT>();
+            const int to = now == 0 ? XS - 1 : now - 1;
+#pragma unroll
+            for (int i = 0; i < FX; ++i) fetch_x(i, s + XS - 1, to);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fetch_w(i, s + WS - 1, to);
             if ((s & 3) == 2) fetch_scales((s & ~3) + 4);
-            const float* sc = reinterpret_cast<const float*>(lds + kBigLds + ((s >> 2) & 1) * SCALES);
+            const float* sc =
+                reinterpret_cast<const float*>(lds + kScaleAt + ((s >> 2) & 1) * SCALES);
             const float sg = sc[kBig * 4 + bw * 4 + (s & 3)];
             const float su = GATED ? sc[kBig * 4 + 4 + (s & 3)] : sg;
-            const int o = now * STAGE + rd;
             auto frag = [&](const uint8_t* p) {
                 Frag f;
-                f.v[0] = *reinterpret_cast<const u32x4*>(p + o);
-                f.v[1] = *reinterpret_cast<const u32x4*>(p + (o ^ 64));
+                f.v[0] = *reinterpret_cast<const u32x4*>(p + rd);
+                f.v[1] = *reinterpret_cast<const u32x4*>(p + (rd ^ 64));
                 return f;
             };
+            const uint8_t* px = rdx + now * SLAB_X;
+            const uint8_t* pw = rdw + now * kBigSlab;
             auto scale = [&](int i, int j, f32x4 t, float sx) {
                 const float f = sx * (GATED && (i & 1) ? su : sg);
 #pragma unroll
@@ -496,10 +522,10 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
             if constexpr (WIDE) {
                 Wide w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = widen(frag(rdw + i * 16 * kSlab));
+                for (int i = 0; i < 4; ++i) w[i] = widen(frag(pw + i * 16 * kSlab));
 #pragma unroll
                 for (int j = 0; j < JF; ++j) {
-                    const Wide x = widen(frag(rdx + j * 16 * kSlab));
+                    const Wide x = widen(frag(px + j * 16 * kSlab));
                     const float sx = sc[(wm * (BM / 2) + j * 16 + (lane & 15)) * 4 + (s & 3)];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) scale(i, j, mma_wide(w[i], x, zero), sx);
@@ -507,16 +533,16 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
             } else {
                 Frag w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = frag(rdw + i * 16 * kSlab);
+                for (int i = 0; i < 4; ++i) w[i] = frag(pw + i * 16 * kSlab);
 #pragma unroll
                 for (int j = 0; j < JF; ++j) {
-                    const Frag x = frag(rdx + j * 16 * kSlab);
+                    const Frag x = frag(px + j * 16 * kSlab);
                     const float sx = sc[(wm * (BM / 2) + j * 16 + (lane & 15)) * 4 + (s & 3)];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) scale(i, j, mma_fp8(w[i], x, zero), sx);
                 }
             }
-            now = now + 1 < ST ? now + 1 : 0;
+            now = now + 1 < XS ? now + 1 : 0;
         }
     }
     wait_and_barrier<0>();   // LDS is free for what follows
@@ -661,10 +687,11 @@ constexpr int kGrid = 256;                       // blocks of the big kernel
 constexpr int kGroup = 8;                        // runs of 256 rows side by side
 
 struct Plan {
-    int32_t pre[kKinds][MOE_EP_MAX_LOCAL_EXPERTS + 1];   // tiles in front of a group
-    // shares: whole rounds of 256-row tiles, then of the rest this block's
-    // tiles of 256 rows (0 or 1), and its runs of the 128-row and 64-row tiles
-    int32_t rounds, big, half0, halves, quarter0, quarters, small_to;
+    int total[kKinds];                           // tiles of each kind
+    int small_to;
+    // whole rounds of 256-row tiles, then of the rest this block's tiles of
+    // 256 rows (0 or 1), and its runs of the 128-row and 64-row tiles
+    int rounds, big, half0, halves, quarter0, quarters;
 };
 
 struct Cut {
@@ -689,28 +716,50 @@ __device__ __forceinline__ Cut cut_rows(int rows, int small_to) {
     return c;
 }
 
-// Tile counts of each kind, and the tiles in front of each group (a wave).
-__device__ __forceinline__ void count_tiles(const MatmulArgs& a, int small_to, int nt_big,
-                                            int nt_small, Plan* p, int (&total)[kKinds]) {
+// The rows of the groups g0 + lane (0 past the last).
+__device__ __forceinline__ int lane_rows(const MatmulArgs& a, int g0) {
+    const int g = g0 + (int)(threadIdx.x & 63);
+    return g < a.groups ? group_rows(a, g) : 0;
+}
+
+// Everything here is done by each wave for itself, with no LDS (the tiles take
+// all of it): a group to a lane, 64 groups at a time. rows0: lane_rows(a, 0).
+__device__ __forceinline__ void count_tiles(const MatmulArgs& a, int rows0, int small_to,
+                                            int nt_big, int nt_small, int (&total)[kKinds]) {
 #pragma unroll
     for (int k = 0; k < kKinds; ++k) total[k] = 0;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
-        const int g = g0 + (int)threadIdx.x;
-        Cut c = {};
-        if (g < a.groups) c = cut_rows(group_rows(a, g), small_to);
+        const Cut c = cut_rows(g0 ? lane_rows(a, g0) : rows0, small_to);
 #pragma unroll
         for (int k = 0; k < kKinds; ++k) {
-            const int32_t t = c.n[k] * (k == 3 ? nt_small : nt_big);
-            const int32_t inc = wave_inclusive_scan(t);
-            if (g < a.groups) p->pre[k][g] = total[k] + inc - t;
-            total[k] += __shfl(inc, 63, 64);
+            const int32_t inc = wave_inclusive_scan(c.n[k] * (k == 3 ? nt_small : nt_big));
+            total[k] += __builtin_amdgcn_readlane(inc, 63);
         }
     }
-    if (threadIdx.x < kKinds) {
-        int32_t v = 0;
-#pragma unroll
-        for (int k = 0; k < kKinds; ++k) v = (int)threadIdx.x == k ? total[k] : v;
-        p->pre[threadIdx.x][a.groups] = v;
+}
+
+// The group of tile t of a kind, its rows and the tile's number in it.
+struct Place {
+    int g, rows, l;
+};
+
+__device__ __forceinline__ Place find_tile(const MatmulArgs& a, int rows0, int small_to, int kind,
+                                           int nt, int t) {
+    for (int g0 = 0;; g0 += 64) {
+        const int rows = g0 ? lane_rows(a, g0) : rows0;
+        const Cut c = cut_rows(rows, small_to);
+        const int n = nt * (kind == 0 ? c.n[0] : kind == 1 ? c.n[1] : kind == 2 ? c.n[2] : c.n[3]);
+        const int32_t inc = wave_inclusive_scan(n);
+        const uint64_t behind = __ballot(inc > t);
+        if (behind || g0 + 64 >= a.groups) {     // t is below the total: a lane is found
+            const int lane = behind ? __builtin_ctzll(behind) : 0;
+            Place p;
+            p.g = uniform(g0 + lane);
+            p.rows = __builtin_amdgcn_readlane(rows, lane);
+            p.l = t - (__builtin_amdgcn_readlane(inc, lane) - __builtin_amdgcn_readlane(n, lane));
+            return p;
+        }
+        t -= __builtin_amdgcn_readlane(inc, 63);
     }
 }
 
@@ -732,87 +781,82 @@ __device__ __forceinline__ int tile_of(int b, int grid, int left) {
 // unit everything is cut into 64-row tiles (and these are spread over the
 // XCDs): 3.5 rounds then take 3.5 tiles' time and not 4, and a few rows an
 // expert, bound by the weights' bytes, are read by all CUs.
-__device__ __forceinline__ void make_plan(const MatmulArgs& a, int small_to, int nt_big,
-                                          int nt_small, int pos, Plan* p) {
-    if (threadIdx.x < 64) {
-        int n[kKinds];
-        count_tiles(a, small_to, nt_big, nt_small, p, n);
-        auto units = [&]() { return 4 * (n[0] % kGrid) + 2 * n[1] + n[2]; };
-        if (small_to && n[0] * 4 + n[1] * 2 + n[2] > kGrid) {
-            // small tiles beside so much else cost more than part-filled ones
-            small_to = 0;
-            count_tiles(a, 0, nt_big, nt_small, p, n);
-        }
-        const int u = units();
-        int high = (u + kGrid - 1) / kGrid;
-        int big = n[0] % kGrid, half = n[1], quarter = n[2];
-        if (high == 1) {
-            quarter += 2 * half + 4 * big;
-            big = half = 0;
-        } else if (high < 4) {
-            half += 2 * big;
-            big = 0;
-        }
-        // a column holds high / 2 halves, beside a 256-row tile (high - 4) / 2
-        while ((kGrid - big) * (high / 2) + big * (high >= 4 ? (high - 4) / 2 : 0) < half) ++high;
-        const int hc = high / 2, hb = high >= 4 ? (high - 4) / 2 : 0;
-        const int over = half - (kGrid - big) * hc;
-        int h0[4], hn[4], rem[4], sum = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = (int)threadIdx.x * 4 + i;
-            const bool b = c < big;
-            const int at = b ? c * hb : (c - big) * hc;
-            const int most = b ? hb : hc;
-            int m = (b ? over : half) - at;
-            m = m < 0 ? 0 : m > most ? most : m;
-            h0[i] = (b ? (kGrid - big) * hc : 0) + at;
-            hn[i] = m;
-            rem[i] = high - (b ? 4 : 0) - 2 * m;
-            sum += rem[i];
-        }
-        int q = wave_inclusive_scan(sum) - sum;
-        if ((int)threadIdx.x == pos / 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i == pos % 4) {
-                    p->rounds = n[0] / kGrid;
-                    p->big = pos < big ? 1 : 0;
-                    p->half0 = h0[i];
-                    p->halves = hn[i];
-                    const int left = quarter - q;
-                    p->quarter0 = q;
-                    p->quarters = left < 0 ? 0 : left > rem[i] ? rem[i] : left;
-                    p->small_to = small_to;
-                }
-                q += rem[i];
-            }
-            if (high == 1) {
-                const int t = tile_of(blockIdx.x, kGrid, quarter);
-                p->quarter0 = t;
-                p->quarters = t < 0 ? 0 : 1;
-            }
-        }
+__device__ __forceinline__ Plan make_plan(const MatmulArgs& a, int rows0, int small_to, int nt_big,
+                                          int nt_small, int pos) {
+    Plan p;
+    int (&n)[kKinds] = p.total;
+    count_tiles(a, rows0, small_to, nt_big, nt_small, n);
+    if (small_to && n[0] * 4 + n[1] * 2 + n[2] > kGrid) {
+        // small tiles beside so much else cost more than part-filled ones
+        small_to = 0;
+        count_tiles(a, rows0, 0, nt_big, nt_small, n);
     }
-    __syncthreads();
+    p.small_to = small_to;
+    const int u = 4 * (n[0] % kGrid) + 2 * n[1] + n[2];
+    int high = (u + kGrid - 1) / kGrid;
+    int big = n[0] % kGrid, half = n[1], quarter = n[2];
+    if (high == 1) {
+        quarter += 2 * half + 4 * big;
+        big = half = 0;
+    } else if (high < 4) {
+        half += 2 * big;
+        big = 0;
+    }
+    // a column holds high / 2 halves, beside a 256-row tile (high - 4) / 2
+    while ((kGrid - big) * (high / 2) + big * (high >= 4 ? (high - 4) / 2 : 0) < half) ++high;
+    const int hc = high / 2, hb = high >= 4 ? (high - 4) / 2 : 0;
+    const int over = half - (kGrid - big) * hc;
+    int h0[4], hn[4], rem[4], sum = 0;           // four columns to a lane
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = (int)(threadIdx.x & 63) * 4 + i;
+        const bool b = c < big;
+        const int at = b ? c * hb : (c - big) * hc;
+        const int most = b ? hb : hc;
+        int m = (b ? over : half) - at;
+        m = m < 0 ? 0 : m > most ? most : m;
+        h0[i] = (b ? (kGrid - big) * hc : 0) + at;
+        hn[i] = m;
+        rem[i] = high - (b ? 4 : 0) - 2 * m;
+        sum += rem[i];
+    }
+    int q = wave_inclusive_scan(sum) - sum;
+    p.rounds = n[0] / kGrid;
+    p.big = pos < big ? 1 : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i == pos % 4) {
+            const int left = quarter - q;
+            p.half0 = __builtin_amdgcn_readlane(h0[i], pos / 4);
+            p.halves = __builtin_amdgcn_readlane(hn[i], pos / 4);
+            p.quarter0 = __builtin_amdgcn_readlane(q, pos / 4);
+            p.quarters = __builtin_amdgcn_readlane(left < 0 ? 0 : left > rem[i] ? rem[i] : left,
+                                                   pos / 4);
+        }
+        q += rem[i];
+    }
+    if (high == 1) {
+        const int t = tile_of(blockIdx.x, kGrid, quarter);
+        p.quarter0 = t;
+        p.quarters = t < 0 ? 0 : 1;
+    }
+    return p;
 }
 
 template <int EB, bool WIDE, bool GATED>
 __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a, int small_to_) {
-    __shared__ __align__(1024) uint8_t lds[kBigLds + (EB == 1 ? kScaleLds : 0)];
-    __shared__ Plan p;
+    __shared__ __align__(1024) uint8_t lds[kLds];
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
     constexpr int BB = GATED ? kBig / 2 : kBig;
     const int nt = (a.N + BO - 1) / BO, ntb = (a.N + BB - 1) / BB;
     // blocks go to the eight XCDs in turn: neighbouring tiles, which share rows
     // of x and w, to the blocks of one XCD (with an L2 of its own)
     const int pos = (blockIdx.x & 7) * (kGrid / 8) + (blockIdx.x >> 3);
-    make_plan(a, small_to_, ntb, nt, pos, &p);
-    const int small_to = uniform(p.small_to);
-    const int rounds = uniform(p.rounds), big = uniform(p.big);
-    const int halves = uniform(p.halves), quarters = uniform(p.quarters);
-    const int nbig = uniform(p.pre[0][a.groups]), nhalf = uniform(p.pre[1][a.groups]);
-    const int nquarter = uniform(p.pre[2][a.groups]), nsmall = uniform(p.pre[3][a.groups]);
+    const int rows0 = lane_rows(a, 0);
+    const Plan p = make_plan(a, rows0, small_to_, ntb, nt, pos);
+    const int small_to = p.small_to, rounds = p.rounds, big = p.big;
+    const int halves = p.halves, quarters = p.quarters;
+    const int nbig = p.total[0], nhalf = p.total[1], nquarter = p.total[2], nsmall = p.total[3];
     const int whole = nbig / kGrid * kGrid;       // tiles of whole rounds
     const int items = rounds + big + halves + quarters;
     for (int i = 0; i < items; ++i) {
@@ -823,7 +867,7 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
             t = l < 0 ? i * kGrid + pos : whole + pos;
         } else if ((l -= big) < halves) {
             kind = from = 1;
-            t = uniform(p.half0) + l;
+            t = p.half0 + l;
             if (t >= nhalf) {
                 from = 0;
                 sub = (t - nhalf) % 2;
@@ -831,7 +875,7 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
             }
         } else {
             kind = from = 2;
-            t = uniform(p.quarter0) + l - halves;
+            t = p.quarter0 + l - halves;
             if (t >= nquarter + 2 * nhalf) {
                 from = 0;
                 t -= nquarter + 2 * nhalf;
@@ -844,10 +888,10 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
                 t /= 2;
             }
         }
-        const int g = uniform(find_source(p.pre[from], a.groups, t));
-        const int rows = uniform(group_rows(a, g));
+        const Place at = find_tile(a, rows0, small_to, from, ntb, t);
+        const int g = at.g, rows = at.rows;
         const Cut c = cut_rows(rows, small_to);
-        l = t - uniform(p.pre[from][g]);
+        l = at.l;
         int m0, n0;
         if (from == 0) {
             // kGroup runs of rows at a time, over all columns
@@ -873,10 +917,9 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
         int t = tile_of(blockIdx.x, kGrid, nsmall - t0);
         if (t < 0) break;       // a last, partial round
         t += t0;
-        const int g = uniform(find_source(p.pre[3], a.groups, t));
-        const int rows = uniform(group_rows(a, g));
+        const Place at = find_tile(a, rows0, small_to, 3, nt, t);
+        const int g = at.g, rows = at.rows, l = at.l;
         const Cut c = cut_rows(rows, small_to);
-        const int l = t - uniform(p.pre[3][g]);
         const int from = c.n[0] * 256 + c.n[1] * 128 + c.n[2] * 64;
         small_tile<EB, WIDE, GATED, kWaves>(a, g, from + l % c.n[3] * kSmall, rows,
                                             l / c.n[3] * BO, reinterpret_cast<float*>(lds));
