@@ -128,118 +128,262 @@ __device__ __forceinline__ int group_rows(const MatmulArgs& a, int g) {
     return c < 0 ? 0 : c > a.rows ? a.rows : c;
 }
 
+// The buffer resource of row_rsrc as four scalar registers.
+__device__ __forceinline__ i32x4 row_rsrc4(const uint8_t* p, int64_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    i32x4 r;
+    r[0] = uniform((int)(uint32_t)at);
+    r[1] = uniform((int)(uint32_t)(at >> 32) & 0xFFFF);
+    r[2] = uniform((int)(bytes < INT32_MAX ? bytes : INT32_MAX));
+    r[3] = 0x00020000;
+    return r;
+}
+
+// 16 (or 4) bytes per lane from memory into LDS, lane l's at dst + 16 l (4 l);
+// dst is uniform, in M0. Written out so that the compiler does not count it
+// among the loads that an LDS read has to wait for: with its own form of this
+// instruction it waits for every load in flight before the next LDS read,
+// whatever that reads. The instruction has no output register; what it
+// writes is ordered by the waits and barriers below.
+__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t dst, uint32_t off, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(dst), "v"(off), "s"(r), "s"(soff)
+                 : "m0");
+}
+__device__ __forceinline__ void load4_to_lds(i32x4 r, uint32_t dst, uint32_t off, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                 :
+                 : "s"(dst), "v"(off), "s"(r), "s"(soff)
+                 : "m0");
+}
+
+// Tile of block b in a round of `left` tiles over the grid, -1 for none.
+// Blocks go to the eight XCDs in turn, so each XCD (with an L2 of its own)
+// gets a run of neighbouring tiles, which share rows of x and w.
+__device__ __forceinline__ int tile_of(int b, int grid, int left) {
+    const int r = left < grid ? left : grid;
+    const int per = (r + 7) / 8;
+    const int slot = b >> 3;
+    const int t = (b & 7) * per + slot;
+    return slot < per && t < r ? t : -1;
+}
+
 // ---------------------------------------------------------------------
 // Small tiles, for a few rows: 16 rows of x by 16 rows of w (gated: 8 gate
 // rows and their 8 up rows). Bound by the weights' bytes, so what counts is
-// loads in flight: the slabs of k are dealt to the block's waves in turn (the
-// block reads runs of 1 or 2 KB of each row), each keeps four slabs of both
-// operands on their way to registers, and the waves' sums are added in wave
-// order through LDS.
+// loads in flight. A block's eight waves share out the slabs of k in runs of
+// four (512 bytes of a row); each wave has its own four slabs of both operands
+// in LDS, always on their way, with no barrier between them: behind the last
+// slab of a tile it asks for the first of the block's next tile. The waves'
+// sums are added in wave order through LDS.
+//
+// The way through LDS is for the loads' sake: an MFMA wants neighbouring lanes
+// in different rows, and a load straight into that order takes 64 cycles for
+// its 1 KB (one 16-byte piece at a time), which held a CU to 36 GB/s; eight
+// neighbouring lanes to a row's 128 bytes take a quarter of that.
 // ---------------------------------------------------------------------
 constexpr int kSmall = 16;
 constexpr int kSmallPitch = kSmall + 4;
-template <int WAVES>
-constexpr int kSmallLds = WAVES * kSmall * kSmallPitch * 4;
-constexpr int kSmallDepth = 4;
+constexpr int kRun = 4;                          // slabs of a wave in LDS
+constexpr int kRing = kRun * 2 * kSmall * kSlab; // bytes of them
+constexpr int kPartAt = kWaves * kRing;          // the waves' sums, twice
+constexpr int kPart = kWaves * kSmall * kSmallPitch * 4;
+constexpr int kSmallScaleAt = kPartAt + 2 * kPart;        // fp8: scales of two runs
+constexpr int kSmallScale = 256 + 64;                     // 16 rows x 4, 2 blocks x 4 (padded)
+constexpr int kSmallLds = kSmallScaleAt + kWaves * 2 * 512;
 
-template <int EB, bool WIDE, bool GATED, int WAVES>
-__device__ __forceinline__ void small_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
-                                           float* lds) {
+// What a wave needs to load a small tile.
+struct SmallTile {
+    i32x4 rx, rw, rxs, rws;
+    uint32_t vx[2], vw[2], vxs, vws;
+    int g, m0, rows, n0;
+};
+
+template <int EB, bool GATED>
+__device__ __forceinline__ SmallTile small_setup(const MatmulArgs& a, int g, int m0, int rows,
+                                                 int n0) {
+    SmallTile t;
     const int lane = threadIdx.x & 63;
-    const int wave = threadIdx.x >> 6;
     const int kb = a.row_bytes;
     const int nslab = (kb + kSlab - 1) / kSlab;
     const int left = rows - m0;
     const int nw = GATED ? 2 * a.N : a.N;
-    const auto rx = row_rsrc(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
-                             (int64_t)(left - 1) * a.x_row + kb);
-    const auto rw = row_rsrc(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
-    const int r = lane & 15;
-    // lane l has the chunks l / 16 and l / 16 + 4 of a slab: a load takes 64
-    // consecutive bytes of each of 16 rows
-    const uint32_t kin = (uint32_t)(lane >> 4) * 16u;
-    const uint32_t vx = r < left ? (uint32_t)r * (uint32_t)a.x_row : kOutside;
-    const int wn = GATED ? n0 + (r & 7) : n0 + r;
-    const uint32_t vw =
-        wn < a.N ? (uint32_t)(GATED && r >= 8 ? a.N + wn : wn) * (uint32_t)a.w_row : kOutside;
-
-    const float* xs = nullptr;
-    const float* ws = nullptr;
+    t.g = g;
+    t.m0 = m0;
+    t.rows = rows;
+    t.n0 = n0;
+    t.rx = row_rsrc4(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
+                     (int64_t)(left - 1) * a.x_row + kb);
+    t.rw = row_rsrc4(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = h * 8 + (lane >> 3);
+        const uint32_t chunk = ((lane & 7) ^ ((r >> 1) & 7)) * 16;
+        t.vx[h] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk : kOutside;
+        const int n = GATED ? n0 + (r & 7) : n0 + r;
+        t.vw[h] = n < a.N ? (uint32_t)(GATED && r >= 8 ? a.N + n : n) * (uint32_t)a.w_row + chunk
+                          : kOutside;
+    }
+    t.rxs = t.rx;
+    t.rws = t.rw;
+    t.vxs = t.vws = kOutside;
     if constexpr (EB == 1) {
-        xs = a.xs + g * a.xs_stride + (int64_t)(m0 + (r < left ? r : left - 1)) * a.xs_pitch;
-        // the rows of w behind a lane's sums (4 * (lane / 16) on) share a block
+        // lane r: four scales of row r; lanes 4 b + i: block b's of slab i
+        if (lane < 16 && lane < left) t.vxs = (uint32_t)lane * (uint32_t)a.xs_pitch * 4;
+        t.rxs = row_rsrc4(
+            reinterpret_cast<const uint8_t*>(a.xs + g * a.xs_stride + (int64_t)m0 * a.xs_pitch),
+            (int64_t)left * a.xs_pitch * 4);
         const int per = (a.N + kScaleBlock - 1) / kScaleBlock;
-        const int blk = n0 / kScaleBlock + (GATED && lane >= 32 ? per : 0);
-        ws = a.ws + g * a.ws_stride + (int64_t)blk * nslab;
+        const int b = lane >> 2;
+        if (b < (GATED ? 2 : 1))
+            t.vws = ((uint32_t)(n0 / kScaleBlock + b * per) * (uint32_t)nslab + (lane & 3)) * 4;
+        t.rws = row_rsrc4(reinterpret_cast<const uint8_t*>(a.ws + g * a.ws_stride),
+                          (int64_t)(GATED ? 2 : 1) * per * nslab * 4);
     }
+    return t;
+}
 
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    Frag fx[kSmallDepth], fw[kSmallDepth];
-    float sc[kSmallDepth];
-    // A slab past the last loads nothing but zeros (the buffers' range check).
-    auto load = [&](int d, int s) {
-        const uint32_t k0 = (uint32_t)s * kSlab + kin;
+// Slab s of a tile into place j of the wave's ring (a slab past the last: zeros).
+__device__ __forceinline__ void small_fetch(const MatmulArgs& a, const SmallTile& t, int s, int j,
+                                            uint32_t ring) {
+    const int lane = threadIdx.x & 63;
+    const int kb = a.row_bytes;
+    const uint32_t k = s * kSlab < kb ? s * kSlab : 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t k = k0 + 64 * h;
-            const bool in = k < (uint32_t)kb;
-            fw[d].v[h] = ld_row_buf<false>(rw, in ? vw + k : kOutside);
-            fx[d].v[h] = ld_row_buf<false>(rx, in ? vx + k : kOutside);
-        }
-        if constexpr (EB == 1) {
-            const int c = s < nslab ? s : nslab - 1;
-            sc[d] = xs[c] * ws[c];
-        }
+    for (int h = 0; h < 2; ++h) {
+        const int chunk = ((lane & 7) ^ ((h * 4 + (lane >> 4)) & 7)) * 16;
+        const uint32_t none = s * kSlab + chunk < kb ? 0u : kOutside;
+        const uint32_t at = ring + j * 2 * kSmall * kSlab + h * 1024;
+        load_to_lds(t.rw, at, t.vw[h] | none, k);
+        load_to_lds(t.rx, at + kSmall * kSlab, t.vx[h] | none, k);
+    }
+}
+
+// The scales of the four slabs from s on (a multiple of 4).
+__device__ __forceinline__ void small_fetch_scales(const MatmulArgs& a, const SmallTile& t, int s,
+                                                   uint32_t at) {
+    const int nslab = (a.row_bytes + kSlab - 1) / kSlab;
+    const uint32_t k = s < nslab ? s * 4 : 0;
+    const uint32_t none = s < nslab ? 0u : kOutside;
+    if ((threadIdx.x & 63) < 16) load_to_lds(t.rxs, at, t.vxs | none, k);
+    if ((threadIdx.x & 63) < 16)
+        load4_to_lds(t.rws, at + 256, s + (int)(threadIdx.x & 3) < nslab ? t.vws : kOutside, k);
+}
+
+// Works through the block's tiles, number t of `total` at place(t) = {g, m0,
+// rows, n0}.
+template <int EB, bool WIDE, bool GATED, class Next>
+__device__ __forceinline__ void small_tiles(const MatmulArgs& a, uint8_t* lds, int total,
+                                            const Next& place) {
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int kb = a.row_bytes;
+    const int nslab = (kb + kSlab - 1) / kSlab;
+    const int runs = (nslab + kWaves * kRun - 1) / (kWaves * kRun);   // of each wave
+    const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
+    const uint32_t ring = lds0 + wave * kRing;
+    const uint32_t scales = lds0 + kSmallScaleAt + wave * 1024;
+    const uint8_t* mine = lds + wave * kRing;
+    const int r = lane & 15;
+    const int rd = r * kSlab + (((lane >> 4) ^ ((r >> 1) & 7)) * 16);
+
+    auto tile_at = [&](int t0) {
+        const int t = t0 < total ? tile_of(blockIdx.x, gridDim.x, total - t0) : -1;
+        return t < 0 ? -1 : t + t0;
     };
+    int t0 = 0, at = tile_at(0);
+    if (at < 0) return;
+    SmallTile cur = place(at);
+    if constexpr (EB == 1) small_fetch_scales(a, cur, wave * kRun, scales);
 #pragma unroll
-    for (int d = 0; d < kSmallDepth; ++d) load(d, wave + d * WAVES);
-    for (int s = wave; s < nslab; s += WAVES * kSmallDepth) {
+    for (int j = 0; j < kRun; ++j) small_fetch(a, cur, wave * kRun + j, j, ring);
+    int odd = 0, run = 0;                        // parity of the tile and of the run
+    for (;;) {
+        t0 += gridDim.x;
+        at = tile_at(t0);
+        SmallTile nxt = cur;
+        if (at >= 0) nxt = place(at);
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < runs; ++i) {
+            const bool ahead = i + 1 < runs;     // the next run is this tile's
+            const int s1 = at >= 0 || ahead ? ((ahead ? i + 1 : 0) * kWaves + wave) * kRun
+                                            : nslab;
 #pragma unroll
-        for (int d = 0; d < kSmallDepth; ++d) {
-            if constexpr (EB == 2) {
-                acc = mma_bf16(fw[d].v[0], fx[d].v[0], acc);
-                acc = mma_bf16(fw[d].v[1], fx[d].v[1], acc);
-            } else {
-                const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-                const f32x4 t = WIDE ? mma_wide(widen(fw[d]), widen(fx[d]), zero)
-                                     : mma_fp8(fw[d], fx[d], zero);
+            for (int j = 0; j < kRun; ++j) {
+                // the oldest slab has arrived (and, before it, its run's scales)
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kRun - 1) * 4) : "memory");
+                const uint8_t* p = mine + j * 2 * kSmall * kSlab;
+                Frag w, x;
+                w.v[0] = *reinterpret_cast<const u32x4*>(p + rd);
+                w.v[1] = *reinterpret_cast<const u32x4*>(p + (rd ^ 64));
+                x.v[0] = *reinterpret_cast<const u32x4*>(p + kSmall * kSlab + rd);
+                x.v[1] = *reinterpret_cast<const u32x4*>(p + kSmall * kSlab + (rd ^ 64));
+                float sc = 0.f;
+                if constexpr (EB == 1) {
+                    const float* q = reinterpret_cast<const float*>(lds + kSmallScaleAt + wave * 1024 +
+                                                                    run * 512);
+                    sc = q[r * 4 + j] * q[64 + (GATED && lane >= 32 ? 4 : 0) + j];
+                    // a scale row's padding may hold anything
+                    if ((i * kWaves + wave) * kRun + j >= nslab) sc = 0.f;
+                }
+                // read, so its place can be filled again
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                if constexpr (EB == 1) {
+                    if (j == 0) small_fetch_scales(a, ahead ? cur : nxt, s1, scales + (run ^ 1) * 512);
+                }
+                if (ahead) small_fetch(a, cur, s1 + j, j, ring);
+                else small_fetch(a, nxt, s1 + j, j, ring);
+                if constexpr (EB == 2) {
+                    acc = mma_bf16(w.v[0], x.v[0], acc);
+                    acc = mma_bf16(w.v[1], x.v[1], acc);
+                } else {
+                    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                    const f32x4 t = WIDE ? mma_wide(widen(w), widen(x), zero) : mma_fp8(w, x, zero);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(t[q], sc[d], acc[q]);
+                    for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(t[q], sc, acc[q]);
+                }
             }
-            load(d, s + (d + kSmallDepth) * WAVES);
+            run ^= 1;
         }
-    }
 
-    *reinterpret_cast<f32x4*>(lds + ((wave * kSmall + r) * kSmallPitch + (lane >> 4) * 4)) = acc;
-    __syncthreads();
-    constexpr int BO = GATED ? kSmall / 2 : kSmall;
-    const int o = threadIdx.x % BO, m = threadIdx.x / BO;
-    const int n = n0 + o;
-    if (m < kSmall && m < left && n < a.N) {
-        float v = 0.f, up = 0.f;
+        float* part = reinterpret_cast<float*>(lds + kPartAt + odd * kPart);
+        *reinterpret_cast<f32x4*>(part + ((wave * kSmall + r) * kSmallPitch + (lane >> 4) * 4)) = acc;
+        // the waves' sums are written; loads stay in flight
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        constexpr int BO = GATED ? kSmall / 2 : kSmall;
+        const int o = threadIdx.x % BO, m = threadIdx.x / BO;
+        const int n = cur.n0 + o;
+        if (m < kSmall && cur.m0 + m < cur.rows && n < a.N) {
+            float v = 0.f, up = 0.f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            v += lds[(w * kSmall + m) * kSmallPitch + o];
-            if (GATED) up += lds[(w * kSmall + m) * kSmallPitch + o + 8];
+            for (int w = 0; w < kWaves; ++w) {
+                v += part[(w * kSmall + m) * kSmallPitch + o];
+                if (GATED) up += part[(w * kSmall + m) * kSmallPitch + o + 8];
+            }
+            if (a.bias) {
+                const float* b = a.bias + cur.g * a.bias_stride + n;
+                v += b[0];
+                if (GATED) up += b[a.N];
+            }
+            v = GATED ? silu_gated(v, up) : apply_act(v, a.act);
+            const bool f32 = EB == 1 ? WIDE : a.out_dtype == MOE_EP_F32;
+            const int64_t row = cur.m0 + m;
+            if (a.res) {
+                const uint8_t* q = a.res + row * a.res_row;
+                v += f32 ? reinterpret_cast<const float*>(q)[n]
+                         : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(q)[n] << 16);
+            }
+            uint8_t* p = a.out + cur.g * a.out_stride + row * a.out_row;
+            if (f32) reinterpret_cast<float*>(p)[n] = v;
+            else reinterpret_cast<uint16_t*>(p)[n] = (uint16_t)to_bf16_rne(v);
         }
-        if (a.bias) {
-            const float* b = a.bias + g * a.bias_stride + n;
-            v += b[0];
-            if (GATED) up += b[a.N];
-        }
-        v = GATED ? silu_gated(v, up) : apply_act(v, a.act);
-        const bool f32 = EB == 1 ? WIDE : a.out_dtype == MOE_EP_F32;
-        const int64_t row = m0 + m;
-        if (a.res) {
-            const uint8_t* q = a.res + row * a.res_row;
-            v += f32 ? reinterpret_cast<const float*>(q)[n]
-                     : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(q)[n] << 16);
-        }
-        uint8_t* p = a.out + g * a.out_stride + row * a.out_row;
-        if (f32) reinterpret_cast<float*>(p)[n] = v;
-        else reinterpret_cast<uint16_t*>(p)[n] = (uint16_t)to_bf16_rne(v);
+        if (at < 0) break;
+        cur = nxt;
+        odd ^= 1;
     }
-    __syncthreads();   // the next tile writes lds again
+    // nothing of this block's is on its way into LDS when the block ends
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 // ---------------------------------------------------------------------
@@ -289,36 +433,6 @@ __device__ __forceinline__ int wrow(int r, int n0, int N, int& n) {
     }
     n = n0 + (r >> 6) * 32 + q * 8 + (i >> 1) * 4 + t;
     return (i & 1) ? N + n : n;
-}
-
-// The buffer resource of row_rsrc as four scalar registers.
-__device__ __forceinline__ i32x4 row_rsrc4(const uint8_t* p, int64_t bytes) {
-    const uint64_t at = reinterpret_cast<uint64_t>(p);
-    i32x4 r;
-    r[0] = uniform((int)(uint32_t)at);
-    r[1] = uniform((int)(uint32_t)(at >> 32) & 0xFFFF);
-    r[2] = uniform((int)(bytes < INT32_MAX ? bytes : INT32_MAX));
-    r[3] = 0x00020000;
-    return r;
-}
-
-// 16 (or 4) bytes per lane from memory into LDS, lane l's at dst + 16 l (4 l);
-// dst is uniform, in M0. Written out so that the compiler does not count it
-// among the loads that an LDS read has to wait for: with its own form of this
-// instruction it waits for every load in flight before the next LDS read,
-// whatever that reads. The instruction has no output register; what it
-// writes is ordered by the waits and barriers below.
-__device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t dst, uint32_t off, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :
-                 : "s"(dst), "v"(off), "s"(r), "s"(soff)
-                 : "m0");
-}
-__device__ __forceinline__ void load4_to_lds(i32x4 r, uint32_t dst, uint32_t off, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :
-                 : "s"(dst), "v"(off), "s"(r), "s"(soff)
-                 : "m0");
 }
 
 // Waits until at most LEFT of this wave's loads are in flight and for its LDS
@@ -700,6 +814,10 @@ struct Cut {
 
 __device__ __forceinline__ Cut cut_rows(int rows, int small_to) {
     Cut c = {};
+    if (small_to == INT32_MAX) {                 // small tiles alone
+        c.n[3] = (rows + kSmall - 1) / kSmall;
+        return c;
+    }
     c.n[0] = rows / 256;
     int r = rows % 256;
     if (r > 192) {
@@ -761,17 +879,6 @@ __device__ __forceinline__ Place find_tile(const MatmulArgs& a, int rows0, int s
         }
         t -= __builtin_amdgcn_readlane(inc, 63);
     }
-}
-
-// Tile of block b in a round of `left` tiles over the grid, -1 for none.
-// Blocks go to the eight XCDs in turn, so each XCD (with an L2 of its own)
-// gets a run of neighbouring tiles, which share rows of x and w.
-__device__ __forceinline__ int tile_of(int b, int grid, int left) {
-    const int r = left < grid ? left : grid;
-    const int per = (r + 7) / 8;
-    const int slot = b >> 3;
-    const int t = (b & 7) * per + slot;
-    return slot < per && t < r ? t : -1;
 }
 
 // The block's share. Rounds of 256-row tiles come first, one per block. What
@@ -913,57 +1020,30 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
         else if (kind == 1) big_tile<EB, WIDE, GATED, 128>(a, g, m0, rows, n0, lds);
         else big_tile<EB, WIDE, GATED, 64>(a, g, m0, rows, n0, lds);
     }
-    for (int t0 = 0; t0 < nsmall; t0 += kGrid) {
-        int t = tile_of(blockIdx.x, kGrid, nsmall - t0);
-        if (t < 0) break;       // a last, partial round
-        t += t0;
-        const Place at = find_tile(a, rows0, small_to, 3, nt, t);
-        const int g = at.g, rows = at.rows, l = at.l;
-        const Cut c = cut_rows(rows, small_to);
-        const int from = c.n[0] * 256 + c.n[1] * 128 + c.n[2] * 64;
-        small_tile<EB, WIDE, GATED, kWaves>(a, g, from + l % c.n[3] * kSmall, rows,
-                                            l / c.n[3] * BO, reinterpret_cast<float*>(lds));
-    }
+    if (nsmall > 0)
+        small_tiles<EB, WIDE, GATED>(a, lds, nsmall, [&](int t) {
+            const Place at = find_tile(a, rows0, small_to, 3, nt, t);
+            const Cut c = cut_rows(at.rows, small_to);
+            const int from = c.n[0] * 256 + c.n[1] * 128 + c.n[2] * 64;
+            return small_setup<EB, GATED>(a, at.g, from + at.l % c.n[3] * kSmall, at.rows,
+                                          at.l / c.n[3] * BO);
+        });
 }
 
 // Small tiles alone, where the host knows that there are few rows.
-template <int EB, bool WIDE, bool GATED, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 4) void small_kernel(const MatmulArgs a) {
-    __shared__ __align__(16) uint8_t lds[kSmallLds<WAVES>];
-    __shared__ int32_t pre[MOE_EP_MAX_LOCAL_EXPERTS + 1];
+template <int EB, bool WIDE, bool GATED>
+__global__ __launch_bounds__(kThreads, 2) void small_kernel(const MatmulArgs a) {
+    __shared__ __align__(1024) uint8_t lds[kSmallLds];
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
     const int nt = (a.N + BO - 1) / BO;
-    int total = (a.rows + kSmall - 1) / kSmall * nt;
-    if (a.counts) {
-        if (threadIdx.x < 64) {
-            int32_t run = 0;
-            for (int g0 = 0; g0 < a.groups; g0 += 64) {
-                const int g = g0 + (int)threadIdx.x;
-                const int32_t t =
-                    g < a.groups ? (group_rows(a, g) + kSmall - 1) / kSmall * nt : 0;
-                const int32_t inc = wave_inclusive_scan(t);
-                if (g < a.groups) pre[g] = run + inc - t;
-                run += __shfl(inc, 63, 64);
-            }
-            if (threadIdx.x == 0) pre[a.groups] = run;
-        }
-        __syncthreads();
-        total = uniform(pre[a.groups]);
-    }
-    for (int t0 = 0; t0 < total; t0 += gridDim.x) {
-        int l = tile_of(blockIdx.x, gridDim.x, total - t0);
-        if (l < 0) break;       // a last, partial round
-        l += t0;
-        int g = 0, rows = a.rows;
-        if (a.counts) {
-            g = uniform(find_source(pre, a.groups, l));
-            rows = uniform(group_rows(a, g));
-            l -= uniform(pre[g]);
-        }
-        const int mt = (rows + kSmall - 1) / kSmall;
-        small_tile<EB, WIDE, GATED, WAVES>(a, g, l % mt * kSmall, rows, l / mt * BO,
-                                           reinterpret_cast<float*>(lds));
-    }
+    const int rows0 = lane_rows(a, 0);
+    int n[kKinds];
+    count_tiles(a, rows0, INT32_MAX, 0, nt, n);
+    small_tiles<EB, WIDE, GATED>(a, lds, n[3], [&](int t) {
+        const Place at = find_tile(a, rows0, INT32_MAX, 3, nt, t);
+        const int mt = (at.rows + kSmall - 1) / kSmall;
+        return small_setup<EB, GATED>(a, at.g, at.l % mt * kSmall, at.rows, at.l / mt * BO);
+    });
 }
 
 template <int EB, bool WIDE, bool GATED>
@@ -978,12 +1058,9 @@ hipError_t launch(const MatmulArgs& a, hipStream_t st) {
     if (!few) {
         matmul_kernel<EB, WIDE, GATED>
             <<<kGrid, kThreads, 0, st>>>(a, e4m3 || !a.counts ? 0 : kSmall);
-    } else if (small <= 256) {
-        // a block of sixteen waves per CU reads a tile in half the steps
-        small_kernel<EB, WIDE, GATED, 16><<<(unsigned)((small + 7) / 8 * 8), 1024, 0, st>>>(a);
     } else {
-        const int64_t grid = small < 512 ? (small + 7) / 8 * 8 : 512;
-        small_kernel<EB, WIDE, GATED, 8><<<(unsigned)grid, 512, 0, st>>>(a);
+        const int64_t grid = small < kGrid ? (small + 7) / 8 * 8 : kGrid;
+        small_kernel<EB, WIDE, GATED><<<(unsigned)grid, kThreads, 0, st>>>(a);
     }
     return hipGetLastError();
 }
