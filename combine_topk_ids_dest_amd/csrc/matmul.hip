@@ -415,9 +415,9 @@ constexpr int kScaleAt = kLds - kScaleLds;
 // (256 rows: with two slabs of each, a slab's time is below HBM's loaded
 // latency of about 2 us, and the products wait for the weights.)
 template <int EB, int BM>
-constexpr int kStagesX = EB == 2 ? (BM == 256 ? 2 : BM == 128 ? 3 : 4) : (BM == 256 ? 2 : 3);
+constexpr int kStagesX = BM > 128 ? 2 : EB == 2 && BM == 64 ? 4 : 3;
 template <int EB, int BM>
-constexpr int kStagesW = EB == 2 ? (BM == 64 ? 4 : 3) : (BM == 256 ? 2 : 3);
+constexpr int kStagesW = EB == 2 ? (BM == 64 ? 4 : 3) : (BM > 128 ? 2 : 3);
 
 // Row of w behind row r of a tile whose first output column is n0, and its
 // output column n (columns n >= N do not exist). A fragment's row 4 q + t
@@ -459,9 +459,9 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
                                          uint8_t* lds) {
     constexpr int JF = BM / 32;                   // fragments of x of a wave
     constexpr int XS = kStagesX<EB, BM>, WS = kStagesW<EB, BM>;
-    constexpr int SLAB_X = BM * kSlab;
+    constexpr int FX = (BM + 63) / 64;            // loads of x of a wave and slab
+    constexpr int SLAB_X = FX * 64 * kSlab;
     constexpr int AT_W = XS * SLAB_X;             // slabs of w behind those of x
-    constexpr int FX = BM / 64;                   // loads of x of a wave and slab
     constexpr int FETCH = FX + 4;
     static_assert(XS <= WS && AT_W + WS * kBigSlab <= (EB == 1 ? kScaleAt : kLds), "");
     const int lane = threadIdx.x & 63;
@@ -469,7 +469,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
     const int wm = wave >> 2, wn = wave & 3;
     const int kb = a.row_bytes;
     const int nslab = (kb + kSlab - 1) / kSlab;
-    const int left = rows - m0;
+    const int left = rows - m0 < BM ? rows - m0 : BM;
     const int nw = GATED ? 2 * a.N : a.N;
     const i32x4 rx = row_rsrc4(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
                                (int64_t)(left - 1) * a.x_row + kb);
@@ -507,7 +507,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
     i32x4 rxs = rx, rws = rw;
     if constexpr (EB == 1) {
         const int row = wave * 64 + lane;
-        if (row < BM && row < left) vxs = (uint32_t)row * (uint32_t)a.xs_pitch * 4;
+        if (row < left) vxs = (uint32_t)row * (uint32_t)a.xs_pitch * 4;
         rxs = row_rsrc4(reinterpret_cast<const uint8_t*>(a.xs + g * a.xs_stride +
                                                          (int64_t)m0 * a.xs_pitch),
                         (int64_t)left * a.xs_pitch * 4);
@@ -532,7 +532,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
     };
 
     const int rd = (lane & 15) * kSlab + (((lane >> 4) ^ ((lane >> 1) & 7)) * 16);
-    const uint8_t* rdx = lds + wm * (BM / 2) * kSlab;
+    const uint8_t* rdx = lds + wm * (JF * 16) * kSlab;
     const uint8_t* rdw = lds + AT_W + wn * 64 * kSlab;
     f32x4 acc[4][JF];
 #pragma unroll
@@ -640,7 +640,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
 #pragma unroll
                 for (int j = 0; j < JF; ++j) {
                     const Wide x = widen(frag(px + j * 16 * kSlab));
-                    const float sx = sc[(wm * (BM / 2) + j * 16 + (lane & 15)) * 4 + (s & 3)];
+                    const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) scale(i, j, mma_wide(w[i], x, zero), sx);
                 }
@@ -651,7 +651,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
 #pragma unroll
                 for (int j = 0; j < JF; ++j) {
                     const Frag x = frag(px + j * 16 * kSlab);
-                    const float sx = sc[(wm * (BM / 2) + j * 16 + (lane & 15)) * 4 + (s & 3)];
+                    const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) scale(i, j, mma_fp8(w[i], x, zero), sx);
                 }
@@ -662,7 +662,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
     wait_and_barrier<0>();   // LDS is free for what follows
 
     // Epilogue. A lane has QN quads of consecutive columns from n on, of rows
-    // wm * BM / 2 + 16 j + lane % 16. Rows and columns that do not exist are
+    // 16 (wm JF + j) + lane % 16. Rows and columns that do not exist are
     // outside the buffers' ranges: their loads give 0, their stores nothing.
     constexpr int QN = GATED ? 2 : 4;
     const int n = n0 + (GATED ? wn * 32 + (lane >> 4) * 8 : wn * 64 + (lane >> 4) * 16);
@@ -685,7 +685,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
         return activate<GATED>(acc[GATED ? 2 * q : q][j], acc[GATED ? 2 * q + 1 : q][j], a.act);
     };
     uint8_t* const out = a.out + g * a.out_stride + (int64_t)m0 * a.out_row;
-    const int mrow = wm * (BM / 2) + (lane & 15);
+    const int mrow = wm * (JF * 16) + (lane & 15);
 
     if constexpr (EB == 1 && WIDE) {
         if (a.out_dtype == MOE_EP_E4M3) {
@@ -768,13 +768,13 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
         u32x4 r[JB][QN / 2];
         if (a.res) {
 #pragma unroll
-            for (int j = 0; j < JB; ++j)
+            for (int j = 0; j < JB && j0 + j < JF; ++j)
 #pragma unroll
                 for (int q = 0; q < QN / 2; ++q)
                     r[j][q] = ld_row_buf<false>(rr, at(j0 + j, 2 * q, a.res_row));
         }
 #pragma unroll
-        for (int j = 0; j < JB; ++j)
+        for (int j = 0; j < JB && j0 + j < JF; ++j)
 #pragma unroll
             for (int q = 0; q < QN / 2; ++q) {
                 f32x4 lo = value(2 * q, j0 + j), hi = value(2 * q + 1, j0 + j);
@@ -791,46 +791,33 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
 }
 
 // ---------------------------------------------------------------------
-// The work list. A group's rows are cut into runs of 256; what is left into
-// runs of 128 and 64 rows and, up to small_to rows, small tiles. One block per
-// CU works through its share, which every block computes for itself from the
-// counts (there is no queue, so nothing to clear and no order left to chance).
+// The work list. A group's rows are cut into equal runs of at most 256 rows (a
+// multiple of 32), so that a group's weights are read by all of its runs at the
+// same time, side by side on one XCD, and from HBM once. (Whole runs of 256 and
+// a remainder read them twice: 1.7 times the bytes at 32 experts of 240 to 1280
+// rows, 1066 against 835 us for 32 experts of 7168 -> 2 x 2048.) Groups of up to small_to rows get small tiles.
+//
+// Tiles are dealt out longest runs first, one to a block and round, one block
+// per CU. Every block computes its share from the counts for itself: there is
+// no queue, so nothing to clear and no order left to chance.
 // ---------------------------------------------------------------------
-constexpr int kKinds = 4;                        // runs of 256, 128, 64 rows, small
-constexpr int kGrid = 256;                       // blocks of the big kernel
-constexpr int kGroup = 8;                        // runs of 256 rows side by side
-
-struct Plan {
-    int total[kKinds];                           // tiles of each kind
-    int small_to;
-    // whole rounds of 256-row tiles, then of the rest this block's tiles of
-    // 256 rows (0 or 1), and its runs of the 128-row and 64-row tiles
-    int rounds, big, half0, halves, quarter0, quarters;
-};
+constexpr int kGrid = 256;                       // blocks
+constexpr int kGroup = 8;                        // runs of rows side by side
+constexpr int kKinds = 9;                        // runs of 32 k rows, k = 1..8; small: 0
 
 struct Cut {
-    int n[kKinds];                               // runs of rows of each kind
+    int runs, kind;
 };
 
 __device__ __forceinline__ Cut cut_rows(int rows, int small_to) {
-    Cut c = {};
-    if (small_to == INT32_MAX) {                 // small tiles alone
-        c.n[3] = (rows + kSmall - 1) / kSmall;
+    Cut c;
+    if (rows <= small_to) {
+        c.kind = 0;
+        c.runs = (rows + kSmall - 1) / kSmall;
         return c;
     }
-    c.n[0] = rows / 256;
-    int r = rows % 256;
-    if (r > 192) {
-        ++c.n[0];
-        r = 0;
-    } else if (r > 64 + small_to) {
-        c.n[1] = 1;
-        r = r > 128 ? r - 128 : 0;
-    }
-    c.n[2] = r / 64;
-    r %= 64;
-    if (r > small_to) ++c.n[2];
-    else c.n[3] = (r + kSmall - 1) / kSmall;
+    c.runs = (rows + 255) / 256;
+    c.kind = ((rows + c.runs - 1) / c.runs + 31) / 32;
     return c;
 }
 
@@ -842,21 +829,33 @@ __device__ __forceinline__ int lane_rows(const MatmulArgs& a, int g0) {
 
 // Everything here is done by each wave for itself, with no LDS (the tiles take
 // all of it): a group to a lane, 64 groups at a time. rows0: lane_rows(a, 0).
-__device__ __forceinline__ void count_tiles(const MatmulArgs& a, int rows0, int small_to,
-                                            int nt_big, int nt_small, int (&total)[kKinds]) {
+
+// Runs of each kind, of all groups.
+__device__ __forceinline__ void count_runs(const MatmulArgs& a, int rows0, int small_to,
+                                           int (&total)[kKinds]) {
 #pragma unroll
     for (int k = 0; k < kKinds; ++k) total[k] = 0;
     for (int g0 = 0; g0 < a.groups; g0 += 64) {
         const Cut c = cut_rows(g0 ? lane_rows(a, g0) : rows0, small_to);
+        const int32_t inc = wave_inclusive_scan(c.runs);
 #pragma unroll
         for (int k = 0; k < kKinds; ++k) {
-            const int32_t inc = wave_inclusive_scan(c.n[k] * (k == 3 ? nt_small : nt_big));
-            total[k] += __builtin_amdgcn_readlane(inc, 63);
+            uint64_t mine = __ballot(c.kind == k && c.runs > 0);
+            while (mine) {                       // few lanes, or all of one kind
+                const int l = __builtin_ctzll(mine);
+                // a stretch of lanes of this kind at once
+                const uint64_t rest = ~(mine >> l);
+                const int n = rest ? __builtin_ctzll(rest) : 64 - l;
+                total[k] += __builtin_amdgcn_readlane(inc, l + n - 1) -
+                            (l ? __builtin_amdgcn_readlane(inc, l - 1) : 0);
+                mine = l + n < 64 ? mine >> (l + n) << (l + n) : 0;
+            }
         }
     }
 }
 
-// The group of tile t of a kind, its rows and the tile's number in it.
+// The group of tile t of a kind (nt tiles to a run), its rows and the tile's
+// number in it.
 struct Place {
     int g, rows, l;
 };
@@ -866,7 +865,7 @@ __device__ __forceinline__ Place find_tile(const MatmulArgs& a, int rows0, int s
     for (int g0 = 0;; g0 += 64) {
         const int rows = g0 ? lane_rows(a, g0) : rows0;
         const Cut c = cut_rows(rows, small_to);
-        const int n = nt * (kind == 0 ? c.n[0] : kind == 1 ? c.n[1] : kind == 2 ? c.n[2] : c.n[3]);
+        const int n = c.kind == kind ? nt * c.runs : 0;
         const int32_t inc = wave_inclusive_scan(n);
         const uint64_t behind = __ballot(inc > t);
         if (behind || g0 + 64 >= a.groups) {     // t is below the total: a lane is found
@@ -881,77 +880,8 @@ __device__ __forceinline__ Place find_tile(const MatmulArgs& a, int rows0, int s
     }
 }
 
-// The block's share. Rounds of 256-row tiles come first, one per block. What
-// is left, in units of a 64-row tile, would fill `high` units of each block: it
-// is laid out in columns of that height, largest tiles first. With less than a
-// 256-row tile's height the 256-row tiles left are cut in two, with a single
-// unit everything is cut into 64-row tiles (and these are spread over the
-// XCDs): 3.5 rounds then take 3.5 tiles' time and not 4, and a few rows an
-// expert, bound by the weights' bytes, are read by all CUs.
-__device__ __forceinline__ Plan make_plan(const MatmulArgs& a, int rows0, int small_to, int nt_big,
-                                          int nt_small, int pos) {
-    Plan p;
-    int (&n)[kKinds] = p.total;
-    count_tiles(a, rows0, small_to, nt_big, nt_small, n);
-    if (small_to && n[0] * 4 + n[1] * 2 + n[2] > kGrid) {
-        // small tiles beside so much else cost more than part-filled ones
-        small_to = 0;
-        count_tiles(a, rows0, 0, nt_big, nt_small, n);
-    }
-    p.small_to = small_to;
-    const int u = 4 * (n[0] % kGrid) + 2 * n[1] + n[2];
-    int high = (u + kGrid - 1) / kGrid;
-    int big = n[0] % kGrid, half = n[1], quarter = n[2];
-    if (high == 1) {
-        quarter += 2 * half + 4 * big;
-        big = half = 0;
-    } else if (high < 4) {
-        half += 2 * big;
-        big = 0;
-    }
-    // a column holds high / 2 halves, beside a 256-row tile (high - 4) / 2
-    while ((kGrid - big) * (high / 2) + big * (high >= 4 ? (high - 4) / 2 : 0) < half) ++high;
-    const int hc = high / 2, hb = high >= 4 ? (high - 4) / 2 : 0;
-    const int over = half - (kGrid - big) * hc;
-    int h0[4], hn[4], rem[4], sum = 0;           // four columns to a lane
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = (int)(threadIdx.x & 63) * 4 + i;
-        const bool b = c < big;
-        const int at = b ? c * hb : (c - big) * hc;
-        const int most = b ? hb : hc;
-        int m = (b ? over : half) - at;
-        m = m < 0 ? 0 : m > most ? most : m;
-        h0[i] = (b ? (kGrid - big) * hc : 0) + at;
-        hn[i] = m;
-        rem[i] = high - (b ? 4 : 0) - 2 * m;
-        sum += rem[i];
-    }
-    int q = wave_inclusive_scan(sum) - sum;
-    p.rounds = n[0] / kGrid;
-    p.big = pos < big ? 1 : 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (i == pos % 4) {
-            const int left = quarter - q;
-            p.half0 = __builtin_amdgcn_readlane(h0[i], pos / 4);
-            p.halves = __builtin_amdgcn_readlane(hn[i], pos / 4);
-            p.quarter0 = __builtin_amdgcn_readlane(q, pos / 4);
-            p.quarters = __builtin_amdgcn_readlane(left < 0 ? 0 : left > rem[i] ? rem[i] : left,
-                                                   pos / 4);
-        }
-        q += rem[i];
-    }
-    if (high == 1) {
-        const int t = tile_of(blockIdx.x, kGrid, quarter);
-        p.quarter0 = t;
-        p.quarters = t < 0 ? 0 : 1;
-    }
-    return p;
-}
-
 template <int EB, bool WIDE, bool GATED>
-__global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a, int small_to_) {
+__global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a, int small_to) {
     __shared__ __align__(1024) uint8_t lds[kLds];
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
     constexpr int BB = GATED ? kBig / 2 : kBig;
@@ -960,73 +890,71 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
     // of x and w, to the blocks of one XCD (with an L2 of its own)
     const int pos = (blockIdx.x & 7) * (kGrid / 8) + (blockIdx.x >> 3);
     const int rows0 = lane_rows(a, 0);
-    const Plan p = make_plan(a, rows0, small_to_, ntb, nt, pos);
-    const int small_to = p.small_to, rounds = p.rounds, big = p.big;
-    const int halves = p.halves, quarters = p.quarters;
-    const int nbig = p.total[0], nhalf = p.total[1], nquarter = p.total[2], nsmall = p.total[3];
-    const int whole = nbig / kGrid * kGrid;       // tiles of whole rounds
-    const int items = rounds + big + halves + quarters;
-    for (int i = 0; i < items; ++i) {
-        int kind, t, from = 0, sub = 0;          // a tile of kind `from`, its part `sub`
-        int l = i - rounds;
-        if (l < big) {
-            kind = 0;
-            t = l < 0 ? i * kGrid + pos : whole + pos;
-        } else if ((l -= big) < halves) {
-            kind = from = 1;
-            t = p.half0 + l;
-            if (t >= nhalf) {
-                from = 0;
-                sub = (t - nhalf) % 2;
-                t = whole + (t - nhalf) / 2;
-            }
-        } else {
-            kind = from = 2;
-            t = p.quarter0 + l - halves;
-            if (t >= nquarter + 2 * nhalf) {
-                from = 0;
-                t -= nquarter + 2 * nhalf;
-                sub = t % 4;
-                t = whole + t / 4;
-            } else if (t >= nquarter) {
-                from = 1;
-                t -= nquarter;
-                sub = t % 2;
-                t /= 2;
-            }
+    int n[kKinds], total = 0;
+    for (;;) {
+        count_runs(a, rows0, small_to, n);
+        total = 0;
+#pragma unroll
+        for (int k = 1; k < kKinds; ++k) {
+            n[k] *= ntb;
+            total += n[k];
         }
-        const Place at = find_tile(a, rows0, small_to, from, ntb, t);
-        const int g = at.g, rows = at.rows;
-        const Cut c = cut_rows(rows, small_to);
-        l = at.l;
-        int m0, n0;
-        if (from == 0) {
-            // kGroup runs of rows at a time, over all columns
-            const int m8 = l / (kGroup * ntb) * kGroup;
-            const int wide = c.n[0] - m8 < kGroup ? c.n[0] - m8 : kGroup;
-            const int in = l - m8 * ntb;
-            m0 = (m8 + in % wide) * 256;
-            n0 = in / wide;
-        } else if (from == 1) {
-            m0 = c.n[0] * 256;
-            n0 = l;
-        } else {
-            m0 = c.n[0] * 256 + c.n[1] * 128 + l % c.n[2] * 64;
-            n0 = l / c.n[2];
+        // small tiles beside so much else cost more than part-filled ones
+        if (!small_to || total <= kGrid) break;
+        small_to = 0;
+    }
+    const int nsmall = n[0] * nt;
+    const int whole = total / kGrid * kGrid;
+    // The last, partial round: with at most half (a quarter) as many tiles as
+    // blocks, each tile is cut in two (four) by its rows. 3.5 rounds then take
+    // 3.5 tiles' time and not 4, and a few rows an expert, bound by the
+    // weights' bytes, are read by all CUs.
+    const int parts = (total - whole) * 4 <= kGrid ? 4 : (total - whole) * 2 <= kGrid ? 2 : 1;
+    for (int t0 = 0; t0 < total; t0 += kGrid) {
+        int t = t0 + pos, sub = 0, cut = 1;
+        if (t0 == whole) {
+            const int u = tile_of(blockIdx.x, kGrid, (total - whole) * parts);
+            if (u < 0) break;
+            t = whole + u / parts;
+            sub = u % parts;
+            cut = parts;
         }
-        n0 *= BB;
-        m0 += sub * (kind == 1 ? 128 : 64);
-        if (kind == 0) big_tile<EB, WIDE, GATED, 256>(a, g, m0, rows, n0, lds);
-        else if (kind == 1) big_tile<EB, WIDE, GATED, 128>(a, g, m0, rows, n0, lds);
-        else big_tile<EB, WIDE, GATED, 64>(a, g, m0, rows, n0, lds);
+        int kind = kKinds - 1;
+#pragma unroll
+        for (int k = kKinds - 1; k > 1; --k)
+            if (kind == k && t >= n[k]) {
+                t -= n[k];
+                --kind;
+            }
+        const Place at = find_tile(a, rows0, small_to, kind, ntb, t);
+        const int runs = cut_rows(at.rows, small_to).runs;
+        // kGroup runs of rows at a time, over all columns
+        const int m8 = at.l / (kGroup * ntb) * kGroup;
+        const int wide = runs - m8 < kGroup ? runs - m8 : kGroup;
+        const int in = at.l - m8 * ntb;
+        const int from = (m8 + in % wide) * kind * 32;
+        const int end = from + kind * 32 < at.rows ? from + kind * 32 : at.rows;
+        const int jf = (kind + cut - 1) / cut;
+        const int m0 = from + sub * jf * 32;
+        if (m0 >= end) continue;
+        const int n0 = in / wide * BB;
+        // (a tile of a run-time number of fragments was 18 % slower: its loop
+        // is full of branches)
+        auto run = [&](auto bm) {
+            big_tile<EB, WIDE, GATED, decltype(bm)::value>(a, at.g, m0, end, n0, lds);
+        };
+        if (jf > 7) run(std::integral_constant<int, 256>{});
+        else if (jf > 6) run(std::integral_constant<int, 224>{});
+        else if (jf > 5) run(std::integral_constant<int, 192>{});
+        else if (jf > 4) run(std::integral_constant<int, 160>{});
+        else if (jf > 2) run(std::integral_constant<int, 128>{});
+        else run(std::integral_constant<int, 64>{});
     }
     if (nsmall > 0)
         small_tiles<EB, WIDE, GATED>(a, lds, nsmall, [&](int t) {
-            const Place at = find_tile(a, rows0, small_to, 3, nt, t);
-            const Cut c = cut_rows(at.rows, small_to);
-            const int from = c.n[0] * 256 + c.n[1] * 128 + c.n[2] * 64;
-            return small_setup<EB, GATED>(a, at.g, from + at.l % c.n[3] * kSmall, at.rows,
-                                          at.l / c.n[3] * BO);
+            const Place at = find_tile(a, rows0, small_to, 0, nt, t);
+            const int mt = cut_rows(at.rows, small_to).runs;
+            return small_setup<EB, GATED>(a, at.g, at.l % mt * kSmall, at.rows, at.l / mt * BO);
         });
 }
 
@@ -1038,10 +966,10 @@ __global__ __launch_bounds__(kThreads, 2) void small_kernel(const MatmulArgs a) 
     const int nt = (a.N + BO - 1) / BO;
     const int rows0 = lane_rows(a, 0);
     int n[kKinds];
-    count_tiles(a, rows0, INT32_MAX, 0, nt, n);
-    small_tiles<EB, WIDE, GATED>(a, lds, n[3], [&](int t) {
-        const Place at = find_tile(a, rows0, INT32_MAX, 3, nt, t);
-        const int mt = (at.rows + kSmall - 1) / kSmall;
+    count_runs(a, rows0, INT32_MAX, n);
+    small_tiles<EB, WIDE, GATED>(a, lds, n[0] * nt, [&](int t) {
+        const Place at = find_tile(a, rows0, INT32_MAX, 0, nt, t);
+        const int mt = cut_rows(at.rows, INT32_MAX).runs;
         return small_setup<EB, GATED>(a, at.g, at.l % mt * kSmall, at.rows, at.l / mt * BO);
     });
 }
