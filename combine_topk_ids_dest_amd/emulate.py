@@ -23,6 +23,15 @@ Device layout (all dense, rank-major):
   ret             [W_dst, W_src, cap, H]
   out             [W_src, T, H]
 
+With set_layer() the ranks are a whole MoE layer and not only its data
+movement: the router makes ids and wts of the source rows before the pack,
+the experts make Y of the batched rows between batch and reduce, and an
+expert that every token passes through is added to out behind the unpack:
+  logits          [W_src, T, E]            fp32
+  hidden          [e_local, W*cap, I]      a lane's expert rows between their
+                                           two products (fp8: codes + scales)
+  shared          [T, I_shared]            a lane's, the same for that expert
+
 Lanes: rank i uses lane i % lanes for the buffers that ranks share (the
 workspace, b and Y), so no two lanes read or write the same expert rows. With several lanes, step(streams=...) runs the ranks of
 each lane on its own HIP stream, so the kernels of different ranks may
@@ -146,6 +155,7 @@ class LogicalEP:
         self.workspace = self.workspaces[0]
         self._calls = {}
         self._events = {}
+        self._layer = None
 
     # -- inputs ---------------------------------------------------------
     def set_source(self, s: int, ids, wts, payload_rows: Sequence):
@@ -163,6 +173,128 @@ class LogicalEP:
         destination."""
         for y in self.Y_lanes[1:]:
             y.copy_(self.Y)
+
+    # -- the layer around the path ---------------------------------------
+    def set_layer(self, w13: torch.Tensor, w2: torch.Tensor,
+                  w13_scale: Optional[torch.Tensor] = None,
+                  w2_scale: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, route: Optional[dict] = None,
+                  shared13: Optional[torch.Tensor] = None,
+                  shared2: Optional[torch.Tensor] = None):
+        """The weights of a layer whose step() then runs whole.
+
+        w13 [E, 2I, H] (gate rows, then up rows), w2 [E, H, I]: every rank's
+        experts, bf16; or, where the pack quantises payload 0 to fp8 in
+        groups of 128, e4m3 codes with block scales w13_scale
+        [E, 2 ceil(I/128), H/128] and w2_scale [E, ceil(H/128), I/128].
+        gate: bf16 [E, H], the router (without it the ids and weights of
+        set_source stand); route: further arguments of moe_ep_route_topk
+        (score, bias, n_group, topk_group, renormalize, scale). shared13
+        [2S, H], shared2 [H, S]: bf16, the expert that every token passes
+        through."""
+        fp8 = self.quant_group is not None
+        if self.quant_fp4 or (fp8 and self.quant_group != B.SCALE_BLOCK):
+            raise ValueError("the experts take bf16 rows or fp8 rows in groups of 128")
+        if self.row_bytes[0] != 2 * self.H:
+            raise ValueError("the layer needs payload 0 = bf16 [T, H]")
+        if w13.dim() != 3 or w13.size(0) != self.E or w13.size(1) % 2:
+            raise ValueError("w13 must be [E, 2I, H]")
+        inter = w13.size(1) // 2
+        if tuple(w13.shape) != (self.E, 2 * inter, self.H) or \
+                tuple(w2.shape) != (self.E, self.H, inter):
+            raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
+        if fp8 != (w13_scale is not None) or fp8 != (w2_scale is not None):
+            raise ValueError("block scales go with rows that the pack quantises")
+        if (shared13 is None) != (shared2 is None):
+            raise ValueError("shared13 and shared2 go together")
+        el, ecap, dev = self.e_local, self.expert_cap, self.device
+        layer = dict(w13=w13, w2=w2, w13_scale=w13_scale, w2_scale=w2_scale, gate=gate,
+                     route=dict(route or {}), shared13=shared13, shared2=shared2)
+        if fp8:
+            layer["hidden"] = [
+                (torch.empty((el, ecap, inter), dtype=torch.uint8, device=dev),
+                 torch.empty((el, ecap, B.scale_pitch(inter, B.SCALE_BLOCK)), device=dev))
+                for _ in range(self.lanes)]
+        else:
+            layer["hidden"] = [torch.empty((el, ecap, inter), dtype=torch.bfloat16, device=dev)
+                               for _ in range(self.lanes)]
+        if gate is not None:
+            layer["logits"] = torch.empty((self.W, self.T, self.E), device=dev)
+        if shared13 is not None:
+            layer["shared"] = [torch.empty((self.T, shared13.size(0) // 2),
+                                           dtype=torch.bfloat16, device=dev)
+                               for _ in range(self.lanes)]
+        self._layer = layer
+        self._calls = {}
+
+    def _source_rows(self, s: int):
+        return self.src[0][s].view(torch.bfloat16).view(self.T, self.H)
+
+    def _prep_route(self, s: int):
+        y = self._layer
+        return (B.prepare_matmul(self._source_rows(s), y["gate"], y["logits"][s]),
+                B.prepare_route_topk(y["logits"][s], self.ids[s], self.wts[s], **y["route"]))
+
+    def _prep_experts(self, r: int):
+        y, lane = self._layer, r % self.lanes
+        mine = slice(r * self.e_local, (r + 1) * self.e_local)
+        w13, w2, cnt = y["w13"][mine], y["w2"][mine], self.expert_num_tokens[r]
+        b, Y, h = self.b_lanes[lane], self.Y_lanes[lane], y["hidden"][lane]
+        if self.quant_group is None:
+            return (B.prepare_expert_matmul(b[0].view(torch.bfloat16), w13, cnt, h, "silu_gated"),
+                    B.prepare_expert_matmul(h, w2, cnt, Y))
+        return (B.prepare_expert_matmul_fp8(b[0], b[1].view(torch.float32), w13,
+                                            y["w13_scale"][mine], cnt, h[0], "silu_gated",
+                                            out_scale=h[1]),
+                B.prepare_expert_matmul_fp8(h[0], h[1], w2, y["w2_scale"][mine], cnt, Y))
+
+    def _prep_shared(self, s: int):
+        y = self._layer
+        h = y["shared"][s % self.lanes]
+        return (B.prepare_matmul(self._source_rows(s), y["shared13"], h, "silu_gated"),
+                B.prepare_matmul(h, y["shared2"], self.out[s], residual=self.out[s]))
+
+    def route(self, s: int, stream=None):
+        """The router of source rank s: its rows' logits, then ids and wts."""
+        for call in self._prepared("route", s):
+            call(stream)
+
+    def experts(self, r: int, stream=None):
+        """The experts of destination rank r, from its lane's batched rows to
+        its lane's Y."""
+        for call in self._prepared("experts", r):
+            call(stream)
+
+    def shared(self, s: int, stream=None):
+        """Adds the expert of all tokens to source rank s's out."""
+        for call in self._prepared("shared", s):
+            call(stream)
+
+    # the three parts of a step, for one rank, in the order of its lane
+    def _send(self, s: int, stream=None):
+        if self._layer is not None and self._layer["gate"] is not None:
+            self.route(s, stream)
+        self.pack(s, stream)
+
+    def _serve(self, r: int, fused_local: bool, stream=None):
+        self.batch(r, stream)
+        if self._layer is not None:
+            if fused_local:
+                raise ValueError("the fused combine reads each rank's own expert outputs, "
+                                 "and here the ranks of a lane share one buffer of them")
+            self.experts(r, stream)
+        if fused_local:
+            self.reduce_peers(r, stream)
+        else:
+            self.reduce(r, stream)
+
+    def _finish(self, s: int, fused_local: bool, stream=None):
+        if fused_local:
+            self.unpack_fused(s, stream)
+        else:
+            self.unpack(s, stream)
+        if self._layer is not None and self._layer["shared13"] is not None:
+            self.shared(s, stream)
 
     # -- the four calls for one logical rank ----------------------------
     # Each call is marshalled once (binding.prepare_*) and replayed; the
@@ -283,7 +415,9 @@ class LogicalEP:
     def step(self, stream=None, fused_local=False, streams=None):
         """One pass of the whole path over all W logical ranks: W packs,
         then batch + reduce per destination (reusing its lane's b and Y),
-        then W unpacks. fused_local: each rank's local slice is combined by
+        then W unpacks; with set_layer() of the whole layer: the router in
+        front of each pack, the experts between batch and reduce, the expert
+        of all tokens behind each unpack. fused_local: each rank's local slice is combined by
         the fused unpack (its lane's Y stands in for the rank's own expert
         output). streams: one HIP stream per lane; rank i's calls go to
         streams[i % lanes], and each phase starts on every stream only
@@ -310,22 +444,15 @@ class LogicalEP:
             for st in streams:
                 st.wait_event(fork)
         for s in range(self.W):
-            self.pack(s, lane_of[s])
+            self._send(s, lane_of[s])
         if streams is not None:
             self._join(streams, 0)
         for r in range(self.W):
-            self.batch(r, lane_of[r])
-            if fused_local:
-                self.reduce_peers(r, lane_of[r])
-            else:
-                self.reduce(r, lane_of[r])
+            self._serve(r, fused_local, lane_of[r])
         if streams is not None:
             self._join(streams, 1)
         for s in range(self.W):
-            if fused_local:
-                self.unpack_fused(s, lane_of[s])
-            else:
-                self.unpack(s, lane_of[s])
+            self._finish(s, fused_local, lane_of[s])
         if streams is not None:
             for st, ev in zip(streams, self._lane_events("end", len(streams))):
                 ev.record(st)
@@ -341,17 +468,11 @@ class LogicalEP:
     def _phase_calls(self, phase: int, lane: int, fused_local: bool):
         for i in range(lane, self.W, self.lanes):
             if phase == 0:
-                self.pack(i)
+                self._send(i)
             elif phase == 1:
-                self.batch(i)
-                if fused_local:
-                    self.reduce_peers(i)
-                else:
-                    self.reduce(i)
-            elif fused_local:
-                self.unpack_fused(i)
+                self._serve(i, fused_local)
             else:
-                self.unpack(i)
+                self._finish(i, fused_local)
 
     def capture_lane_graphs(self, fused_local=False):
         """Captures the lane graphs (after one eager step, so that every call
