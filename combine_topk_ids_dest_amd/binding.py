@@ -352,25 +352,51 @@ class PreparedCall:
     tensor must be on one GPU (the library takes device pointers only), and
     the stream of a call must belong to that GPU."""
 
+    __slots__ = ("name", "fn", "args", "keep", "device")
+
     def __init__(self, name: str, args: tuple, keep: tuple):
-        devices = {t.get_device() for t in _tensors(keep)}      # -1: not a GPU
-        if len(devices) > 1 or -1 in devices:
-            raise ValueError(f"{name}: every tensor must be on one GPU, got "
-                             f"{sorted({str(t.device) for t in _tensors(keep)})}")
-        self.device = devices.pop() if devices else None
+        device = None
+        for t in keep:
+            if isinstance(t, torch.Tensor):
+                d = t.get_device()                  # -1: not a GPU
+                if d != device:
+                    if device is not None or d < 0:
+                        self._refuse(name, keep)
+                    device = d
+            elif t is not None:
+                for u in _tensors((t,)):
+                    d = u.get_device()
+                    if d < 0 or (device is not None and d != device):
+                        self._refuse(name, keep)
+                    device = d
+        self.device = device
         self.name = name
         self.fn = getattr(_lib or load(), name)
         self.args = args
         self.keep = keep
 
+    @staticmethod
+    def _refuse(name: str, keep: tuple):
+        raise ValueError(f"{name}: every tensor must be on one GPU, got "
+                         f"{sorted({str(t.device) for t in _tensors(keep)})}")
+
     def __call__(self, stream=None) -> None:
-        if self.device is not None and not isinstance(stream, int):
-            dev = (torch.cuda.current_device() if stream is None
-                   else stream.device.index)
-            if dev != self.device:
-                raise ValueError(f"{self.name}: the stream is on cuda:{dev}, the "
-                                 f"tensors on cuda:{self.device}")
-        _check(self.name, self.fn(*self.args, _stream(stream)))
+        if stream is None:
+            dev = torch.cuda.current_device()
+            if self.device is not None and dev != self.device:
+                self._wrong_device(dev)
+            status = self.fn(*self.args, torch._C._cuda_getCurrentRawStream(dev))
+        else:
+            if self.device is not None and not isinstance(stream, int) and \
+                    stream.device.index != self.device:
+                self._wrong_device(stream.device.index)
+            status = self.fn(*self.args, _stream(stream))
+        if status != OK:
+            _check(self.name, status)
+
+    def _wrong_device(self, dev: int):
+        raise ValueError(f"{self.name}: the stream is on cuda:{dev}, the "
+                         f"tensors on cuda:{self.device}")
 
 
 def _tensors(x) -> list:
@@ -866,13 +892,11 @@ def _rows_dense(t: torch.Tensor, first: int, name: str):
 
 def _lead_stride(t: torch.Tensor) -> int:
     """Elements between the blocks along dim 0 (a single block: its size, as
-    the stride of a dim of one may be anything)."""
-    if t.size(0) > 1:
+    the stride of a dim of one may be anything; none: what a row holds)."""
+    n = t.size(0)
+    if n > 1:
         return t.stride(0)
-    n = 1
-    for x in t.shape[1:]:
-        n *= x
-    return n
+    return t.numel() if n else max(t.stride(0), 1)
 
 
 def prepare_route_topk(logits: torch.Tensor, topk_ids: torch.Tensor,

@@ -387,7 +387,7 @@ __device__ __forceinline__ void small_tiles(const MatmulArgs& a, uint8_t* lds, i
 }
 
 // ---------------------------------------------------------------------
-// Big tiles: BM (256, 128 or 64) rows of x by 256 rows of w. Eight waves in
+// Big tiles: BM (128 to 256) rows of x by 256 rows of w. Eight waves in
 // two rows of four, each with BM / 2 x 64 of the sums in registers. Slabs of
 // 128 bytes of k go from memory straight into LDS (no register is spent on a
 // load in flight), one to three slabs ahead of the one being multiplied.
@@ -415,9 +415,9 @@ constexpr int kScaleAt = kLds - kScaleLds;
 // (256 rows: with two slabs of each, a slab's time is below HBM's loaded
 // latency of about 2 us, and the products wait for the weights.)
 template <int EB, int BM>
-constexpr int kStagesX = BM > 128 ? 2 : EB == 2 && BM == 64 ? 4 : 3;
+constexpr int kStagesX = BM > 128 ? 2 : 3;
 template <int EB, int BM>
-constexpr int kStagesW = EB == 2 ? (BM == 64 ? 4 : 3) : (BM > 128 ? 2 : 3);
+constexpr int kStagesW = EB == 2 ? 3 : BM > 128 ? 2 : 3;
 
 // Row of w behind row r of a tile whose first output column is n0, and its
 // output column n (columns n >= N do not exist). A fragment's row 4 q + t
@@ -454,214 +454,67 @@ __device__ __forceinline__ f32x4 load_f32x4(__amdgpu_buffer_rsrc_t r, uint32_t o
     return __builtin_bit_cast(f32x4, ld_row_buf<false>(r, off));
 }
 
-template <int EB, bool WIDE, bool GATED, int BM>
-__device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
-                                         uint8_t* lds) {
-    constexpr int JF = BM / 32;                   // fragments of x of a wave
-    constexpr int XS = kStagesX<EB, BM>, WS = kStagesW<EB, BM>;
-    constexpr int FX = (BM + 63) / 64;            // loads of x of a wave and slab
-    constexpr int SLAB_X = FX * 64 * kSlab;
-    constexpr int AT_W = XS * SLAB_X;             // slabs of w behind those of x
-    constexpr int FETCH = FX + 4;
-    static_assert(XS <= WS && AT_W + WS * kBigSlab <= (EB == 1 ? kScaleAt : kLds), "");
+// fp8: a tile's scales in LDS, of four slabs at a time: 16 bytes per row of x,
+// and 4 bytes per slab and block of w (two: runs of 128 columns, or gate and
+// up). Slab s's set is s / 4 & 1.
+template <int EB, bool GATED>
+struct TileScales {
+    static constexpr int kSet = kBig * 16 + 256;
+    i32x4 rx, rw;
+    uint32_t vx, vw, lds0;
+    int nslab, wave;
+
+    __device__ __forceinline__ TileScales(const MatmulArgs& a, int g, int m0, int left, int n0,
+                                          uint32_t lds) {
+        if constexpr (EB == 1) {
+            const int lane = threadIdx.x & 63;
+            wave = uniform(threadIdx.x >> 6);
+            lds0 = lds + kScaleAt;
+            nslab = a.row_bytes / kSlab;
+            const int row = wave * 64 + lane;
+            vx = row < left ? (uint32_t)row * (uint32_t)a.xs_pitch * 4 : kOutside;
+            rx = row_rsrc4(reinterpret_cast<const uint8_t*>(a.xs + g * a.xs_stride +
+                                                            (int64_t)m0 * a.xs_pitch),
+                           (int64_t)left * a.xs_pitch * 4);
+            const int per = (a.N + kScaleBlock - 1) / kScaleBlock;
+            const int b = lane >> 2;
+            const int n = n0 + (GATED ? 0 : b * kScaleBlock);
+            vw = b < 2 && n < a.N ? ((uint32_t)(n / kScaleBlock + (GATED ? b * per : 0)) *
+                                         (uint32_t)nslab +
+                                     (lane & 3)) * 4
+                                  : kOutside;
+            rw = row_rsrc4(reinterpret_cast<const uint8_t*>(a.ws + g * a.ws_stride),
+                           (int64_t)(GATED ? 2 : 1) * per * nslab * 4);
+        }
+    }
+
+    // the four slabs from s on (a multiple of 4)
+    __device__ __forceinline__ void fetch(int s) const {
+        const uint32_t d = lds0 + ((s >> 2) & 1) * kSet;
+        const uint32_t none = s < nslab ? 0u : kOutside;
+        const uint32_t k = s < nslab ? s * 4 : 0;
+        if (wave < kBig / 64) load_to_lds(rx, d + wave * 1024, vx | none, k);
+        if (wave == kWaves - 1)
+            load4_to_lds(rw, d + kBig * 16,
+                         s + (int)(threadIdx.x & 3) < nslab ? vw : kOutside, k);
+    }
+
+    // slab s's: row r's of x at [4 r + s % 4], block b's at [4 kBig + 4 b + s % 4]
+    __device__ __forceinline__ const float* at(const uint8_t* lds, int s) const {
+        return reinterpret_cast<const float*>(lds + kScaleAt + ((s >> 2) & 1) * kSet);
+    }
+};
+
+// The epilogue of a tile: bias, activation, residual and rounding, or the
+// quantising of rows.
+template <int EB, bool WIDE, bool GATED, int JF>
+__device__ __forceinline__ void finish_tile(const MatmulArgs& a, int g, int m0, int left, int n0,
+                                            f32x4 (&acc)[4][JF], uint8_t* lds) {
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    const int kb = a.row_bytes;
-    const int nslab = (kb + kSlab - 1) / kSlab;
-    const int left = rows - m0 < BM ? rows - m0 : BM;
     const int nw = GATED ? 2 * a.N : a.N;
-    const i32x4 rx = row_rsrc4(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
-                               (int64_t)(left - 1) * a.x_row + kb);
-    const i32x4 rw = row_rsrc4(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
-    const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
-
-    // a wave's load i fills rows (i * 8 + wave) * 8 .. + 7
-    const int sub = lane >> 3;
-    const int chunk = (lane & 7) ^ ((((wave & 1) << 3 | sub) >> 1) & 7);
-    uint32_t vx[FX], vw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (i * 8 + wave) * 8 + sub;
-        if (i < FX) vx[i] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk * 16 : kOutside;
-        int n;
-        const int q = wrow<GATED>(r, n0, a.N, n);
-        vw[i] = n < a.N ? (uint32_t)q * (uint32_t)a.w_row + chunk * 16 : kOutside;
-    }
-    // the last slab may be short: its chunks past the end of k load zeros, and
-    // so do slabs past the last
-    const int last = (kb - chunk * 16 + kSlab - 1) / kSlab;
-    auto fetch_x = [&](int i, int s, int stage) {
-        load_to_lds(rx, lds0 + stage * SLAB_X + wave * 1024 + i * 8192,
-                    vx[i] | (s < last ? 0u : kOutside), s < nslab ? s * kSlab : 0);
-    };
-    auto fetch_w = [&](int i, int s, int stage) {
-        load_to_lds(rw, lds0 + AT_W + stage * kBigSlab + wave * 1024 + i * 8192,
-                    vw[i] | (s < last ? 0u : kOutside), s < nslab ? s * kSlab : 0);
-    };
-
-    // fp8: the scales of four slabs at a time, 16 bytes per row of x, and 4
-    // bytes per block of w and slab (at most 4 blocks); slab s's set is s/4 & 1
-    constexpr int SCALES = kBig * 16 + 256;
-    uint32_t vxs = kOutside, vws = kOutside;
-    i32x4 rxs = rx, rws = rw;
-    if constexpr (EB == 1) {
-        const int row = wave * 64 + lane;
-        if (row < left) vxs = (uint32_t)row * (uint32_t)a.xs_pitch * 4;
-        rxs = row_rsrc4(reinterpret_cast<const uint8_t*>(a.xs + g * a.xs_stride +
-                                                         (int64_t)m0 * a.xs_pitch),
-                        (int64_t)left * a.xs_pitch * 4);
-        // block b of the tile: two runs of 128 columns, gated: gate and up
-        const int per = (a.N + kScaleBlock - 1) / kScaleBlock;
-        const int b = lane >> 2;
-        const int n = n0 + (GATED ? 0 : b * kScaleBlock);
-        if (b < 2 && n < a.N)
-            vws = ((uint32_t)(n / kScaleBlock + (GATED ? b * per : 0)) * (uint32_t)nslab +
-                   (lane & 3)) * 4;
-        rws = row_rsrc4(reinterpret_cast<const uint8_t*>(a.ws + g * a.ws_stride),
-                        (int64_t)(GATED ? 2 : 1) * per * nslab * 4);
-    }
-    const uint32_t scales0 = lds0 + kScaleAt;
-    auto fetch_scales = [&](int s) {              // s a multiple of 4
-        const uint32_t d = scales0 + ((s >> 2) & 1) * SCALES;
-        const uint32_t none = s < nslab ? 0u : kOutside;
-        const uint32_t k = s < nslab ? s * 4 : 0;
-        if (wave * 64 < BM) load_to_lds(rxs, d + wave * 1024, vxs | none, k);
-        if (wave == kWaves - 1)
-            load4_to_lds(rws, d + kBig * 16, s + (lane & 3) < nslab ? vws : kOutside, k);
-    };
-
-    const int rd = (lane & 15) * kSlab + (((lane >> 4) ^ ((lane >> 1) & 7)) * 16);
-    const uint8_t* rdx = lds + wm * (JF * 16) * kSlab;
-    const uint8_t* rdw = lds + AT_W + wn * 64 * kSlab;
-    f32x4 acc[4][JF];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < JF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    // The order of the loads is that of a loop started WS slabs early: step v
-    // loads slab v + XS of x, then slab v + WS of w.
-    if constexpr (EB == 1) fetch_scales(0);
-#pragma unroll
-    for (int v = -WS; v < (EB == 2 ? 0 : -1); ++v) {
-#pragma unroll
-        for (int i = 0; i < FX; ++i)
-            if (v + XS >= 0) fetch_x(i, v + XS, v + XS);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) fetch_w(i, v + WS, v + WS);
-    }
-    // Loads behind those of slab s + 1 when step s waits for it.
-    constexpr int LEFT = (XS - 2) * FETCH + (WS > XS ? 4 : 0);
-
-    if constexpr (EB == 2) {
-        // Fragments are read half a slab ahead, so that the reads of one half
-        // run under the products of the other.
-        u32x4 fx[2][JF], fw[2][4];
-        // Multiplies one half while reading half h of the slab at stages ix
-        // and iw, and with FETCHES does step f's loads, in small steps: a wave
-        // issues in order.
-        auto step = [&](const u32x4 (&x)[JF], const u32x4 (&w)[4], int ix, int iw, int h,
-                        u32x4 (&nx)[JF], u32x4 (&nwf)[4], auto fetches, int f, int tx, int tw) {
-            const int o = rd ^ (h * 64);
-#pragma unroll
-            for (int j = 0; j < JF; ++j) {
-                if constexpr (decltype(fetches)::value) {
-#pragma unroll
-                    for (int i = j * FETCH / JF; i < (j + 1) * FETCH / JF; ++i) {
-                        if (i < FX) fetch_x(i, f + XS, tx);
-                        else fetch_w(i - FX, f + WS, tw);
-                    }
-                }
-#pragma unroll
-                for (int i = j * 4 / JF; i < (j + 1) * 4 / JF; ++i)
-                    nwf[i] = *reinterpret_cast<const u32x4*>(rdw + iw * kBigSlab + o + i * 16 * kSlab);
-                nx[j] = *reinterpret_cast<const u32x4*>(rdx + ix * SLAB_X + o + j * 16 * kSlab);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i][j] = mma_bf16(w[i], x[j], acc[i][j]);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
-        wait_and_barrier<LEFT + FETCH>();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            fw[0][i] = *reinterpret_cast<const u32x4*>(rdw + rd + i * 16 * kSlab);
-#pragma unroll
-        for (int j = 0; j < JF; ++j)
-            fx[0][j] = *reinterpret_cast<const u32x4*>(rdx + rd + j * 16 * kSlab);
-        int ix = 0, iw = 0;                       // stages of slab s
-        for (int s = 0; s < nslab; ++s) {
-            step(fx[0], fw[0], ix, iw, 1, fx[1], fw[1], std::false_type{}, 0, 0, 0);
-            // slab s is read; slab s + 1 has arrived
-            wait_and_barrier<LEFT>();
-            const int nix = ix + 1 < XS ? ix + 1 : 0, niw = iw + 1 < WS ? iw + 1 : 0;
-            step(fx[1], fw[1], nix, niw, 0, fx[0], fw[0], std::true_type{}, s, ix, iw);
-            ix = nix;
-            iw = niw;
-        }
-    } else {
-        // Slab by slab: the sums of a slab are complete before they are
-        // scaled, so the halves cannot be taken apart.
-        const int bw = GATED ? 0 : wn >> 1;       // the wave's block (gated: both)
-        static_assert(XS == WS, "");
-        int now = 0;
-        for (int s = 0; s < nslab; ++s) {
-            // slab s and its scales (older than the loads that may still be
-            // in flight) have arrived; slab s - 1 is read
-            wait_and_barrier<LEFT>();
-            const int to = now == 0 ? XS - 1 : now - 1;
-#pragma unroll
-            for (int i = 0; i < FX; ++i) fetch_x(i, s + XS - 1, to);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) fetch_w(i, s + WS - 1, to);
-            if ((s & 3) == 2) fetch_scales((s & ~3) + 4);
-            const float* sc =
-                reinterpret_cast<const float*>(lds + kScaleAt + ((s >> 2) & 1) * SCALES);
-            const float sg = sc[kBig * 4 + bw * 4 + (s & 3)];
-            const float su = GATED ? sc[kBig * 4 + 4 + (s & 3)] : sg;
-            auto frag = [&](const uint8_t* p) {
-                Frag f;
-                f.v[0] = *reinterpret_cast<const u32x4*>(p + rd);
-                f.v[1] = *reinterpret_cast<const u32x4*>(p + (rd ^ 64));
-                return f;
-            };
-            const uint8_t* px = rdx + now * SLAB_X;
-            const uint8_t* pw = rdw + now * kBigSlab;
-            auto scale = [&](int i, int j, f32x4 t, float sx) {
-                const float f = sx * (GATED && (i & 1) ? su : sg);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(t[q], f, acc[i][j][q]);
-            };
-            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (WIDE) {
-                Wide w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = widen(frag(pw + i * 16 * kSlab));
-#pragma unroll
-                for (int j = 0; j < JF; ++j) {
-                    const Wide x = widen(frag(px + j * 16 * kSlab));
-                    const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) scale(i, j, mma_wide(w[i], x, zero), sx);
-                }
-            } else {
-                Frag w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = frag(pw + i * 16 * kSlab);
-#pragma unroll
-                for (int j = 0; j < JF; ++j) {
-                    const Frag x = frag(px + j * 16 * kSlab);
-                    const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) scale(i, j, mma_fp8(w[i], x, zero), sx);
-                }
-            }
-            now = now + 1 < XS ? now + 1 : 0;
-        }
-    }
-    wait_and_barrier<0>();   // LDS is free for what follows
-
-    // Epilogue. A lane has QN quads of consecutive columns from n on, of rows
+    // A lane has QN quads of consecutive columns from n on, of rows
     // 16 (wm JF + j) + lane % 16. Rows and columns that do not exist are
     // outside the buffers' ranges: their loads give 0, their stores nothing.
     constexpr int QN = GATED ? 2 : 4;
@@ -790,12 +643,357 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
     }
 }
 
+template <int EB, bool WIDE, bool GATED, int BM>
+__device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
+                                         uint8_t* lds) {
+    constexpr int JF = BM / 32;                   // fragments of x of a wave
+    constexpr int XS = kStagesX<EB, BM>, WS = kStagesW<EB, BM>;
+    constexpr int FX = (BM + 63) / 64;            // loads of x of a wave and slab
+    constexpr int SLAB_X = FX * 64 * kSlab;
+    constexpr int AT_W = XS * SLAB_X;             // slabs of w behind those of x
+    constexpr int FETCH = FX + 4;
+    static_assert(XS <= WS && AT_W + WS * kBigSlab <= (EB == 1 ? kScaleAt : kLds), "");
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int kb = a.row_bytes;
+    const int nslab = (kb + kSlab - 1) / kSlab;
+    const int left = rows - m0 < BM ? rows - m0 : BM;
+    const int nw = GATED ? 2 * a.N : a.N;
+    const i32x4 rx = row_rsrc4(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
+                               (int64_t)(left - 1) * a.x_row + kb);
+    const i32x4 rw = row_rsrc4(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
+    const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
+
+    // a wave's load i fills rows (i * 8 + wave) * 8 .. + 7
+    const int sub = lane >> 3;
+    const int chunk = (lane & 7) ^ ((((wave & 1) << 3 | sub) >> 1) & 7);
+    uint32_t vx[FX], vw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (i * 8 + wave) * 8 + sub;
+        if (i < FX) vx[i] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk * 16 : kOutside;
+        int n;
+        const int q = wrow<GATED>(r, n0, a.N, n);
+        vw[i] = n < a.N ? (uint32_t)q * (uint32_t)a.w_row + chunk * 16 : kOutside;
+    }
+    // the last slab may be short: its chunks past the end of k load zeros, and
+    // so do slabs past the last
+    const int last = (kb - chunk * 16 + kSlab - 1) / kSlab;
+    auto fetch_x = [&](int i, int s, int stage) {
+        load_to_lds(rx, lds0 + stage * SLAB_X + wave * 1024 + i * 8192,
+                    vx[i] | (s < last ? 0u : kOutside), s < nslab ? s * kSlab : 0);
+    };
+    auto fetch_w = [&](int i, int s, int stage) {
+        load_to_lds(rw, lds0 + AT_W + stage * kBigSlab + wave * 1024 + i * 8192,
+                    vw[i] | (s < last ? 0u : kOutside), s < nslab ? s * kSlab : 0);
+    };
+
+    const TileScales<EB, GATED> scales(a, g, m0, left, n0, lds0);
+
+    const int rd = (lane & 15) * kSlab + (((lane >> 4) ^ ((lane >> 1) & 7)) * 16);
+    const uint8_t* rdx = lds + wm * (JF * 16) * kSlab;
+    const uint8_t* rdw = lds + AT_W + wn * 64 * kSlab;
+    f32x4 acc[4][JF];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < JF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // The order of the loads is that of a loop started WS slabs early: step v
+    // loads slab v + XS of x, then slab v + WS of w.
+    if constexpr (EB == 1) scales.fetch(0);
+#pragma unroll
+    for (int v = -WS; v < (EB == 2 ? 0 : -1); ++v) {
+#pragma unroll
+        for (int i = 0; i < FX; ++i)
+            if (v + XS >= 0) fetch_x(i, v + XS, v + XS);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fetch_w(i, v + WS, v + WS);
+    }
+    // Loads behind those of slab s + 1 when step s waits for it.
+    constexpr int LEFT = (XS - 2) * FETCH + (WS > XS ? 4 : 0);
+
+    if constexpr (EB == 2) {
+        // Fragments are read half a slab ahead, so that the reads of one half
+        // run under the products of the other.
+        u32x4 fx[2][JF], fw[2][4];
+        // Multiplies one half while reading half h of the slab at stages ix
+        // and iw, and with FETCHES does step f's loads, in small steps: a wave
+        // issues in order.
+        auto step = [&](const u32x4 (&x)[JF], const u32x4 (&w)[4], int ix, int iw, int h,
+                        u32x4 (&nx)[JF], u32x4 (&nwf)[4], auto fetches, int f, int tx, int tw) {
+            const int o = rd ^ (h * 64);
+#pragma unroll
+            for (int j = 0; j < JF; ++j) {
+                if constexpr (decltype(fetches)::value) {
+#pragma unroll
+                    for (int i = j * FETCH / JF; i < (j + 1) * FETCH / JF; ++i) {
+                        if (i < FX) fetch_x(i, f + XS, tx);
+                        else fetch_w(i - FX, f + WS, tw);
+                    }
+                }
+#pragma unroll
+                for (int i = j * 4 / JF; i < (j + 1) * 4 / JF; ++i)
+                    nwf[i] = *reinterpret_cast<const u32x4*>(rdw + iw * kBigSlab + o + i * 16 * kSlab);
+                nx[j] = *reinterpret_cast<const u32x4*>(rdx + ix * SLAB_X + o + j * 16 * kSlab);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][j] = mma_bf16(w[i], x[j], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        wait_and_barrier<LEFT + FETCH>();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            fw[0][i] = *reinterpret_cast<const u32x4*>(rdw + rd + i * 16 * kSlab);
+#pragma unroll
+        for (int j = 0; j < JF; ++j)
+            fx[0][j] = *reinterpret_cast<const u32x4*>(rdx + rd + j * 16 * kSlab);
+        int ix = 0, iw = 0;                       // stages of slab s
+        for (int s = 0; s < nslab; ++s) {
+            step(fx[0], fw[0], ix, iw, 1, fx[1], fw[1], std::false_type{}, 0, 0, 0);
+            // slab s is read; slab s + 1 has arrived
+            wait_and_barrier<LEFT>();
+            const int nix = ix + 1 < XS ? ix + 1 : 0, niw = iw + 1 < WS ? iw + 1 : 0;
+            step(fx[1], fw[1], nix, niw, 0, fx[0], fw[0], std::true_type{}, s, ix, iw);
+            ix = nix;
+            iw = niw;
+        }
+    } else {
+        // Slab by slab: the sums of a slab are complete before they are
+        // scaled, so the halves cannot be taken apart.
+        const int bw = GATED ? 0 : wn >> 1;       // the wave's block (gated: both)
+        static_assert(XS == WS, "");
+        int now = 0;
+        for (int s = 0; s < nslab; ++s) {
+            // slab s and its scales (older than the loads that may still be
+            // in flight) have arrived; slab s - 1 is read
+            wait_and_barrier<LEFT>();
+            const int to = now == 0 ? XS - 1 : now - 1;
+#pragma unroll
+            for (int i = 0; i < FX; ++i) fetch_x(i, s + XS - 1, to);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fetch_w(i, s + WS - 1, to);
+            if ((s & 3) == 2) scales.fetch((s & ~3) + 4);
+            const float* sc = scales.at(lds, s);
+            const float sg = sc[kBig * 4 + bw * 4 + (s & 3)];
+            const float su = GATED ? sc[kBig * 4 + 4 + (s & 3)] : sg;
+            auto frag = [&](const uint8_t* p) {
+                Frag f;
+                f.v[0] = *reinterpret_cast<const u32x4*>(p + rd);
+                f.v[1] = *reinterpret_cast<const u32x4*>(p + (rd ^ 64));
+                return f;
+            };
+            const uint8_t* px = rdx + now * SLAB_X;
+            const uint8_t* pw = rdw + now * kBigSlab;
+            auto scale = [&](int i, int j, f32x4 t, float sx) {
+                const float f = sx * (GATED && (i & 1) ? su : sg);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(t[q], f, acc[i][j][q]);
+            };
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (WIDE) {
+                Wide w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = widen(frag(pw + i * 16 * kSlab));
+#pragma unroll
+                for (int j = 0; j < JF; ++j) {
+                    const Wide x = widen(frag(px + j * 16 * kSlab));
+                    const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) scale(i, j, mma_wide(w[i], x, zero), sx);
+                }
+            } else {
+                Frag w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = frag(pw + i * 16 * kSlab);
+#pragma unroll
+                for (int j = 0; j < JF; ++j) {
+                    const Frag x = frag(px + j * 16 * kSlab);
+                    const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) scale(i, j, mma_fp8(w[i], x, zero), sx);
+                }
+            }
+            now = now + 1 < XS ? now + 1 : 0;
+        }
+    }
+    wait_and_barrier<0>();   // LDS is free for what follows
+    finish_tile<EB, WIDE, GATED, JF>(a, g, m0, left, n0, acc, lds);
+}
+
+// ---------------------------------------------------------------------
+// Narrow tiles: up to 64 rows of x by 256 rows of w, bound by the weights'
+// bytes. HBM gives runs of 128 bytes of many rows at 4 to 5 TB/s and runs of
+// 256 bytes at 6 (measured with plain loads of 470 MB), so here k goes by
+// pairs of slabs, and to fit that into LDS with loads in flight the rows of w
+// go by halves: unit u is half u % 2 (fragments 2 h and 2 h + 1 of each wave)
+// of pair u / 2, 128 rows of 256 bytes. Two or three units are on their way
+// while one is multiplied; the fragments of x stay in registers for both
+// halves of a pair.
+//
+// LDS: chunk c of a 256-byte row r is at place c ^ (r & 15): the sets of 16
+// lanes named above meet on no bank.
+// ---------------------------------------------------------------------
+constexpr int kNarrow = 64;
+constexpr int kPair = 2 * kSlab;
+constexpr int kPairX = kNarrow * kPair;
+constexpr int kUnit = 128 * kPair;
+
+template <int EB, bool WIDE, bool GATED>
+__device__ __forceinline__ void narrow_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
+                                            uint8_t* lds) {
+    constexpr int JF = 2;
+    constexpr int WU = EB == 2 ? 4 : 3;           // units of w in LDS
+    constexpr int AT_W = 2 * kPairX;              // behind two pairs of x
+    static_assert(AT_W + WU * kUnit <= (EB == 1 ? kScaleAt : kLds), "");
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    const int kb = a.row_bytes;
+    const int nslab = (kb + kSlab - 1) / kSlab;
+    const int npair = (nslab + 1) / 2;
+    const int left = rows - m0 < kNarrow ? rows - m0 : kNarrow;
+    const int nw = GATED ? 2 * a.N : a.N;
+    const i32x4 rx = row_rsrc4(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
+                               (int64_t)(left - 1) * a.x_row + kb);
+    const i32x4 rw = row_rsrc4(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
+    const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
+
+    // a wave's load i fills rows (i * 8 + wave) * 4 .. + 3
+    const int sub = lane >> 4;
+    const uint32_t chunk = ((lane & 15) ^ ((wave & 3) * 4 + sub)) * 16;
+    uint32_t vx[2], vw[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (i * 8 + wave) * 4 + sub;
+        if (i < 2) vx[i] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk : kOutside;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int n;
+            const int q = wrow<GATED>((r >> 5) * 64 + h * 32 + (r & 31), n0, a.N, n);
+            vw[h][i] = n < a.N ? (uint32_t)q * (uint32_t)a.w_row + chunk : kOutside;
+        }
+    }
+    auto fetch_x = [&](int p) {
+        const uint32_t none = p * kPair + (int)chunk < kb ? 0u : kOutside;
+        const uint32_t k = p * kPair < kb ? p * kPair : 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            load_to_lds(rx, lds0 + (p & 1) * kPairX + (i * 8 + wave) * 1024, vx[i] | none, k);
+    };
+    auto fetch_w = [&](int p, int h, int slot) {
+        const uint32_t none = p * kPair + (int)chunk < kb ? 0u : kOutside;
+        const uint32_t k = p * kPair < kb ? p * kPair : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            load_to_lds(rw, lds0 + AT_W + slot * kUnit + (i * 8 + wave) * 1024, vw[h][i] | none, k);
+    };
+    const TileScales<EB, GATED> scales(a, g, m0, left, n0, lds0);
+
+    const int r = lane & 15;
+    const int rd = r * kPair + (((lane >> 4) ^ r) * 16);
+    const uint8_t* rdx = lds + wm * 32 * kPair;
+    const uint8_t* rdw = lds + AT_W + wn * 32 * kPair;
+    f32x4 acc[4][JF];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < JF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // The order of the loads is that of a loop started three units early: odd
+    // units load x of the pair after the next, then every unit w of the unit
+    // WU - 1 ahead.
+    if constexpr (EB == 1) scales.fetch(0);
+    fetch_x(0);
+    fetch_w(0, 0, 0);
+    if (WU == 4) fetch_w(0, 1, 1);
+    fetch_x(1);
+    if (WU == 4) fetch_w(1, 0, 2);
+    else fetch_w(0, 1, 1);
+    int slot = 0;                                 // of unit u
+    u32x4 x[JF][4];
+    for (int p = 0; p < npair; ++p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // unit u (and x of its pair, older) has arrived: behind it are the
+            // units after it and the x asked for between them
+            if (h == 0) wait_and_barrier<WU == 4 ? 10 : 6>();
+            else wait_and_barrier<WU == 4 ? 10 : 4>();
+            const int to = slot == 0 ? WU - 1 : slot - 1;
+            if (EB == 1 && h == 0 && (p & 1)) scales.fetch(2 * (p + 1));
+            if (h == 1) fetch_x(p + 2);
+            if (WU == 4) fetch_w(h == 0 ? p + 1 : p + 2, 1 - h, to);
+            else fetch_w(p + 1, h, to);
+            if (h == 0) {
+#pragma unroll
+                for (int j = 0; j < JF; ++j)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        x[j][t] = *reinterpret_cast<const u32x4*>(
+                            rdx + (p & 1) * kPairX + j * 16 * kPair + (rd ^ (t * 64)));
+            }
+            u32x4 w[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    w[i][t] = *reinterpret_cast<const u32x4*>(rdw + slot * kUnit + i * 16 * kPair +
+                                                              (rd ^ (t * 64)));
+            if constexpr (EB == 2) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < JF; ++j)
+                            acc[2 * h + i][j] = mma_bf16(w[i][t], x[j][t], acc[2 * h + i][j]);
+            } else {
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    const int sl = 2 * p + d;
+                    const float* sc = scales.at(lds, sl);
+                    const bool in = sl < nslab;   // a scale row's padding may hold anything
+                    Frag f[2], fx[JF];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        f[i].v[0] = w[i][2 * d];
+                        f[i].v[1] = w[i][2 * d + 1];
+                    }
+#pragma unroll
+                    for (int j = 0; j < JF; ++j) {
+                        fx[j].v[0] = x[j][2 * d];
+                        fx[j].v[1] = x[j][2 * d + 1];
+                        const float sx = sc[(wm * 32 + j * 16 + r) * 4 + (sl & 3)];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                            const f32x4 t = WIDE ? mma_wide(widen(f[i]), widen(fx[j]), zero)
+                                                 : mma_fp8(f[i], fx[j], zero);
+                            const float b = sc[kBig * 4 + (GATED ? i : wn >> 1) * 4 + (sl & 3)];
+                            const float v = in ? sx * b : 0.f;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                acc[2 * h + i][j][q] =
+                                    __builtin_fmaf(t[q], v, acc[2 * h + i][j][q]);
+                        }
+                    }
+                }
+            }
+            slot = slot + 1 < WU ? slot + 1 : 0;
+        }
+    }
+    wait_and_barrier<0>();   // LDS is free for what follows
+    finish_tile<EB, WIDE, GATED, JF>(a, g, m0, left, n0, acc, lds);
+}
+
 // ---------------------------------------------------------------------
 // The work list. A group's rows are cut into equal runs of at most 256 rows (a
 // multiple of 32), so that a group's weights are read by all of its runs at the
 // same time, side by side on one XCD, and from HBM once. (Whole runs of 256 and
 // a remainder read them twice: 1.7 times the bytes at 32 experts of 240 to 1280
-// rows, 1066 against 835 us for 32 experts of 7168 -> 2 x 2048.) Groups of up to small_to rows get small tiles.
+// rows, 1066 against 835 us for products of 7168 columns with 2 x 2048 rows.)
+// Groups of up to small_to rows get small tiles.
 //
 // Tiles are dealt out longest runs first, one to a block and round, one block
 // per CU. Every block computes its share from the counts for itself: there is
@@ -948,7 +1146,7 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
         else if (jf > 5) run(std::integral_constant<int, 192>{});
         else if (jf > 4) run(std::integral_constant<int, 160>{});
         else if (jf > 2) run(std::integral_constant<int, 128>{});
-        else run(std::integral_constant<int, 64>{});
+        else narrow_tile<EB, WIDE, GATED>(a, at.g, m0, end, n0, lds);
     }
     if (nsmall > 0)
         small_tiles<EB, WIDE, GATED>(a, lds, nsmall, [&](int t) {
