@@ -420,18 +420,19 @@ template <int EB, int BM>
 constexpr int kStagesW = EB == 2 ? 3 : BM > 128 ? 2 : 3;
 
 // Row of w behind row r of a tile whose first output column is n0, and its
-// output column n (columns n >= N do not exist). A fragment's row 4 q + t
-// becomes the sums t of the lanes 16 q ..: fragment i of a wave holds the
-// columns 16 q + 4 i + t, gated fragments 2 p + h the gate (h = 0) and up
-// rows of the columns 8 q + 4 p + t.
-template <bool GATED>
+// output column n (columns n >= N do not exist). A wave has FRAGS fragments of
+// 16 rows. A fragment's row 4 q + t becomes the sums t of the lanes 16 q ..;
+// with four, fragment i of a wave holds the columns 16 q + 4 i + t, gated
+// fragments 2 p + h the gate (h = 0) and up rows of the columns 8 q + 4 p + t.
+template <bool GATED, int FRAGS>
 __device__ __forceinline__ int wrow(int r, int n0, int N, int& n) {
-    const int i = (r >> 4) & 3, q = (r >> 2) & 3, t = r & 3;
+    const int i = (r >> 4) & (FRAGS - 1), q = (r >> 2) & 3, t = r & 3;
+    const int wave = r / (FRAGS * 16);
     if (!GATED) {
-        n = n0 + (r & ~63) + q * 16 + i * 4 + t;
+        n = n0 + wave * FRAGS * 16 + q * FRAGS * 4 + i * 4 + t;
         return n;
     }
-    n = n0 + (r >> 6) * 32 + q * 8 + (i >> 1) * 4 + t;
+    n = n0 + wave * FRAGS * 8 + q * FRAGS * 2 + (i >> 1) * 4 + t;
     return (i & 1) ? N + n : n;
 }
 
@@ -507,18 +508,18 @@ struct TileScales {
 
 // The epilogue of a tile: bias, activation, residual and rounding, or the
 // quantising of rows.
-template <int EB, bool WIDE, bool GATED, int JF>
+template <int EB, bool WIDE, bool GATED, int FRAGS, int JF, int WN>
 __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int g, int m0, int left, int n0,
-                                            f32x4 (&acc)[4][JF], uint8_t* lds) {
+                                            f32x4 (&acc)[FRAGS][JF], uint8_t* lds) {
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / WN, wn = wave % WN;
     const int nw = GATED ? 2 * a.N : a.N;
     // A lane has QN quads of consecutive columns from n on, of rows
     // 16 (wm JF + j) + lane % 16. Rows and columns that do not exist are
     // outside the buffers' ranges: their loads give 0, their stores nothing.
-    constexpr int QN = GATED ? 2 : 4;
-    const int n = n0 + (GATED ? wn * 32 + (lane >> 4) * 8 : wn * 64 + (lane >> 4) * 16);
+    constexpr int QN = GATED ? FRAGS / 2 : FRAGS;
+    const int n = n0 + wn * QN * 16 + (lane >> 4) * QN * 4;
     if (a.bias) {
         const auto rb = row_rsrc(reinterpret_cast<const uint8_t*>(a.bias + g * a.bias_stride),
                                  (int64_t)nw * 4);
@@ -613,12 +614,25 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int g, int m0, 
         }
         return;
     }
+    if constexpr (QN == 1) {
+#pragma unroll
+        for (int j = 0; j < JF; ++j) {
+            f32x4 y = value(0, j);
+            if (a.res) {
+                const u32x2 v = __builtin_bit_cast(
+                    u32x2, __builtin_amdgcn_raw_buffer_load_b64(rr, at(j, 0, a.res_row), 0, 0));
+                y += f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+            }
+            __builtin_amdgcn_raw_buffer_store_b64(pack_bf16(y), ro, at(j, 0, a.out_row), 0, 0);
+        }
+        return;
+    }
     // bf16: N is a multiple of 8, so eight columns exist together; the
     // residuals of four rows are on their way at once
     constexpr int JB = JF < 4 ? JF : 4;
 #pragma unroll
     for (int j0 = 0; j0 < JF; j0 += JB) {
-        u32x4 r[JB][QN / 2];
+        u32x4 r[JB][QN < 2 ? 1 : QN / 2];
         if (a.res) {
 #pragma unroll
             for (int j = 0; j < JB && j0 + j < JF; ++j)
@@ -674,7 +688,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
         const int r = (i * 8 + wave) * 8 + sub;
         if (i < FX) vx[i] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk * 16 : kOutside;
         int n;
-        const int q = wrow<GATED>(r, n0, a.N, n);
+        const int q = wrow<GATED, 4>(r, n0, a.N, n);
         vw[i] = n < a.N ? (uint32_t)q * (uint32_t)a.w_row + chunk * 16 : kOutside;
     }
     // the last slab may be short: its chunks past the end of k load zeros, and
@@ -819,7 +833,7 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
         }
     }
     wait_and_barrier<0>();   // LDS is free for what follows
-    finish_tile<EB, WIDE, GATED, JF>(a, g, m0, left, n0, acc, lds);
+    finish_tile<EB, WIDE, GATED, 4, JF, 4>(a, g, m0, left, n0, acc, lds);
 }
 
 // ---------------------------------------------------------------------
@@ -871,7 +885,7 @@ __device__ __forceinline__ void narrow_tile(const MatmulArgs& a, int g, int m0, 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             int n;
-            const int q = wrow<GATED>((r >> 5) * 64 + h * 32 + (r & 31), n0, a.N, n);
+            const int q = wrow<GATED, 4>((r >> 5) * 64 + h * 32 + (r & 31), n0, a.N, n);
             vw[h][i] = n < a.N ? (uint32_t)q * (uint32_t)a.w_row + chunk : kOutside;
         }
     }
@@ -984,7 +998,119 @@ __device__ __forceinline__ void narrow_tile(const MatmulArgs& a, int g, int m0, 
         }
     }
     wait_and_barrier<0>();   // LDS is free for what follows
-    finish_tile<EB, WIDE, GATED, JF>(a, g, m0, left, n0, acc, lds);
+    finish_tile<EB, WIDE, GATED, 4, JF, 4>(a, g, m0, left, n0, acc, lds);
+}
+
+// ---------------------------------------------------------------------
+// Middle tiles, for products whose 256-column tiles would leave most CUs idle
+// (the router's logits, some rows of a few experts): 64 rows of x by 64 of w
+// or 128 by 128, rings of pairs of slabs. What they reach goes by the bytes of
+// weights on their way (HBM's latency under load is about 3 us): four pairs of
+// 16 KB of a CU give 5.5 TB/s, three 3.7. Half of the waves load x, half w: a
+// wave's loads complete in order, so a wave that loaded both would wait for the
+// weights of pairs to come before the rows of the pair at hand, which come from
+// nearer.
+// ---------------------------------------------------------------------
+template <bool GATED, int BM>
+__device__ __forceinline__ void mid_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
+                                         uint8_t* lds) {
+    constexpr int WN = BM == 64 ? 2 : 4;          // waves over the rows of w
+    constexpr int JF = BM * WN / 128;             // fragments of x of a wave
+    constexpr int XR = BM == 64 ? 5 : 2, WR = BM == 64 ? 5 : 3;     // pairs in LDS
+    constexpr int NX = BM / 16;                   // loads of a wave per pair, of x or w
+    constexpr int PAIR = BM * kPair;
+    constexpr int AT_W = XR * PAIR;
+    static_assert(AT_W + WR * PAIR <= kLds, "");
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const bool is_x = wave < 4;
+    const int kb = a.row_bytes;
+    const int npair = (kb + kPair - 1) / kPair;
+    const int left = rows - m0 < BM ? rows - m0 : BM;
+    const int nw = GATED ? 2 * a.N : a.N;
+    const i32x4 rx = row_rsrc4(a.x + g * a.x_stride + (int64_t)m0 * a.x_row,
+                               (int64_t)(left - 1) * a.x_row + kb);
+    const i32x4 rw = row_rsrc4(a.w + g * a.w_stride, (int64_t)(nw - 1) * a.w_row + kb);
+    const i32x4 rs = is_x ? rx : rw;
+    const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
+
+    // a wave's load i fills rows (i * 4 + wave % 4) * 4 .. + 3
+    const int sub = lane >> 4;
+    const uint32_t chunk = ((lane & 15) ^ ((wave & 3) * 4 + sub)) * 16;
+    uint32_t v[NX];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) {
+        const int r = (i * 4 + (wave & 3)) * 4 + sub;
+        if (is_x) {
+            v[i] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk : kOutside;
+        } else {
+            int n;
+            const int q = wrow<GATED, 2>(r, n0, a.N, n);
+            v[i] = n < a.N ? (uint32_t)q * (uint32_t)a.w_row + chunk : kOutside;
+        }
+    }
+    const int ahead = (is_x ? XR : WR) - 1;
+    const uint32_t ring = lds0 + (is_x ? 0 : AT_W) + (wave & 3) * 1024;
+    auto fetch = [&](int p, int slot) {
+        const uint32_t none = p * kPair + (int)chunk < kb ? 0u : kOutside;
+        const uint32_t k = p * kPair < kb ? p * kPair : 0;
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+            load_to_lds(rs, ring + slot * PAIR + i * 4096, v[i] | none, k);
+    };
+    const int r = lane & 15;
+    const int rd = r * kPair + (((lane >> 4) ^ r) * 16);
+    const uint8_t* rdx = lds + wm * JF * 16 * kPair;
+    const uint8_t* rdw = lds + AT_W + wn * 32 * kPair;
+    f32x4 acc[2][JF];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < JF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < ahead; ++p) fetch(p, p);
+    int ix = 0, iw = 0;                           // slots of pair p
+    for (int p = 0; p < npair; ++p) {
+        // pair p has arrived; p - 1 is read
+        if (is_x) wait_and_barrier<(XR - 2) * NX>();
+        else wait_and_barrier<(WR - 2) * NX>();
+        fetch(p + ahead, is_x ? (ix == 0 ? XR - 1 : ix - 1) : (iw == 0 ? WR - 1 : iw - 1));
+        u32x4 x[JF][4], w[2][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int j = 0; j < JF; ++j)
+                x[j][t] = *reinterpret_cast<const u32x4*>(rdx + ix * PAIR + j * 16 * kPair +
+                                                          (rd ^ (t * 64)));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                w[i][t] = *reinterpret_cast<const u32x4*>(rdw + iw * PAIR + i * 16 * kPair +
+                                                          (rd ^ (t * 64)));
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < JF; ++j) acc[i][j] = mma_bf16(w[i][t], x[j][t], acc[i][j]);
+        ix = ix + 1 < XR ? ix + 1 : 0;
+        iw = iw + 1 < WR ? iw + 1 : 0;
+    }
+    wait_and_barrier<0>();   // LDS is free for the next tile
+    finish_tile<2, false, GATED, 2, JF, WN>(a, g, m0, left, n0, acc, lds);
+}
+
+template <bool GATED, int BM>
+__global__ __launch_bounds__(kThreads, 2) void mid_kernel(const MatmulArgs a) {
+    __shared__ __align__(1024) uint8_t lds[kLds];
+    constexpr int BO = GATED ? BM / 2 : BM;
+    const int mt = (a.rows + BM - 1) / BM;
+    const int total = mt * ((a.N + BO - 1) / BO);
+    for (int t0 = 0; t0 < total; t0 += gridDim.x) {
+        const int t = tile_of(blockIdx.x, gridDim.x, total - t0);
+        if (t < 0) break;        // a last, partial round
+        mid_tile<GATED, BM>(a, 0, (t0 + t) % mt * BM, a.rows, (t0 + t) / mt * BO, lds);
+    }
 }
 
 // ---------------------------------------------------------------------
@@ -1002,6 +1128,8 @@ __device__ __forceinline__ void narrow_tile(const MatmulArgs& a, int g, int m0, 
 constexpr int kGrid = 256;                       // blocks
 constexpr int kGroup = 8;                        // runs of rows side by side
 constexpr int kKinds = 9;                        // runs of 32 k rows, k = 1..8; small: 0
+constexpr int kRuns64 = kKinds;                  // every group in runs of 64 rows,
+constexpr int kRuns128 = kKinds + 1;             // or of 128 (but for small ones)
 
 struct Cut {
     int runs, kind;
@@ -1017,6 +1145,16 @@ __device__ __forceinline__ Cut cut_rows(int rows, int small_to) {
     c.runs = (rows + 255) / 256;
     c.kind = ((rows + c.runs - 1) / c.runs + 31) / 32;
     return c;
+}
+
+// A group's runs of a kind.
+__device__ __forceinline__ int runs_of(int rows, int small_to, int kind) {
+    const Cut c = cut_rows(rows, small_to);
+    if (kind >= kRuns64) {
+        const int run = kind == kRuns64 ? 64 : 128;
+        return c.kind ? (rows + run - 1) / run : 0;
+    }
+    return c.kind == kind ? c.runs : 0;
 }
 
 // The rows of the groups g0 + lane (0 past the last).
@@ -1062,8 +1200,7 @@ __device__ __forceinline__ Place find_tile(const MatmulArgs& a, int rows0, int s
                                            int nt, int t) {
     for (int g0 = 0;; g0 += 64) {
         const int rows = g0 ? lane_rows(a, g0) : rows0;
-        const Cut c = cut_rows(rows, small_to);
-        const int n = c.kind == kind ? nt * c.runs : 0;
+        const int n = nt * runs_of(rows, small_to, kind);
         const int32_t inc = wave_inclusive_scan(n);
         const uint64_t behind = __ballot(inc > t);
         if (behind || g0 + 64 >= a.groups) {     // t is below the total: a lane is found
@@ -1102,6 +1239,40 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
         small_to = 0;
     }
     const int nsmall = n[0] * nt;
+    if constexpr (EB == 2) {
+        // Few enough of them that even cut in parts they would leave CUs idle
+        // or share their weights' bytes among them: middle tiles, where one
+        // round does (8 experts of 115 rows, 7168 -> 2 x 2048: 106 us with them,
+        // 112 without; one of 200: 29 and 62).
+        constexpr int G = GATED ? 2 : 1;
+        const int nt64 = (a.N * G + 63) / 64, nt128 = (a.N * G + 127) / 128;
+        if (total > 0 && total <= kGrid / 2) {
+            int runs64 = 0, runs128 = 0;
+            for (int g0 = 0; g0 < a.groups; g0 += 64) {
+                const int rows = g0 ? lane_rows(a, g0) : rows0;
+                runs64 += __builtin_amdgcn_readlane(
+                    wave_inclusive_scan(runs_of(rows, small_to, kRuns64)), 63);
+                runs128 += __builtin_amdgcn_readlane(
+                    wave_inclusive_scan(runs_of(rows, small_to, kRuns128)), 63);
+            }
+            const int kind = runs64 * nt64 <= kGrid    ? kRuns64
+                             : runs128 * nt128 <= kGrid ? kRuns128
+                                                        : 0;
+            if (kind) {
+                const bool wide = kind == kRuns128;
+                const int tiles = wide ? runs128 * nt128 : runs64 * nt64;
+                const int t = tile_of(blockIdx.x, kGrid, tiles);
+                if (t >= 0) {
+                    const Place at = find_tile(a, rows0, small_to, kind, wide ? nt128 : nt64, t);
+                    const int mt = runs_of(at.rows, small_to, kind);
+                    const int m = at.l % mt, c = at.l / mt;
+                    if (wide) mid_tile<GATED, 128>(a, at.g, m * 128, at.rows, c * (128 / G), lds);
+                    else mid_tile<GATED, 64>(a, at.g, m * 64, at.rows, c * (64 / G), lds);
+                }
+                total = 0;
+            }
+        }
+    }
     const int whole = total / kGrid * kGrid;
     // The last, partial round: with at most half (a quarter) as many tiles as
     // blocks, each tile is cut in two (four) by its rows. 3.5 rounds then take
@@ -1172,21 +1343,56 @@ __global__ __launch_bounds__(kThreads, 2) void small_kernel(const MatmulArgs a) 
     });
 }
 
+// What a product over all tokens takes with each kind of tile, in us, from the
+// tiles' measured times: rounds of the grid times a tile's start and its pairs
+// of slabs.
+struct Estimate {
+    double small, mid64, mid128, big;
+};
+
+Estimate estimate(int64_t rows, int64_t nw, int64_t row_bytes) {
+    const double pairs = (double)((row_bytes + 2 * kSlab - 1) / (2 * kSlab));
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    Estimate e;
+    e.small = (double)up(up(rows, kSmall) * up(nw, kSmall), kGrid) * (2.0 + 0.125 * pairs);
+    e.mid64 = (double)up(up(rows, 64) * up(nw, 64), kGrid) * (2.5 + 0.45 * pairs);
+    e.mid128 = (double)up(up(rows, 128) * up(nw, 128), kGrid) * (2.5 + 0.93 * pairs);
+    // a tile of 32 j rows takes 0.75 + 0.27 j us a pair
+    const int64_t runs = up(rows, 256), tiles = runs * up(nw, kBig), rest = tiles % kGrid;
+    const int64_t j = up(up(rows, runs), 32);
+    const int64_t last = rest * 4 <= kGrid ? up(j, 4) : rest * 2 <= kGrid ? up(j, 2) : j;
+    e.big = 3.0 + (double)(tiles / kGrid) * (5.0 + (0.75 + 0.27 * (double)j) * pairs) +
+            (rest ? 5.0 + (0.75 + 0.27 * (double)last) * pairs : 0.0);
+    return e;
+}
+
 template <int EB, bool WIDE, bool GATED>
 hipError_t launch(const MatmulArgs& a, hipStream_t st) {
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
-    constexpr int BB = GATED ? kBig / 2 : kBig;
+    const bool e4m3 = a.out_dtype == MOE_EP_E4M3;
     const int64_t small =
         (int64_t)a.groups * ((a.rows + kSmall - 1) / kSmall) * ((a.N + BO - 1) / BO);
-    const int64_t runs = (int64_t)a.groups * ((a.rows + 63) / 64) * ((a.N + BB - 1) / BB);
-    const bool e4m3 = a.out_dtype == MOE_EP_E4M3;
-    const bool few = !e4m3 && (a.counts ? a.rows <= 2 * kSmall : a.rows <= kSmall || runs < 64);
-    if (!few) {
-        matmul_kernel<EB, WIDE, GATED>
-            <<<kGrid, kThreads, 0, st>>>(a, e4m3 || !a.counts ? 0 : kSmall);
-    } else {
+    bool few = !e4m3 && a.counts && a.rows <= 2 * kSmall;
+    if constexpr (EB == 2) {
+        if (!a.counts) {
+            const Estimate e = estimate(a.rows, GATED ? 2 * (int64_t)a.N : a.N, a.row_bytes);
+            const double mid = e.mid64 < e.mid128 ? e.mid64 : e.mid128;
+            few = e.small <= mid && e.small <= e.big;
+            if (!few && mid <= e.big) {
+                if (e.mid64 <= e.mid128)
+                    mid_kernel<GATED, 64><<<kGrid, kThreads, 0, st>>>(a);
+                else
+                    mid_kernel<GATED, 128><<<kGrid, kThreads, 0, st>>>(a);
+                return hipGetLastError();
+            }
+        }
+    }
+    if (few) {
         const int64_t grid = small < kGrid ? (small + 7) / 8 * 8 : kGrid;
         small_kernel<EB, WIDE, GATED><<<(unsigned)grid, kThreads, 0, st>>>(a);
+    } else {
+        matmul_kernel<EB, WIDE, GATED>
+            <<<kGrid, kThreads, 0, st>>>(a, e4m3 || !a.counts ? 0 : kSmall);
     }
     return hipGetLastError();
 }
