@@ -37,7 +37,8 @@ int check_sizes(int32_t groups, int64_t rows, int64_t H, int64_t N, int32_t act,
     if (act < MOE_EP_ACT_NONE || act > MOE_EP_ACT_SILU_GATED) return MOE_EP_EINVAL;
     *nw = act == MOE_EP_ACT_SILU_GATED ? 2 * N : N;
     if (w_row <= 0 || *nw > INT_MAX / w_row) return MOE_EP_EINVAL;
-    if ((int64_t)groups * ((rows + 15) / 16) > INT_MAX / ((N + 7) / 8)) return MOE_EP_EINVAL;
+    // tile numbers and the steps over them stay below 2^31
+    if ((int64_t)groups * ((rows + 15) / 16) > (INT_MAX / 2) / ((N + 7) / 8)) return MOE_EP_EINVAL;
     return MOE_EP_OK;
 }
 
@@ -116,7 +117,9 @@ int moe_ep_route_topk(const void* logits, int64_t logits_stride, int32_t dtype,
     if (T > INT_MAX / K) return MOE_EP_EINVAL;
     if (logits_stride < E || logits_stride > INT64_MAX / 4 / (T > 0 ? T : 1)) return MOE_EP_EINVAL;
     if (T > 0 && (!logits || !topk_ids || !topk_weights)) return MOE_EP_EINVAL;
-    if (reinterpret_cast<uintptr_t>(logits) % eb) return MOE_EP_EALIGN;
+    if (reinterpret_cast<uintptr_t>(logits) % eb || reinterpret_cast<uintptr_t>(bias) % 4 ||
+        reinterpret_cast<uintptr_t>(topk_ids) % 4 || reinterpret_cast<uintptr_t>(topk_weights) % 4)
+        return MOE_EP_EALIGN;
     if (T == 0) return MOE_EP_OK;
     RouteArgs a = {};
     a.logits = static_cast<const uint8_t*>(logits);

@@ -256,7 +256,10 @@ __device__ __forceinline__ void small_fetch(const MatmulArgs& a, const SmallTile
         const uint32_t none = s * kSlab + chunk < kb ? 0u : kOutside;
         const uint32_t at = ring + j * 2 * kSmall * kSlab + h * 1024;
         load_to_lds(t.rw, at, t.vw[h] | none, k);
-        load_to_lds(t.rx, at + kSmall * kSlab, t.vx[h] | none, k);
+        // the last eight rows of x only where there are any (what LDS holds
+        // there else belongs to sums that are not stored)
+        if (h == 0 || t.rows - t.m0 > 8)
+            load_to_lds(t.rx, at + kSmall * kSlab, t.vx[h] | none, k);
     }
 }
 
@@ -311,8 +314,9 @@ __device__ __forceinline__ void small_tiles(const MatmulArgs& a, uint8_t* lds, i
                                             : nslab;
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
-                // the oldest slab has arrived (and, before it, its run's scales)
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kRun - 1) * 4) : "memory");
+                // the oldest slab has arrived (and, before it, its run's scales):
+                // behind it are three slabs of three or four loads
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kRun - 1) * 3) : "memory");
                 const uint8_t* p = mine + j * 2 * kSmall * kSlab;
                 Frag w, x;
                 w.v[0] = *reinterpret_cast<const u32x4*>(p + rd);
@@ -1356,7 +1360,7 @@ Estimate estimate(int64_t rows, int64_t nw, int64_t row_bytes) {
     Estimate e;
     e.small = (double)up(up(rows, kSmall) * up(nw, kSmall), kGrid) * (2.0 + 0.125 * pairs);
     e.mid64 = (double)up(up(rows, 64) * up(nw, 64), kGrid) * (2.5 + 0.45 * pairs);
-    e.mid128 = (double)up(up(rows, 128) * up(nw, 128), kGrid) * (2.5 + 0.93 * pairs);
+    e.mid128 = (double)up(up(rows, 128) * up(nw, 128), kGrid) * (2.5 + 1.0 * pairs);
     // a tile of 32 j rows takes 0.75 + 0.27 j us a pair
     const int64_t runs = up(rows, 256), tiles = runs * up(nw, kBig), rest = tiles % kGrid;
     const int64_t j = up(up(rows, runs), 32);

@@ -535,8 +535,8 @@ MOE_EP_API int moe_ep_combine_unpack_fused(const void* back, int64_t back_rank_s
  * whose logits are all -inf is a padding token.
  *
  *   logits        [T, E] of dtype (MOE_EP_BF16 or MOE_EP_F32); logits_stride
- *                 elements between tokens (>= E). Aligned to their type.
- *   bias          fp32 [E], nullable.
+ *                 elements between tokens (>= E).
+ *   bias          fp32 [E], nullable. Every pointer aligned to its type.
  *   K             1 <= K <= min(64, E).
  *   n_group       1 <= n_group <= 64, E % n_group == 0; 1 <= topk_group <=
  *                 n_group and K <= topk_group * (E / n_group).
@@ -554,9 +554,11 @@ MOE_EP_API int moe_ep_route_topk(const void* logits, int64_t logits_stride, int3
  * weight matrix per local expert, ragged row counts read on the device:
  *   out[e, r, n] = act(sum_h x[e, r, h] * w[e, n, h] + bias[e, n])
  * for r < expert_num_tokens[e]. Products and sums are fp32 (in the matrix
- * cores, over h in an order that does not depend on the counts of other
- * experts), the activation fp32, the result rounded once. Rows from the count
- * on are not written, and what x holds there has no effect.
+ * cores), the activation fp32, the result rounded once. The order of the sum
+ * over h goes by the sizes and counts of the call: equal calls give equal
+ * bits, but another expert's count may move a result within fp32's rounding.
+ * Rows from the count on are not written, and what x holds there has no
+ * effect.
  *
  *   x             bf16 [e_local, rows, H], expert e at x + e * x_stride
  *                 (elements, >= rows * H); rows dense. For the batched rows
@@ -571,7 +573,7 @@ MOE_EP_API int moe_ep_route_topk(const void* logits, int64_t logits_stride, int3
  * Rows of x, w and out, their strides, bias and its stride are multiples of
  * 16 bytes (EALIGN). Limits: H, N <= MOE_EP_MAX_WIDTH, Nw * H * 2 < 2^31
  * bytes, e_local <= 1024, rows <= INT_MAX and e_local * ceil(rows / 16) *
- * ceil(N / 8) < 2^31.
+ * ceil(N / 8) < 2^30.
  */
 MOE_EP_API int moe_ep_expert_matmul(const void* x, int64_t x_stride, const void* w,
                                     int64_t w_stride, const float* bias, int64_t bias_stride,
@@ -583,7 +585,10 @@ MOE_EP_API int moe_ep_expert_matmul(const void* x, int64_t x_stride, const void*
  * moe_ep_expert_matmul on OCP fp8 E4M3 codes: rows as moe_ep_dispatch_pack_fp8
  * (group 128) sends and moe_ep_expert_batch batches them, weights with one
  * scale per 128 x 128 block. With S the sum of the products of 128 columns'
- * codes, sums add (x_scale * w_scale) * S in ascending column order.
+ * codes, sums add (x_scale * w_scale) * S in fp32. For fp32 and E4M3 outputs S
+ * is an fp32 sum as well; for bf16 outputs it is that of the fp8 matrix
+ * instruction, which drops product bits below 2^-13 of the largest product it
+ * adds (1.4e-5 of a result over 7168 columns, where bf16 rounds to 2^-8).
  *
  *   x             codes [e_local, rows, H] (one byte; x_stride bytes between
  *                 experts), H % 128 == 0.

@@ -26,6 +26,8 @@ def test_route_refusals():
     assert _route(dtype=2) == B.EDTYPE
     assert _route(x=FAKE + 2) == B.EALIGN
     assert _route(x=FAKE + 1, dtype=0) == B.EALIGN
+    assert _route(ids=FAKE + 2) == B.EALIGN and _route(w=FAKE + 2) == B.EALIGN
+    assert _route(bias=FAKE + 1) == B.EALIGN
     assert _route(T=0) == B.OK                      # nothing to do, nothing enqueued
 
 

@@ -394,6 +394,128 @@ def test_expert_matmul_fp8_output_feeds_the_next_product():
 
 
 # ---------------------------------------------------------------------------
+# Sizes that take the larger tiles: enough experts and columns that every cut
+# of the rows (runs of 32 to 256, a last round in halves and quarters) occurs.
+# The 64-bit products run on the GPU here (torch, float64).
+# ---------------------------------------------------------------------------
+
+def _spread(e, top, seed):
+    """Counts from 0 to top, each 32-row class among them, odd ones too."""
+    g = gen(seed)
+    c = torch.randint(0, top + 1, (e,), generator=g).tolist()
+    return [0, top, top - 1, 1, 16, 17, 33] + c[7:]
+
+
+MANY = [
+    # experts, most rows, H, N, act, bias, out
+    (46, 256, 200, 2000, "none", True, BF16),           # a whole round and halves
+    (33, 256, 264, 1000, "silu_gated", False, F32),
+    (20, 700, 136, 2056, "silu", False, BF16),
+    (12, 256, 392, 1096, "silu_gated", True, BF16),     # quarters
+    (70, 64, 72, 1288, "none", False, F32),             # up to 64 rows each
+    (9, 128, 520, 2312, "silu_gated", False, BF16),
+    (3, 1500, 1032, 3200, "gelu", True, F32),
+]
+
+
+@pytest.mark.parametrize("e,top,H,N,act,bias,out", MANY)
+def test_expert_matmul_on_larger_tiles(e, top, H, N, act, bias, out):
+    say(f"[experts, larger] e={e} rows<={top} H={H} N={N} {act} {out}")
+    counts = _spread(e, top, e)[:e]
+    n, x, w, b = _experts(counts, top + 3, H, N, act, bias, 60)
+    x, w, b = _to(x), _to(w), _to(b)
+    o = _marked((e, top + 3, N), out)
+    B.moe_ep_expert_matmul(x, w, torch.tensor(counts, dtype=torch.int32, device=DEV), o, act, b)
+    torch.cuda.synchronize()
+    for i, c in enumerate(n):
+        if c:
+            y, err = product64(x[i, :c].double(), w[i].double(),
+                               None if b is None else b[i].double(), act, N)
+            assert_close(o[i, :c], y.cpu(), err.cpu(), ("expert", i, c))
+        assert bool((o[i, c:].contiguous().view(torch.uint8) == 0xFB).all()), (i, c)
+
+
+MANY8 = [
+    (46, 256, 256, 2048, "none", True, BF16),
+    (33, 256, 384, 1024, "silu_gated", False, F32),
+    (12, 256, 640, 1152, "silu_gated", True, F8),
+    (40, 64, 128, 1280, "none", False, F8),
+    (20, 600, 256, 1096, "silu_gated", False, BF16),
+    (60, 64, 384, 1280, "none", False, BF16),
+]
+
+
+@pytest.mark.parametrize("e,top,H,N,act,bias,out", MANY8)
+def test_expert_matmul_fp8_on_larger_tiles(e, top, H, N, act, bias, out):
+    say(f"[experts fp8, larger] e={e} rows<={top} H={H} N={N} {act} {out}")
+    counts = _spread(e, top, e + 1)[:e]
+    rows = top + 3
+    n, (xq, xs, wq, ws, b), x64, w64 = _experts8(counts, rows, H, N, act, bias, 61)
+    b = _to(b)
+    o = _marked((e, rows, N), torch.uint8 if out == F8 else out)
+    osc = _marked((e, rows, B.scale_pitch(N, 128)), F32) if out == F8 else None
+    B.moe_ep_expert_matmul_fp8(_to(xq), _to(xs), _to(wq), _to(ws),
+                               torch.tensor(counts, dtype=torch.int32, device=DEV), o, act, b, osc)
+    torch.cuda.synchronize()
+    for i, c in enumerate(n):
+        assert bool((o[i, c:].contiguous().view(torch.uint8) == 0xFB).all()), (i, c)
+        if not c:
+            continue
+        y, err = product64(x64[i, :c].to(DEV), w64[i].to(DEV), None if b is None else b[i].double(),
+                           act, N, extra=4)
+        if out != F8:
+            assert_close(o[i, :c], y.cpu(), err.cpu(), ("expert", i, c))
+            continue
+        s = osc[i, :c, :N // 128].double()
+        amax, worst = (t.view(c, N // 128, 128).amax(dim=2) for t in (y.abs(), err))
+        assert bool(((s * 448 - amax).abs() <= worst + 4 * U * amax).all()), (i, c)
+        assert bool((osc[i, :c, N // 128:] == 0).all())
+        sr = s.repeat_interleave(128, dim=1)
+        v = o[i, :c].view(F8).double() * sr
+        tol = err + (y.abs() + err) * 2.0 ** -4 + sr * 2.0 ** -10 + U * y.abs()
+        assert bool(((v - y).abs() <= tol).all()), (i, c, float(((v - y).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("T,H,N,act,bias,residual,out", [
+    (4096, 1032, 2048, "silu_gated", True, True, BF16),
+    (2051, 4104, 2056, "none", False, True, BF16),
+    (8191, 264, 1544, "none", True, False, F32),
+    (700, 2056, 1288, "gelu", True, True, F32),
+    (1023, 520, 520, "silu_gated", False, False, BF16),
+    (130, 4104, 4104, "none", False, True, F32),
+    (20000, 72, 264, "silu", True, False, BF16),
+])
+def test_matmul_on_larger_tiles(T, H, N, act, bias, residual, out):
+    say(f"[matmul, larger] T={T} H={H} N={N} {act} {out}")
+    x, w, b, r = (_to(t) for t in _mm_inputs(T, H, N, act, bias, residual, out, 70))
+    o = torch.full((T, N), float("nan"), dtype=out, device=DEV)
+    B.moe_ep_matmul(x, w, o, act, b, r)
+    torch.cuda.synchronize()
+    y, e = _mm_ref(x, w, b, r, act, N)
+    assert_close(o, y.cpu(), e.cpu(), (T, H, N))
+
+
+def test_products_do_not_depend_on_what_lies_beside_them():
+    """A row's result is the same bits whatever the other groups and rows of
+    the same tile cut hold."""
+    say("[experts] independence")
+    counts, rows, H, N = [200, 40, 0, 256], 256, 264, 520
+    n, x, w, _ = _experts(counts, rows, H, N, "none", False, 80)
+    cnt = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    outs = []
+    for fill in (float("nan"), 3.0):
+        xx = x.clone()
+        for i, c in enumerate(n):
+            xx[i, c:] = fill
+        o = _marked((4, rows, N), F32)
+        B.moe_ep_expert_matmul(_to(xx), _to(w), cnt, o)
+        B.moe_ep_expert_matmul(_to(xx), _to(w), cnt, o)     # and again over its own output
+        outs.append(o)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0].view(torch.uint8), outs[1].view(torch.uint8))
+
+
+# ---------------------------------------------------------------------------
 # Streams, graphs, repeats
 # ---------------------------------------------------------------------------
 
