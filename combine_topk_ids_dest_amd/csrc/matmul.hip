@@ -86,9 +86,13 @@ __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.0f + expf(-v));
 }
 
+__device__ __forceinline__ float gelu(float v) {
+    return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+}
+
 __device__ __forceinline__ float apply_act(float v, int act) {
     if (act == MOE_EP_ACT_SILU) return silu(v);
-    if (act == MOE_EP_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    if (act == MOE_EP_ACT_GELU) return gelu(v);
     return v;
 }
 
@@ -446,14 +450,6 @@ __device__ __forceinline__ void wait_and_barrier() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
 }
 
-// The four output columns n..n+3 (a quad) of a lane: act(v + b), gated with up.
-template <bool GATED>
-__device__ __forceinline__ f32x4 activate(f32x4 v, f32x4 up, int act) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = GATED ? silu_gated(v[i], up[i]) : apply_act(v[i], act);
-    return v;
-}
-
 __device__ __forceinline__ f32x4 load_f32x4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     return __builtin_bit_cast(f32x4, ld_row_buf<false>(r, off));
 }
@@ -538,125 +534,140 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int g, int m0, 
             }
         }
     }
-    auto value = [&](int q, int j) {
-        return activate<GATED>(acc[GATED ? 2 * q : q][j], acc[GATED ? 2 * q + 1 : q][j], a.act);
-    };
     uint8_t* const out = a.out + g * a.out_stride + (int64_t)m0 * a.out_row;
     const int mrow = wm * (JF * 16) + (lane & 15);
 
-    if constexpr (EB == 1 && WIDE) {
-        if (a.out_dtype == MOE_EP_E4M3) {
-            // a row's 128 columns lie in 4 (gated) or 2 waves, 4 lanes each
-            constexpr int WG = GATED ? 4 : 2;
-            float* part = reinterpret_cast<float*>(lds);            // [BM][4]
-            f32x4 y[QN][JF];
+    // The rest once for each activation: one branch, not one for each value.
+    auto rest = [&](auto activation) {
+        auto value = [&](int q, int j) {
+            f32x4 v = acc[GATED ? 2 * q : q][j];
 #pragma unroll
-            for (int j = 0; j < JF; ++j) {
-                float mx = 0.f;
+            for (int e = 0; e < 4; ++e)
+                v[e] = GATED ? silu_gated(v[e], acc[GATED ? 2 * q + 1 : q][j][e]) : activation(v[e]);
+            return v;
+        };
+
+        if constexpr (EB == 1 && WIDE) {
+            if (a.out_dtype == MOE_EP_E4M3) {
+                // a row's 128 columns lie in 4 (gated) or 2 waves, 4 lanes each
+                constexpr int WG = GATED ? 4 : 2;
+                float* part = reinterpret_cast<float*>(lds);            // [BM][4]
+                f32x4 y[QN][JF];
 #pragma unroll
-                for (int q = 0; q < QN; ++q) {
-                    y[q][j] = value(q, j);
+                for (int j = 0; j < JF; ++j) {
+                    float mx = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx = abs_max(mx, y[q][j][e]);
+                    for (int q = 0; q < QN; ++q) {
+                        y[q][j] = value(q, j);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mx = abs_max(mx, y[q][j][e]);
+                    }
+                    mx = abs_max(mx, __shfl_xor(mx, 16, 64));
+                    mx = abs_max(mx, __shfl_xor(mx, 32, 64));
+                    if (lane < 16) part[(mrow + j * 16) * 4 + wn] = mx;
                 }
-                mx = abs_max(mx, __shfl_xor(mx, 16, 64));
-                mx = abs_max(mx, __shfl_xor(mx, 32, 64));
-                if (lane < 16) part[(mrow + j * 16) * 4 + wn] = mx;
-            }
-            __syncthreads();
-            const int groups = a.N / kScaleBlock;
+                __syncthreads();
+                const int groups = a.N / kScaleBlock;
 #pragma unroll
-            for (int j = 0; j < JF; ++j) {
-                const int m = mrow + j * 16;
-                float mx = 0.f;
+                for (int j = 0; j < JF; ++j) {
+                    const int m = mrow + j * 16;
+                    float mx = 0.f;
 #pragma unroll
-                for (int w = 0; w < WG; ++w) mx = abs_max(mx, part[m * 4 + (GATED ? 0 : wn & 2) + w]);
-                const float s = mx > 0.f ? mx / 448.0f : 1.0f;
-                if (m < left && n < a.N) {
-                    uint32_t* o = reinterpret_cast<uint32_t*>(out + (int64_t)m * a.out_row + n);
+                    for (int w = 0; w < WG; ++w) mx = abs_max(mx, part[m * 4 + (GATED ? 0 : wn & 2) + w]);
+                    const float s = mx > 0.f ? mx / 448.0f : 1.0f;
+                    if (m < left && n < a.N) {
+                        uint32_t* o = reinterpret_cast<uint32_t*>(out + (int64_t)m * a.out_row + n);
 #pragma unroll
-                    for (int q = 0; q < QN; ++q) o[q] = codes4(y[q][j], s);
-                    float* os = a.os + g * a.os_stride + (int64_t)(m0 + m) * a.os_pitch;
-                    if (lane < 16 && wn % WG == 0) {
-                        os[n / kScaleBlock] = s;
-                        // the last group's wave also writes the padding
-                        if (n / kScaleBlock == groups - 1)
-                            for (int p = groups; p < (int)a.os_pitch; ++p) os[p] = 0.f;
+                        for (int q = 0; q < QN; ++q) o[q] = codes4(y[q][j], s);
+                        float* os = a.os + g * a.os_stride + (int64_t)(m0 + m) * a.os_pitch;
+                        if (lane < 16 && wn % WG == 0) {
+                            os[n / kScaleBlock] = s;
+                            // the last group's wave also writes the padding
+                            if (n / kScaleBlock == groups - 1)
+                                for (int p = groups; p < (int)a.os_pitch; ++p) os[p] = 0.f;
+                        }
                     }
                 }
+                __syncthreads();   // the next tile writes lds again
+                return;
             }
-            __syncthreads();   // the next tile writes lds again
+        }
+
+        const bool f32 = EB == 1 ? WIDE : a.out_dtype == MOE_EP_F32;
+        const int eb = f32 ? 4 : 2;
+        const auto ro = row_rsrc(out, (int64_t)(left - 1) * a.out_row + (int64_t)a.N * eb);
+        const auto rr = row_rsrc(a.res ? a.res + (int64_t)m0 * a.res_row : out,
+                                 a.res ? (int64_t)(left - 1) * a.res_row + (int64_t)a.N * eb : 0);
+        auto at = [&](int j, int q, int64_t row) {
+            const int m = mrow + j * 16, c = n + q * 4;
+            return m < left && c < a.N ? (uint32_t)m * (uint32_t)row + (uint32_t)(c * eb) : kOutside;
+        };
+        if (f32) {
+#pragma unroll
+            for (int j = 0; j < JF; ++j) {
+                f32x4 r[QN];
+                if (a.res) {
+#pragma unroll
+                    for (int q = 0; q < QN; ++q) r[q] = load_f32x4(rr, at(j, q, a.res_row));
+                }
+#pragma unroll
+                for (int q = 0; q < QN; ++q) {
+                    f32x4 y = value(q, j);
+                    if (a.res) y += r[q];
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), ro,
+                                                           at(j, q, a.out_row), 0, 0);
+                }
+            }
             return;
         }
-    }
-
-    const bool f32 = EB == 1 ? WIDE : a.out_dtype == MOE_EP_F32;
-    const int eb = f32 ? 4 : 2;
-    const auto ro = row_rsrc(out, (int64_t)(left - 1) * a.out_row + (int64_t)a.N * eb);
-    const auto rr = row_rsrc(a.res ? a.res + (int64_t)m0 * a.res_row : out,
-                             a.res ? (int64_t)(left - 1) * a.res_row + (int64_t)a.N * eb : 0);
-    auto at = [&](int j, int q, int64_t row) {
-        const int m = mrow + j * 16, c = n + q * 4;
-        return m < left && c < a.N ? (uint32_t)m * (uint32_t)row + (uint32_t)(c * eb) : kOutside;
-    };
-    if (f32) {
+        if constexpr (QN == 1) {
 #pragma unroll
-        for (int j = 0; j < JF; ++j) {
-            f32x4 r[QN];
+            for (int j = 0; j < JF; ++j) {
+                f32x4 y = value(0, j);
+                if (a.res) {
+                    const u32x2 v = __builtin_bit_cast(
+                        u32x2, __builtin_amdgcn_raw_buffer_load_b64(rr, at(j, 0, a.res_row), 0, 0));
+                    y += f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+                }
+                __builtin_amdgcn_raw_buffer_store_b64(pack_bf16(y), ro, at(j, 0, a.out_row), 0, 0);
+            }
+            return;
+        }
+        // bf16: N is a multiple of 8, so eight columns exist together; the
+        // residuals of four rows are on their way at once
+        constexpr int JB = JF < 4 ? JF : 4;
+#pragma unroll
+        for (int j0 = 0; j0 < JF; j0 += JB) {
+            u32x4 r[JB][QN < 2 ? 1 : QN / 2];
             if (a.res) {
 #pragma unroll
-                for (int q = 0; q < QN; ++q) r[q] = load_f32x4(rr, at(j, q, a.res_row));
-            }
+                for (int j = 0; j < JB && j0 + j < JF; ++j)
 #pragma unroll
-            for (int q = 0; q < QN; ++q) {
-                f32x4 y = value(q, j);
-                if (a.res) y += r[q];
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), ro,
-                                                       at(j, q, a.out_row), 0, 0);
+                    for (int q = 0; q < QN / 2; ++q)
+                        r[j][q] = ld_row_buf<false>(rr, at(j0 + j, 2 * q, a.res_row));
             }
-        }
-        return;
-    }
-    if constexpr (QN == 1) {
-#pragma unroll
-        for (int j = 0; j < JF; ++j) {
-            f32x4 y = value(0, j);
-            if (a.res) {
-                const u32x2 v = __builtin_bit_cast(
-                    u32x2, __builtin_amdgcn_raw_buffer_load_b64(rr, at(j, 0, a.res_row), 0, 0));
-                y += f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
-            }
-            __builtin_amdgcn_raw_buffer_store_b64(pack_bf16(y), ro, at(j, 0, a.out_row), 0, 0);
-        }
-        return;
-    }
-    // bf16: N is a multiple of 8, so eight columns exist together; the
-    // residuals of four rows are on their way at once
-    constexpr int JB = JF < 4 ? JF : 4;
-#pragma unroll
-    for (int j0 = 0; j0 < JF; j0 += JB) {
-        u32x4 r[JB][QN < 2 ? 1 : QN / 2];
-        if (a.res) {
 #pragma unroll
             for (int j = 0; j < JB && j0 + j < JF; ++j)
 #pragma unroll
-                for (int q = 0; q < QN / 2; ++q)
-                    r[j][q] = ld_row_buf<false>(rr, at(j0 + j, 2 * q, a.res_row));
-        }
-#pragma unroll
-        for (int j = 0; j < JB && j0 + j < JF; ++j)
-#pragma unroll
-            for (int q = 0; q < QN / 2; ++q) {
-                f32x4 lo = value(2 * q, j0 + j), hi = value(2 * q + 1, j0 + j);
-                if (a.res) {
-                    const u32x4 v = r[j][q];
-                    lo += f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
-                    hi += f32x4{bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3])};
+                for (int q = 0; q < QN / 2; ++q) {
+                    f32x4 lo = value(2 * q, j0 + j), hi = value(2 * q + 1, j0 + j);
+                    if (a.res) {
+                        const u32x4 v = r[j][q];
+                        lo += f32x4{bf16_lo(v[0]), bf16_hi(v[0]), bf16_lo(v[1]), bf16_hi(v[1])};
+                        hi += f32x4{bf16_lo(v[2]), bf16_hi(v[2]), bf16_lo(v[3]), bf16_hi(v[3])};
+                    }
+                    const u32x2 l = pack_bf16(lo), h = pack_bf16(hi);
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{l[0], l[1], h[0], h[1]}, ro,
+                                                           at(j0 + j, 2 * q, a.out_row), 0, 0);
                 }
-                const u32x2 l = pack_bf16(lo), h = pack_bf16(hi);
-                __builtin_amdgcn_raw_buffer_store_b128(u32x4{l[0], l[1], h[0], h[1]}, ro,
-                                                       at(j0 + j, 2 * q, a.out_row), 0, 0);
-            }
+        }
+    };
+    if constexpr (GATED) {
+        rest([](float v) { return v; });
+    } else {
+        if (a.act == MOE_EP_ACT_SILU) rest([](float v) { return silu(v); });
+        else if (a.act == MOE_EP_ACT_GELU) rest([](float v) { return gelu(v); });
+        else rest([](float v) { return v; });
     }
 }
 
