@@ -461,42 +461,49 @@ template <int EB, bool GATED>
 struct TileScales {
     static constexpr int kSet = kBig * 16 + 256;
     i32x4 rx, rw;
-    uint32_t vx, vw, lds0;
-    int nslab, wave;
+    uint32_t lds0;
+    int nslab, wave, left, pitch, per, n0, N;
 
-    __device__ __forceinline__ TileScales(const MatmulArgs& a, int g, int m0, int left, int n0,
+    __device__ __forceinline__ TileScales(const MatmulArgs& a, int g, int m0, int left_, int n0_,
                                           uint32_t lds) {
         if constexpr (EB == 1) {
-            const int lane = threadIdx.x & 63;
             wave = uniform(threadIdx.x >> 6);
             lds0 = lds + kScaleAt;
             nslab = a.row_bytes / kSlab;
-            const int row = wave * 64 + lane;
-            vx = row < left ? (uint32_t)row * (uint32_t)a.xs_pitch * 4 : kOutside;
+            left = left_;
+            pitch = (int)a.xs_pitch * 4;
+            n0 = n0_;
+            N = a.N;
+            per = (N + kScaleBlock - 1) / kScaleBlock;
             rx = row_rsrc4(reinterpret_cast<const uint8_t*>(a.xs + g * a.xs_stride +
                                                             (int64_t)m0 * a.xs_pitch),
-                           (int64_t)left * a.xs_pitch * 4);
-            const int per = (a.N + kScaleBlock - 1) / kScaleBlock;
-            const int b = lane >> 2;
-            const int n = n0 + (GATED ? 0 : b * kScaleBlock);
-            vw = b < 2 && n < a.N ? ((uint32_t)(n / kScaleBlock + (GATED ? b * per : 0)) *
-                                         (uint32_t)nslab +
-                                     (lane & 3)) * 4
-                                  : kOutside;
+                           (int64_t)left * pitch);
             rw = row_rsrc4(reinterpret_cast<const uint8_t*>(a.ws + g * a.ws_stride),
                            (int64_t)(GATED ? 2 : 1) * per * nslab * 4);
         }
     }
 
-    // the four slabs from s on (a multiple of 4)
+    // The four slabs from s on (a multiple of 4). The lanes' addresses are made
+    // here: one register held over the loop too many is one spilled, and to
+    // load it back waits for every load in flight.
     __device__ __forceinline__ void fetch(int s) const {
+        const int lane = threadIdx.x & 63;
         const uint32_t d = lds0 + ((s >> 2) & 1) * kSet;
-        const uint32_t none = s < nslab ? 0u : kOutside;
         const uint32_t k = s < nslab ? s * 4 : 0;
-        if (wave < kBig / 64) load_to_lds(rx, d + wave * 1024, vx | none, k);
-        if (wave == kWaves - 1)
+        if (wave < kBig / 64) {
+            const int row = wave * 64 + lane;
+            load_to_lds(rx, d + wave * 1024,
+                        s < nslab && row < left ? (uint32_t)row * (uint32_t)pitch : kOutside, k);
+        }
+        if (wave == kWaves - 1) {
+            const int b = lane >> 2;
+            const int n = n0 + (GATED ? 0 : b * kScaleBlock);
+            const uint32_t at =
+                ((uint32_t)(n / kScaleBlock + (GATED ? b * per : 0)) * (uint32_t)nslab + (lane & 3)) *
+                4;
             load4_to_lds(rw, d + kBig * 16,
-                         s + (int)(threadIdx.x & 3) < nslab ? vw : kOutside, k);
+                         b < 2 && n < N && s + (lane & 3) < nslab ? at : kOutside, k);
+        }
     }
 
     // slab s's: row r's of x at [4 r + s % 4], block b's at [4 kBig + 4 b + s % 4]
@@ -696,25 +703,32 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
     // a wave's load i fills rows (i * 8 + wave) * 8 .. + 7
     const int sub = lane >> 3;
     const int chunk = (lane & 7) ^ ((((wave & 1) << 3 | sub) >> 1) & 7);
-    uint32_t vx[FX], vw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = (i * 8 + wave) * 8 + sub;
-        if (i < FX) vx[i] = r < left ? (uint32_t)r * (uint32_t)a.x_row + chunk * 16 : kOutside;
-        int n;
-        const int q = wrow<GATED, 4>(r, n0, a.N, n);
-        vw[i] = n < a.N ? (uint32_t)q * (uint32_t)a.w_row + chunk * 16 : kOutside;
-    }
+    // Rows 64 apart: one offset for x and one for w, and how many of the loads
+    // have a row (in one register, with four bits each). Offsets for every load
+    // are five registers more, and the loop has none to spare: what it spills
+    // it waits for, behind all loads in flight.
+    const int row = wave * 8 + sub;
+    int n;
+    const int wr = wrow<GATED, 4>(row, n0, a.N, n);
+    const uint32_t vx = (uint32_t)row * (uint32_t)a.x_row + chunk * 16;
+    const uint32_t vw = (uint32_t)wr * (uint32_t)a.w_row + chunk * 16;
+    constexpr int STEP_N = GATED ? 32 : 64;       // output columns of 64 rows of w
+    const int have_x = left > row ? (left - row + 63) / 64 : 0;
+    const int have_w = a.N > n ? (a.N - n + STEP_N - 1) / STEP_N : 0;
+    const int have = (have_x < 8 ? have_x : 8) | (have_w < 8 ? have_w : 8) << 4;
+    const uint32_t step_x = 64u * (uint32_t)a.x_row, step_w = (uint32_t)STEP_N * (uint32_t)a.w_row;
     // the last slab may be short: its chunks past the end of k load zeros, and
     // so do slabs past the last
     const int last = (kb - chunk * 16 + kSlab - 1) / kSlab;
     auto fetch_x = [&](int i, int s, int stage) {
         load_to_lds(rx, lds0 + stage * SLAB_X + wave * 1024 + i * 8192,
-                    vx[i] | (s < last ? 0u : kOutside), s < nslab ? s * kSlab : 0);
+                    s < last && i < (have & 15) ? vx + i * step_x : kOutside,
+                    s < nslab ? s * kSlab : 0);
     };
     auto fetch_w = [&](int i, int s, int stage) {
         load_to_lds(rw, lds0 + AT_W + stage * kBigSlab + wave * 1024 + i * 8192,
-                    vw[i] | (s < last ? 0u : kOutside), s < nslab ? s * kSlab : 0);
+                    s < last && i < have >> 4 ? vw + i * step_w : kOutside,
+                    s < nslab ? s * kSlab : 0);
     };
 
     const TileScales<EB, GATED> scales(a, g, m0, left, n0, lds0);
