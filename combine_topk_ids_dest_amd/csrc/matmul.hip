@@ -806,6 +806,10 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
         // scaled, so the halves cannot be taken apart.
         const int bw = GATED ? 0 : wn >> 1;       // the wave's block (gated: both)
         static_assert(XS == WS, "");
+        // A register loaded in front of the loop (a spilled one) is waited for
+        // at its first use in the loop, in every round, and with it all loads
+        // into LDS: wait for it here, in a form that the compiler sees (vmcnt 0).
+        __builtin_amdgcn_s_waitcnt(0x0F70);
         int now = 0;
         for (int s = 0; s < nslab; ++s) {
             // slab s and its scales (older than the loads that may still be
