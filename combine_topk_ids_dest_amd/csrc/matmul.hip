@@ -846,8 +846,18 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
                 for (int j = 0; j < JF; ++j) {
                     const Wide x = widen(frag(px + j * 16 * kSlab));
                     const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
+                    // two chains of products at a time: each waits for its own sum
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) scale(i, j, mma_wide(w[i], x, zero), sx);
+                    for (int i = 0; i < 4; i += 2) {
+                        f32x4 t0 = zero, t1 = zero;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            t0 = mma_bf16(w[i].v[q], x.v[q], t0);
+                            t1 = mma_bf16(w[i + 1].v[q], x.v[q], t1);
+                        }
+                        scale(i, j, t0, sx);
+                        scale(i + 1, j, t1, sx);
+                    }
                 }
             } else {
                 Frag w[4];
