@@ -142,6 +142,12 @@ __device__ __forceinline__ i32x4 row_rsrc4(const uint8_t* p, int64_t bytes) {
     return r;
 }
 
+// A resource that went through a branch, in scalar registers again: the loads
+// below take nothing else, and at -O1 the compiler may hold it in vector ones.
+__device__ __forceinline__ i32x4 uniform(i32x4 r) {
+    return i32x4{uniform(r[0]), uniform(r[1]), uniform(r[2]), uniform(r[3])};
+}
+
 // 16 (or 4) bytes per lane from memory into LDS, lane l's at dst + 16 l (4 l);
 // dst is uniform, in M0. Written out so that the compiler does not count it
 // among the loads that an LDS read has to wait for: with its own form of this
@@ -193,7 +199,6 @@ constexpr int kRing = kRun * 2 * kSmall * kSlab; // bytes of them
 constexpr int kPartAt = kWaves * kRing;          // the waves' sums, twice
 constexpr int kPart = kWaves * kSmall * kSmallPitch * 4;
 constexpr int kSmallScaleAt = kPartAt + 2 * kPart;        // fp8: scales of two runs
-constexpr int kSmallScale = 256 + 64;                     // 16 rows x 4, 2 blocks x 4 (padded)
 constexpr int kSmallLds = kSmallScaleAt + kWaves * 2 * 512;
 
 // What a wave needs to load a small tile.
@@ -258,11 +263,11 @@ __device__ __forceinline__ void small_fetch(const MatmulArgs& a, const SmallTile
         const int chunk = ((lane & 7) ^ ((h * 4 + (lane >> 4)) & 7)) * 16;
         const uint32_t none = s * kSlab + chunk < kb ? 0u : kOutside;
         const uint32_t at = ring + j * 2 * kSmall * kSlab + h * 1024;
-        load_to_lds(t.rw, at, t.vw[h] | none, k);
+        load_to_lds(uniform(t.rw), at, t.vw[h] | none, k);
         // the last eight rows of x only where there are any (what LDS holds
         // there else belongs to sums that are not stored)
         if (h == 0 || t.rows - t.m0 > 8)
-            load_to_lds(t.rx, at + kSmall * kSlab, t.vx[h] | none, k);
+            load_to_lds(uniform(t.rx), at + kSmall * kSlab, t.vx[h] | none, k);
     }
 }
 
@@ -272,9 +277,9 @@ __device__ __forceinline__ void small_fetch_scales(const MatmulArgs& a, const Sm
     const int nslab = (a.row_bytes + kSlab - 1) / kSlab;
     const uint32_t k = s < nslab ? s * 4 : 0;
     const uint32_t none = s < nslab ? 0u : kOutside;
-    if ((threadIdx.x & 63) < 16) load_to_lds(t.rxs, at, t.vxs | none, k);
+    if ((threadIdx.x & 63) < 16) load_to_lds(uniform(t.rxs), at, t.vxs | none, k);
     if ((threadIdx.x & 63) < 16)
-        load4_to_lds(t.rws, at + 256, s + (int)(threadIdx.x & 3) < nslab ? t.vws : kOutside, k);
+        load4_to_lds(uniform(t.rws), at + 256, s + (int)(threadIdx.x & 3) < nslab ? t.vws : kOutside, k);
 }
 
 // Works through the block's tiles, number t of `total` at place(t) = {g, m0,
@@ -1387,7 +1392,9 @@ __global__ __launch_bounds__(kThreads, 2) void small_kernel(const MatmulArgs a) 
 
 // What a product over all tokens takes with each kind of tile, in us, from the
 // tiles' measured times: rounds of the grid times a tile's start and its pairs
-// of slabs.
+// of slabs. Both sides measured where the choice turns, in us: 4096 x 7168 by
+// 256 rows of w: 64 x 64 tiles 37, big 82, 16 x 16 135; 128 rows of that: 16 x 16
+// 10, 64 x 64 24; 2048 x 7168 by 4096 rows: big 99, 128 x 128 125 to 129.
 struct Estimate {
     double small, mid64, mid128, big;
 };
