@@ -154,14 +154,20 @@ __device__ __forceinline__ i32x4 uniform(i32x4 r) {
 // instruction it waits for every load in flight before the next LDS read,
 // whatever that reads. The instruction has no output register; what it
 // writes is ordered by the waits and barriers below.
+//
+// A memory instruction may read a scalar register five wait states after a
+// vector instruction wrote it at the soonest (a readfirstlane, or the readlane
+// that brings a spilled one back), and the compiler, which sees to that
+// elsewhere, does not look in here: s_mov and s_nop 3 are the five, whatever
+// comes before. (M0 itself needs one.)
 __device__ __forceinline__ void load_to_lds(i32x4 r, uint32_t dst, uint32_t off, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(dst), "v"(off), "s"(r), "s"(soff)
                  : "m0");
 }
 __device__ __forceinline__ void load4_to_lds(i32x4 r, uint32_t dst, uint32_t off, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, %3 offen lds"
                  :
                  : "s"(dst), "v"(off), "s"(r), "s"(soff)
                  : "m0");
