@@ -20,6 +20,7 @@
 #include <type_traits>
 
 #include "experts.h"
+#include "tiles.h"
 
 namespace moe_ep {
 namespace {
@@ -173,17 +174,6 @@ __device__ __forceinline__ void load4_to_lds(i32x4 r, uint32_t dst, uint32_t off
                  : "m0");
 }
 
-// Tile of block b in a round of `left` tiles over the grid, -1 for none.
-// Blocks go to the eight XCDs in turn, so each XCD (with an L2 of its own)
-// gets a run of neighbouring tiles, which share rows of x and w.
-__device__ __forceinline__ int tile_of(int b, int grid, int left) {
-    const int r = left < grid ? left : grid;
-    const int per = (r + 7) / 8;
-    const int slot = b >> 3;
-    const int t = (b & 7) * per + slot;
-    return slot < per && t < r ? t : -1;
-}
-
 // ---------------------------------------------------------------------
 // Small tiles, for a few rows: 16 rows of x by 16 rows of w (gated: 8 gate
 // rows and their 8 up rows). Bound by the weights' bytes, so what counts is
@@ -198,7 +188,6 @@ __device__ __forceinline__ int tile_of(int b, int grid, int left) {
 // its 1 KB (one 16-byte piece at a time), which held a CU to 36 GB/s; eight
 // neighbouring lanes to a row's 128 bytes take a quarter of that.
 // ---------------------------------------------------------------------
-constexpr int kSmall = 16;
 constexpr int kSmallPitch = kSmall + 4;
 constexpr int kRun = 4;                          // slabs of a wave in LDS
 constexpr int kRing = kRun * 2 * kSmall * kSlab; // bytes of them
@@ -1178,27 +1167,8 @@ __global__ __launch_bounds__(kThreads, 2) void mid_kernel(const MatmulArgs a) {
 // per CU. Every block computes its share from the counts for itself: there is
 // no queue, so nothing to clear and no order left to chance.
 // ---------------------------------------------------------------------
-constexpr int kGrid = 256;                       // blocks
-constexpr int kGroup = 8;                        // runs of rows side by side
-constexpr int kKinds = 9;                        // runs of 32 k rows, k = 1..8; small: 0
 constexpr int kRuns64 = kKinds;                  // every group in runs of 64 rows,
 constexpr int kRuns128 = kKinds + 1;             // or of 128 (but for small ones)
-
-struct Cut {
-    int runs, kind;
-};
-
-__device__ __forceinline__ Cut cut_rows(int rows, int small_to) {
-    Cut c;
-    if (rows <= small_to) {
-        c.kind = 0;
-        c.runs = (rows + kSmall - 1) / kSmall;
-        return c;
-    }
-    c.runs = (rows + 255) / 256;
-    c.kind = ((rows + c.runs - 1) / c.runs + 31) / 32;
-    return c;
-}
 
 // A group's runs of a kind.
 __device__ __forceinline__ int runs_of(int rows, int small_to, int kind) {
@@ -1274,9 +1244,6 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
     constexpr int BB = GATED ? kBig / 2 : kBig;
     const int nt = (a.N + BO - 1) / BO, ntb = (a.N + BB - 1) / BB;
-    // blocks go to the eight XCDs in turn: neighbouring tiles, which share rows
-    // of x and w, to the blocks of one XCD (with an L2 of its own)
-    const int pos = (blockIdx.x & 7) * (kGrid / 8) + (blockIdx.x >> 3);
     const int rows0 = lane_rows(a, 0);
     int n[kKinds], total = 0;
     for (;;) {
@@ -1326,21 +1293,11 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
             }
         }
     }
-    const int whole = total / kGrid * kGrid;
-    // The last, partial round: with at most half (a quarter) as many tiles as
-    // blocks, each tile is cut in two (four) by its rows. 3.5 rounds then take
-    // 3.5 tiles' time and not 4, and a few rows an expert, bound by the
-    // weights' bytes, are read by all CUs.
-    const int parts = (total - whole) * 4 <= kGrid ? 4 : (total - whole) * 2 <= kGrid ? 2 : 1;
+    const int parts = last_parts(total);
     for (int t0 = 0; t0 < total; t0 += kGrid) {
-        int t = t0 + pos, sub = 0, cut = 1;
-        if (t0 == whole) {
-            const int u = tile_of(blockIdx.x, kGrid, (total - whole) * parts);
-            if (u < 0) break;
-            t = whole + u / parts;
-            sub = u % parts;
-            cut = parts;
-        }
+        const Turn turn = turn_of(blockIdx.x, t0, total, parts);
+        if (turn.t < 0) break;
+        int t = turn.t;
         int kind = kKinds - 1;
 #pragma unroll
         for (int k = kKinds - 1; k > 1; --k)
@@ -1350,27 +1307,21 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
             }
         const Place at = find_tile(a, rows0, small_to, kind, ntb, t);
         const int runs = cut_rows(at.rows, small_to).runs;
-        // kGroup runs of rows at a time, over all columns
-        const int m8 = at.l / (kGroup * ntb) * kGroup;
-        const int wide = runs - m8 < kGroup ? runs - m8 : kGroup;
-        const int in = at.l - m8 * ntb;
-        const int from = (m8 + in % wide) * kind * 32;
-        const int end = from + kind * 32 < at.rows ? from + kind * 32 : at.rows;
-        const int jf = (kind + cut - 1) / cut;
-        const int m0 = from + sub * jf * 32;
-        if (m0 >= end) continue;
-        const int n0 = in / wide * BB;
+        const Piece p = piece_of(at.l, at.rows, runs, kind, ntb, turn.sub, turn.cut);
+        if (p.m0 >= p.end) continue;
+        const int n0 = p.col * BB;
         // (a tile of a run-time number of fragments was 18 % slower: its loop
         // is full of branches)
         auto run = [&](auto bm) {
-            big_tile<EB, WIDE, GATED, decltype(bm)::value>(a, at.g, m0, end, n0, lds);
+            big_tile<EB, WIDE, GATED, decltype(bm)::value>(a, at.g, p.m0, p.end, n0, lds);
         };
-        if (jf > 7) run(std::integral_constant<int, 256>{});
-        else if (jf > 6) run(std::integral_constant<int, 224>{});
-        else if (jf > 5) run(std::integral_constant<int, 192>{});
-        else if (jf > 4) run(std::integral_constant<int, 160>{});
-        else if (jf > 2) run(std::integral_constant<int, 128>{});
-        else narrow_tile<EB, WIDE, GATED>(a, at.g, m0, end, n0, lds);
+        const int bm = tile_rows(p.fragments);
+        if (bm == 256) run(std::integral_constant<int, 256>{});
+        else if (bm == 224) run(std::integral_constant<int, 224>{});
+        else if (bm == 192) run(std::integral_constant<int, 192>{});
+        else if (bm == 160) run(std::integral_constant<int, 160>{});
+        else if (bm == 128) run(std::integral_constant<int, 128>{});
+        else narrow_tile<EB, WIDE, GATED>(a, at.g, p.m0, p.end, n0, lds);
     }
     if (nsmall > 0)
         small_tiles<EB, WIDE, GATED>(a, lds, nsmall, [&](int t) {
