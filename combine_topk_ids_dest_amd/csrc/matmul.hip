@@ -11,12 +11,15 @@
 // silu_gated: w holds N gate rows, then N up rows; a tile takes both rows of
 // each of its output columns.
 //
-// fp8: a slab of 128 codes is one scale block: acc += (sx * sw) * slab sum.
-// The fp8 matrix instruction drops product bits below 2^-13 of the largest
-// product it adds (measured: 1.4e-5 of the result over 7168 columns, against
-// 4e-7 in bf16). That vanishes under the rounding of a bf16 result (2^-8), so
-// bf16 outputs use it; for fp32 and e4m3 outputs, whose scales are fp32, the
-// codes are widened to bf16 (exactly) and multiplied there (`WIDE`).
+// fp8: a slab of 128 codes is one scale block: acc += (sx * sw) * slab sum. The
+// codes are widened to bf16 (exactly) and multiplied there. The fp8 matrix
+// instructions, of 32 and of 128 columns alike, drop product bits below 2^-13
+// of the largest product they add: 448 * 448 - 448 * 448 and 126 ones come out
+// as 120 (errors up to 9e-5 of the products' absolute sum were measured, in
+// bf16 3e-7), and sums are held in 32 bits here whatever the result's type. In
+// turn on one card, with the fp8 instruction and widened, bf16 results: 32
+// experts of 15575 rows, 2048 -> 7168, 337 and 503 us; 8 experts of 917 rows, 30
+// and 43; 8 experts of 480 rows, 7168 -> 2 x 2048, 50 and 82.
 #include <type_traits>
 
 #include "experts.h"
@@ -29,7 +32,6 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 
 constexpr int kThreads = 512;                    // of a block of big tiles
@@ -48,13 +50,6 @@ struct Frag {
 __device__ __forceinline__ f32x4 mma_bf16(const u32x4& w, const u32x4& x, f32x4 acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
                                                    __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
-}
-
-// e4m3 x e4m3 with the blocks' exponents at 1.0 (127)
-__device__ __forceinline__ f32x4 mma_fp8(const Frag& w, const Frag& x, f32x4 acc) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-        __builtin_bit_cast(i32x8, w), __builtin_bit_cast(i32x8, x), acc, 0, 0, 0, 0x7F7F7F7F, 0,
-        0x7F7F7F7F);
 }
 
 // 32 e4m3 codes as bf16, in code order.
@@ -279,7 +274,7 @@ __device__ __forceinline__ void small_fetch_scales(const MatmulArgs& a, const Sm
 
 // Works through the block's tiles, number t of `total` at place(t) = {g, m0,
 // rows, n0}.
-template <int EB, bool WIDE, bool GATED, class Next>
+template <int EB, bool GATED, class Next>
 __device__ __forceinline__ void small_tiles(const MatmulArgs& a, uint8_t* lds, int total,
                                             const Next& place) {
     const int lane = threadIdx.x & 63;
@@ -346,7 +341,7 @@ __device__ __forceinline__ void small_tiles(const MatmulArgs& a, uint8_t* lds, i
                     acc = mma_bf16(w.v[1], x.v[1], acc);
                 } else {
                     const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-                    const f32x4 t = WIDE ? mma_wide(widen(w), widen(x), zero) : mma_fp8(w, x, zero);
+                    const f32x4 t = mma_wide(widen(w), widen(x), zero);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) acc[q] = __builtin_fmaf(t[q], sc, acc[q]);
                 }
@@ -374,7 +369,7 @@ __device__ __forceinline__ void small_tiles(const MatmulArgs& a, uint8_t* lds, i
                 if (GATED) up += b[a.N];
             }
             v = GATED ? silu_gated(v, up) : apply_act(v, a.act);
-            const bool f32 = EB == 1 ? WIDE : a.out_dtype == MOE_EP_F32;
+            const bool f32 = a.out_dtype == MOE_EP_F32;
             const int64_t row = cur.m0 + m;
             if (a.res) {
                 const uint8_t* q = a.res + row * a.res_row;
@@ -514,7 +509,7 @@ struct TileScales {
 
 // The epilogue of a tile: bias, activation, residual and rounding, or the
 // quantising of rows.
-template <int EB, bool WIDE, bool GATED, int FRAGS, int JF, int WN>
+template <int EB, bool GATED, int FRAGS, int JF, int WN>
 __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int g, int m0, int left, int n0,
                                             f32x4 (&acc)[FRAGS][JF], uint8_t* lds) {
     const int lane = threadIdx.x & 63;
@@ -554,7 +549,7 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int g, int m0, 
             return v;
         };
 
-        if constexpr (EB == 1 && WIDE) {
+        if constexpr (EB == 1) {
             if (a.out_dtype == MOE_EP_E4M3) {
                 // a row's 128 columns lie in 4 (gated) or 2 waves, 4 lanes each
                 constexpr int WG = GATED ? 4 : 2;
@@ -600,7 +595,7 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int g, int m0, 
             }
         }
 
-        const bool f32 = EB == 1 ? WIDE : a.out_dtype == MOE_EP_F32;
+        const bool f32 = a.out_dtype == MOE_EP_F32;
         const int eb = f32 ? 4 : 2;
         const auto ro = row_rsrc(out, (int64_t)(left - 1) * a.out_row + (int64_t)a.N * eb);
         const auto rr = row_rsrc(a.res ? a.res + (int64_t)m0 * a.res_row : out,
@@ -678,7 +673,7 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int g, int m0, 
     }
 }
 
-template <int EB, bool WIDE, bool GATED, int BM>
+template <int EB, bool GATED, int BM>
 __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
                                          uint8_t* lds) {
     constexpr int JF = BM / 32;                   // fragments of x of a wave
@@ -838,44 +833,31 @@ __device__ __forceinline__ void big_tile(const MatmulArgs& a, int g, int m0, int
                 for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(t[q], f, acc[i][j][q]);
             };
             const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (WIDE) {
-                Wide w[4];
+            Wide w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = widen(frag(pw + i * 16 * kSlab));
+            for (int i = 0; i < 4; ++i) w[i] = widen(frag(pw + i * 16 * kSlab));
 #pragma unroll
-                for (int j = 0; j < JF; ++j) {
-                    const Wide x = widen(frag(px + j * 16 * kSlab));
-                    const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
-                    // two chains of products at a time: each waits for its own sum
+            for (int j = 0; j < JF; ++j) {
+                const Wide x = widen(frag(px + j * 16 * kSlab));
+                const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
+                // two chains of products at a time: each waits for its own sum
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        f32x4 t0 = zero, t1 = zero;
+                for (int i = 0; i < 4; i += 2) {
+                    f32x4 t0 = zero, t1 = zero;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            t0 = mma_bf16(w[i].v[q], x.v[q], t0);
-                            t1 = mma_bf16(w[i + 1].v[q], x.v[q], t1);
-                        }
-                        scale(i, j, t0, sx);
-                        scale(i + 1, j, t1, sx);
+                    for (int q = 0; q < 4; ++q) {
+                        t0 = mma_bf16(w[i].v[q], x.v[q], t0);
+                        t1 = mma_bf16(w[i + 1].v[q], x.v[q], t1);
                     }
-                }
-            } else {
-                Frag w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = frag(pw + i * 16 * kSlab);
-#pragma unroll
-                for (int j = 0; j < JF; ++j) {
-                    const Frag x = frag(px + j * 16 * kSlab);
-                    const float sx = sc[(wm * (JF * 16) + j * 16 + (lane & 15)) * 4 + (s & 3)];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) scale(i, j, mma_fp8(w[i], x, zero), sx);
+                    scale(i, j, t0, sx);
+                    scale(i + 1, j, t1, sx);
                 }
             }
             now = now + 1 < XS ? now + 1 : 0;
         }
     }
     wait_and_barrier<0>();   // LDS is free for what follows
-    finish_tile<EB, WIDE, GATED, 4, JF, 4>(a, g, m0, left, n0, acc, lds);
+    finish_tile<EB, GATED, 4, JF, 4>(a, g, m0, left, n0, acc, lds);
 }
 
 // ---------------------------------------------------------------------
@@ -896,7 +878,7 @@ constexpr int kPair = 2 * kSlab;
 constexpr int kPairX = kNarrow * kPair;
 constexpr int kUnit = 128 * kPair;
 
-template <int EB, bool WIDE, bool GATED>
+template <int EB, bool GATED>
 __device__ __forceinline__ void narrow_tile(const MatmulArgs& a, int g, int m0, int rows, int n0,
                                             uint8_t* lds) {
     constexpr int JF = 2;
@@ -1024,8 +1006,7 @@ __device__ __forceinline__ void narrow_tile(const MatmulArgs& a, int g, int m0, 
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-                            const f32x4 t = WIDE ? mma_wide(widen(f[i]), widen(fx[j]), zero)
-                                                 : mma_fp8(f[i], fx[j], zero);
+                            const f32x4 t = mma_wide(widen(f[i]), widen(fx[j]), zero);
                             const float b = sc[kBig * 4 + (GATED ? i : wn >> 1) * 4 + (sl & 3)];
                             const float v = in ? sx * b : 0.f;
 #pragma unroll
@@ -1040,7 +1021,7 @@ __device__ __forceinline__ void narrow_tile(const MatmulArgs& a, int g, int m0, 
         }
     }
     wait_and_barrier<0>();   // LDS is free for what follows
-    finish_tile<EB, WIDE, GATED, 4, JF, 4>(a, g, m0, left, n0, acc, lds);
+    finish_tile<EB, GATED, 4, JF, 4>(a, g, m0, left, n0, acc, lds);
 }
 
 // ---------------------------------------------------------------------
@@ -1139,7 +1120,7 @@ __device__ __forceinline__ void mid_tile(const MatmulArgs& a, int g, int m0, int
         iw = iw + 1 < WR ? iw + 1 : 0;
     }
     wait_and_barrier<0>();   // LDS is free for the next tile
-    finish_tile<2, false, GATED, 2, JF, WN>(a, g, m0, left, n0, acc, lds);
+    finish_tile<2, GATED, 2, JF, WN>(a, g, m0, left, n0, acc, lds);
 }
 
 template <bool GATED, int BM>
@@ -1238,7 +1219,7 @@ __device__ __forceinline__ Place find_tile(const MatmulArgs& a, int rows0, int s
     }
 }
 
-template <int EB, bool WIDE, bool GATED>
+template <int EB, bool GATED>
 __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a, int small_to) {
     __shared__ __align__(1024) uint8_t lds[kLds];
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
@@ -1313,7 +1294,7 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
         // (a tile of a run-time number of fragments was 18 % slower: its loop
         // is full of branches)
         auto run = [&](auto bm) {
-            big_tile<EB, WIDE, GATED, decltype(bm)::value>(a, at.g, p.m0, p.end, n0, lds);
+            big_tile<EB, GATED, decltype(bm)::value>(a, at.g, p.m0, p.end, n0, lds);
         };
         const int bm = tile_rows(p.fragments);
         if (bm == 256) run(std::integral_constant<int, 256>{});
@@ -1321,10 +1302,10 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
         else if (bm == 192) run(std::integral_constant<int, 192>{});
         else if (bm == 160) run(std::integral_constant<int, 160>{});
         else if (bm == 128) run(std::integral_constant<int, 128>{});
-        else narrow_tile<EB, WIDE, GATED>(a, at.g, p.m0, p.end, n0, lds);
+        else narrow_tile<EB, GATED>(a, at.g, p.m0, p.end, n0, lds);
     }
     if (nsmall > 0)
-        small_tiles<EB, WIDE, GATED>(a, lds, nsmall, [&](int t) {
+        small_tiles<EB, GATED>(a, lds, nsmall, [&](int t) {
             const Place at = find_tile(a, rows0, small_to, 0, nt, t);
             const int mt = cut_rows(at.rows, small_to).runs;
             return small_setup<EB, GATED>(a, at.g, at.l % mt * kSmall, at.rows, at.l / mt * BO);
@@ -1332,7 +1313,7 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
 }
 
 // Small tiles alone, where the host knows that there are few rows.
-template <int EB, bool WIDE, bool GATED>
+template <int EB, bool GATED>
 __global__ __launch_bounds__(kThreads, 2) void small_kernel(const MatmulArgs a) {
     __shared__ __align__(1024) uint8_t lds[kSmallLds];
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
@@ -1340,7 +1321,7 @@ __global__ __launch_bounds__(kThreads, 2) void small_kernel(const MatmulArgs a) 
     const int rows0 = lane_rows(a, 0);
     int n[kKinds];
     count_runs(a, rows0, INT32_MAX, n);
-    small_tiles<EB, WIDE, GATED>(a, lds, n[0] * nt, [&](int t) {
+    small_tiles<EB, GATED>(a, lds, n[0] * nt, [&](int t) {
         const Place at = find_tile(a, rows0, INT32_MAX, 0, nt, t);
         const int mt = cut_rows(at.rows, INT32_MAX).runs;
         return small_setup<EB, GATED>(a, at.g, at.l % mt * kSmall, at.rows, at.l / mt * BO);
@@ -1372,7 +1353,7 @@ Estimate estimate(int64_t rows, int64_t nw, int64_t row_bytes) {
     return e;
 }
 
-template <int EB, bool WIDE, bool GATED>
+template <int EB, bool GATED>
 hipError_t launch(const MatmulArgs& a, hipStream_t st) {
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
     const bool e4m3 = a.out_dtype == MOE_EP_E4M3;
@@ -1395,9 +1376,9 @@ hipError_t launch(const MatmulArgs& a, hipStream_t st) {
     }
     if (few) {
         const int64_t grid = small < kGrid ? (small + 7) / 8 * 8 : kGrid;
-        small_kernel<EB, WIDE, GATED><<<(unsigned)grid, kThreads, 0, st>>>(a);
+        small_kernel<EB, GATED><<<(unsigned)grid, kThreads, 0, st>>>(a);
     } else {
-        matmul_kernel<EB, WIDE, GATED>
+        matmul_kernel<EB, GATED>
             <<<kGrid, kThreads, 0, st>>>(a, e4m3 || !a.counts ? 0 : kSmall);
     }
     return hipGetLastError();
@@ -1407,10 +1388,8 @@ hipError_t launch(const MatmulArgs& a, hipStream_t st) {
 
 hipError_t launch_matmul(const MatmulArgs& a, hipStream_t st) {
     const bool gated = a.act == MOE_EP_ACT_SILU_GATED;
-    if (!a.fp8) return gated ? launch<2, false, true>(a, st) : launch<2, false, false>(a, st);
-    if (a.out_dtype == MOE_EP_BF16)
-        return gated ? launch<1, false, true>(a, st) : launch<1, false, false>(a, st);
-    return gated ? launch<1, true, true>(a, st) : launch<1, true, false>(a, st);
+    if (!a.fp8) return gated ? launch<2, true>(a, st) : launch<2, false>(a, st);
+    return gated ? launch<1, true>(a, st) : launch<1, false>(a, st);
 }
 
 }  // namespace moe_ep

@@ -585,10 +585,8 @@ MOE_EP_API int moe_ep_expert_matmul(const void* x, int64_t x_stride, const void*
  * moe_ep_expert_matmul on OCP fp8 E4M3 codes: rows as moe_ep_dispatch_pack_fp8
  * (group 128) sends and moe_ep_expert_batch batches them, weights with one
  * scale per 128 x 128 block. With S the sum of the products of 128 columns'
- * codes, sums add (x_scale * w_scale) * S in fp32. For fp32 and E4M3 outputs S
- * is an fp32 sum as well; for bf16 outputs it is that of the fp8 matrix
- * instruction, which drops product bits below 2^-13 of the largest product it
- * adds (1.4e-5 of a result over 7168 columns, where bf16 rounds to 2^-8).
+ * codes, sums add (x_scale * w_scale) * S in fp32. S is an fp32 sum as well, of
+ * exact products.
  *
  *   x             codes [e_local, rows, H] (one byte; x_stride bytes between
  *                 experts), H % 128 == 0.
