@@ -156,6 +156,7 @@ class LogicalEP:
         self._calls = {}
         self._events = {}
         self._layer = None
+        self._lane_graphs = None
 
     # -- inputs ---------------------------------------------------------
     def set_source(self, s: int, ids, wts, payload_rows: Sequence):
@@ -191,7 +192,12 @@ class LogicalEP:
         set_source stand); route: further arguments of moe_ep_route_topk
         (score, bias, n_group, topk_group, renormalize, scale). shared13
         [2S, H], shared2 [H, S]: bf16, the expert that every token passes
-        through."""
+        through.
+
+        A new layer ends the graphs of capture_lane_graphs: they read and
+        write the buffers of the layer that they were captured with. So do
+        graphs of step() that a caller has captured: replay none of them
+        behind another set_layer."""
         fp8 = self.quant_group is not None
         if self.quant_fp4 or (fp8 and self.quant_group != B.SCALE_BLOCK):
             raise ValueError("the experts take bf16 rows or fp8 rows in groups of 128")
@@ -226,6 +232,7 @@ class LogicalEP:
                                for _ in range(self.lanes)]
         self._layer = layer
         self._calls = {}
+        self._lane_graphs = None
 
     def _source_rows(self, s: int):
         return self.src[0][s].view(torch.bfloat16).view(self.T, self.H)
@@ -476,7 +483,8 @@ class LogicalEP:
 
     def capture_lane_graphs(self, fused_local=False):
         """Captures the lane graphs (after one eager step, so that every call
-        is marshalled). Replay them with step_graphs."""
+        is marshalled). Replay them with step_graphs, until set_layer."""
+        self._lane_graphs = None
         self.step(fused_local=fused_local)
         torch.cuda.synchronize()
         graphs = []
@@ -496,6 +504,8 @@ class LogicalEP:
         streams[lane]; the phases are joined across the streams as in step.
         Ordered after the work on `stream` (default: the current stream),
         which waits for the whole step."""
+        if self._lane_graphs is None:
+            raise RuntimeError("no lane graphs of this layer: call capture_lane_graphs first")
         if len(streams) != self.lanes:
             raise ValueError("one stream per lane")
         main = stream if stream is not None else torch.cuda.current_stream()
