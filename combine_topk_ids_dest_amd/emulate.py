@@ -277,6 +277,11 @@ class LogicalEP:
         for call in self._prepared("shared", s):
             call(stream)
 
+    def _check_fused(self, fused_local: bool):
+        if fused_local and self._layer is not None:
+            raise ValueError("the fused combine reads each rank's own expert outputs, "
+                             "and here the ranks of a lane share one buffer of them")
+
     # the three parts of a step, for one rank, in the order of its lane
     def _send(self, s: int, stream=None):
         if self._layer is not None and self._layer["gate"] is not None:
@@ -286,9 +291,6 @@ class LogicalEP:
     def _serve(self, r: int, fused_local: bool, stream=None):
         self.batch(r, stream)
         if self._layer is not None:
-            if fused_local:
-                raise ValueError("the fused combine reads each rank's own expert outputs, "
-                                 "and here the ranks of a lane share one buffer of them")
             self.experts(r, stream)
         if fused_local:
             self.reduce_peers(r, stream)
@@ -431,7 +433,9 @@ class LogicalEP:
         after the previous phase has ended on all of them. The step is
         ordered after the work already on `stream` (default: the current
         stream), and that stream waits for the whole step. A step over
-        several lanes runs eagerly only (not under HIP graph capture)."""
+        several lanes runs eagerly only (not under HIP graph capture). With a
+        layer fused_local is refused."""
+        self._check_fused(fused_local)
         if streams is None:
             lane_of = [stream] * self.W
         else:
@@ -484,6 +488,7 @@ class LogicalEP:
     def capture_lane_graphs(self, fused_local=False):
         """Captures the lane graphs (after one eager step, so that every call
         is marshalled). Replay them with step_graphs, until set_layer."""
+        self._check_fused(fused_local)
         self._lane_graphs = None
         self.step(fused_local=fused_local)
         torch.cuda.synchronize()

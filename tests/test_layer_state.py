@@ -52,6 +52,20 @@ def test_a_refused_layer_leaves_the_graphs():
     assert ep._lane_graphs is graphs
 
 
+def test_a_fused_step_with_a_layer_is_refused_before_anything_is_enqueued():
+    ep = _ep()
+    ep.set_layer(**_weights())
+    graphs = ep._lane_graphs = [[_Graph()] for _ in range(3)]
+    calls = []
+    ep._prepared = lambda kind, i: calls.append(kind) or (lambda stream: None)
+    for refused in (lambda: ep.step(fused_local=True),
+                    lambda: ep.step(fused_local=True, streams=[None]),
+                    lambda: ep.capture_lane_graphs(fused_local=True)):
+        with pytest.raises(ValueError, match="share one buffer"):
+            refused()
+    assert calls == [] and ep._lane_graphs is graphs
+
+
 @pytest.mark.gpu
 def test_graphs_of_a_new_layer_run_the_new_layer():
     from test_gpu_layer import ROUTE, build, check, weights
