@@ -187,7 +187,9 @@ class LogicalEP:
         w13 [E, 2I, H] (gate rows, then up rows), w2 [E, H, I]: every rank's
         experts, bf16; or, where the pack quantises payload 0 to fp8 in
         groups of 128, e4m3 codes with block scales w13_scale
-        [E, 2 ceil(I/128), H/128] and w2_scale [E, ceil(H/128), I/128].
+        [E, 2 ceil(I/128), H/128] and w2_scale [E, ceil(H/128), I/128]
+        (copied here if a rank's experts do not start on a 16-byte boundary
+        in them; an expert stride of a multiple of 4 saves that).
         gate: bf16 [E, H], the router (without it the ids and weights of
         set_source stand); route: further arguments of moe_ep_route_topk
         (score, bias, n_group, topk_group, renormalize, scale). shared13
@@ -213,6 +215,8 @@ class LogicalEP:
             raise ValueError("block scales go with rows that the pack quantises")
         if (shared13 is None) != (shared2 is None):
             raise ValueError("shared13 and shared2 go together")
+        if fp8:
+            w13_scale, w2_scale = self._aligned_scales(w13_scale), self._aligned_scales(w2_scale)
         el, ecap, dev = self.e_local, self.expert_cap, self.device
         layer = dict(w13=w13, w2=w2, w13_scale=w13_scale, w2_scale=w2_scale, gate=gate,
                      route=dict(route or {}), shared13=shared13, shared2=shared2)
@@ -233,6 +237,17 @@ class LogicalEP:
         self._layer = layer
         self._calls = {}
         self._lane_graphs = None
+
+    def _aligned_scales(self, scale: torch.Tensor) -> torch.Tensor:
+        """scale [E, ., .] itself if every rank's experts start on a 16-byte
+        boundary, as the product takes them, else a copy whose experts do."""
+        if scale.dim() != 3 or scale.size(0) != self.E:
+            raise ValueError("block scales must be [E, ., .]")
+        if all(scale[r * self.e_local].data_ptr() % 16 == 0 for r in range(self.W)):
+            return scale
+        per = scale.size(1) * scale.size(2)
+        room = scale.new_zeros((self.E, (per + 3) // 4 * 4))
+        return room[:, :per].view(self.E, scale.size(1), scale.size(2)).copy_(scale)
 
     def _source_rows(self, s: int):
         return self.src[0][s].view(torch.bfloat16).view(self.T, self.H)

@@ -603,6 +603,8 @@ MOE_EP_API int moe_ep_expert_matmul(const void* x, int64_t x_stride, const void*
  *   out_scale     fp32 [e_local, rows, Np], Np = N / 128 rounded up to 4, its
  *                 padding written +0.0; out_scale_stride elements between
  *                 experts (>= rows * Np). NULL for the other types.
+ * x_scale, w_scale and out_scale start on 16-byte boundaries, x_scale_stride and
+ * out_scale_stride are multiples of 4; w_scale_stride may be any (EALIGN).
  * Everything else as moe_ep_expert_matmul. EDTYPE for another out_dtype.
  */
 MOE_EP_API int moe_ep_expert_matmul_fp8(const void* x, int64_t x_stride, const float* x_scale,

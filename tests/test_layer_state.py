@@ -66,6 +66,26 @@ def test_a_fused_step_with_a_layer_is_refused_before_anything_is_enqueued():
     assert calls == [] and ep._lane_graphs is graphs
 
 
+@pytest.mark.parametrize("E,H,inter", [(8, 384, 128), (8, 256, 384), (16, 640, 640), (8, 512, 128)])
+def test_every_rank_s_block_scales_start_aligned(E, H, inter):
+    """The fp8 product takes block scales from a 16-byte boundary on; with an odd
+    number of blocks an expert, a rank's slice of dense scales starts at 4, 8 or
+    12 bytes."""
+    ep = LogicalEP(T=4, H=H, E=E, K=2, W=8, cap=4, row_bytes=[2 * H], combine_dtype=torch.bfloat16,
+                   device="cpu", quant_group=128)
+    s13 = torch.rand(E, 2 * (-(-inter // 128)), H // 128)
+    s2 = torch.rand(E, H // 128, inter // 128)
+    f8 = torch.float8_e4m3fn
+    ep.set_layer(torch.zeros(E, 2 * inter, H, dtype=f8), torch.zeros(E, H, inter, dtype=f8), s13, s2)
+    per = E // 8
+    for name, given in (("w13_scale", s13), ("w2_scale", s2)):
+        for r in range(8):
+            mine = ep._layer[name][r * per:(r + 1) * per]
+            assert mine.data_ptr() % 16 == 0, (name, r)
+            assert torch.equal(mine, given[r * per:(r + 1) * per])
+            assert mine[0].is_contiguous()
+
+
 @pytest.mark.gpu
 def test_graphs_of_a_new_layer_run_the_new_layer():
     from test_gpu_layer import ROUTE, build, check, weights
@@ -86,3 +106,12 @@ def test_graphs_of_a_new_layer_run_the_new_layer():
         ep.step_graphs(streams)
         torch.cuda.synchronize()
         check(ep, xs, d, f13, f2, False)
+
+
+@pytest.mark.gpu
+def test_layer_with_an_odd_number_of_block_scales_a_rank():
+    from test_gpu_layer import build, check
+    ep, *rest = build(8, 8, 2, 40, 384, 128, 64, True)
+    ep.step()
+    torch.cuda.synchronize()
+    check(ep, *rest, True)
