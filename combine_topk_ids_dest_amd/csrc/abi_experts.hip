@@ -31,7 +31,8 @@ inline bool covers(int64_t stride, int64_t rows, int64_t width, int64_t blocks, 
 // Sizes that the calls share; nw = rows of w.
 int check_sizes(int32_t groups, int64_t rows, int64_t H, int64_t N, int32_t act, int64_t w_row,
                 int64_t* nw) {
-    if (groups <= 0 || groups > MOE_EP_MAX_LOCAL_EXPERTS || rows < 0 || rows > INT_MAX ||
+    // sums like rows + 255 (runs of rows, and where they end) stay below 2^31
+    if (groups <= 0 || groups > MOE_EP_MAX_LOCAL_EXPERTS || rows < 0 || rows > INT_MAX - 255 ||
         H <= 0 || H > MOE_EP_MAX_WIDTH || N <= 0 || N > MOE_EP_MAX_WIDTH)
         return MOE_EP_EINVAL;
     if (act < MOE_EP_ACT_NONE || act > MOE_EP_ACT_SILU_GATED) return MOE_EP_EINVAL;

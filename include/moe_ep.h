@@ -572,7 +572,7 @@ MOE_EP_API int moe_ep_route_topk(const void* logits, int64_t logits_stride, int3
  *                 out + e * out_stride (>= rows * N). Must not overlap x or w.
  * Rows of x, w and out, their strides, bias and its stride are multiples of
  * 16 bytes (EALIGN). Limits: H, N <= MOE_EP_MAX_WIDTH, Nw * H * 2 < 2^31
- * bytes, e_local <= 1024, rows <= INT_MAX and e_local * ceil(rows / 16) *
+ * bytes, e_local <= 1024, rows <= INT_MAX - 255 and e_local * ceil(rows / 16) *
  * ceil(N / 8) < 2^30.
  */
 MOE_EP_API int moe_ep_expert_matmul(const void* x, int64_t x_stride, const void* w,
