@@ -146,9 +146,21 @@ def _check(name: str, status: int):
         raise MoeEpError(name, status, status_string(status))
 
 
+def _raw_stream_lookup(c):
+    """The look-up of a device's current stream handle: torch's raw one, which
+    makes no Stream object, where this torch has it, else the public one."""
+    raw = getattr(c, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return raw
+    return lambda device: torch.cuda.current_stream(device).cuda_stream
+
+
+_raw_stream = _raw_stream_lookup(torch._C)
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -385,7 +397,7 @@ class PreparedCall:
             dev = torch.cuda.current_device()
             if self.device is not None and dev != self.device:
                 self._wrong_device(dev)
-            status = self.fn(*self.args, torch._C._cuda_getCurrentRawStream(dev))
+            status = self.fn(*self.args, _raw_stream(dev))
         else:
             if self.device is not None and not isinstance(stream, int) and \
                     stream.device.index != self.device:
