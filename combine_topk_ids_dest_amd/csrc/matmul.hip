@@ -108,6 +108,16 @@ __device__ __forceinline__ float abs_max(float m, float x) {
     return a > m ? a : m;
 }
 
+// amax / 448, or 1 without an amax. Among fp32's smallest numbers that rounds
+// to 0, or so far down that amax / s is past what rounds to the largest code
+// (464 to 448), and the codes would be NaN: there the scale is the number above.
+// (A row of bf16, as the pack quantises it, has no amax so small.)
+__device__ __forceinline__ float group_scale(float amax) {
+    const float s = amax / 448.0f;
+    if (s * 460.0f < amax) return __uint_as_float(__float_as_uint(s) + 1);
+    return amax > 0.f ? s : 1.0f;
+}
+
 // Four e4m3 codes of v / s; each carries the sign of its input.
 __device__ __forceinline__ uint32_t codes4(f32x4 v, float s) {
     float q[4];
@@ -576,7 +586,7 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int g, int m0, 
                     float mx = 0.f;
 #pragma unroll
                     for (int w = 0; w < WG; ++w) mx = abs_max(mx, part[m * 4 + (GATED ? 0 : wn & 2) + w]);
-                    const float s = mx > 0.f ? mx / 448.0f : 1.0f;
+                    const float s = group_scale(mx);
                     if (m < left && n < a.N) {
                         uint32_t* o = reinterpret_cast<uint32_t*>(out + (int64_t)m * a.out_row + n);
 #pragma unroll

@@ -599,7 +599,9 @@ MOE_EP_API int moe_ep_expert_matmul(const void* x, int64_t x_stride, const void*
  *                 experts (>= Bn * H / 128).
  *   out           bf16, fp32, or with MOE_EP_E4M3 codes (N % 128 == 0;
  *                 out_stride bytes) quantised as moe_ep_dispatch_pack_fp8
- *                 quantises 128 columns, from the fp32 results, with
+ *                 quantises 128 columns, from the fp32 results, with (for an
+ *                 amax below 2^-136 the scale may be one step above amax / 448,
+ *                 where rounded down it leaves values past the largest code)
  *   out_scale     fp32 [e_local, rows, Np], Np = N / 128 rounded up to 4, its
  *                 padding written +0.0; out_scale_stride elements between
  *                 experts (>= rows * Np). NULL for the other types.
