@@ -3,9 +3,9 @@
 //   out[g][r][n] = act(sum_k x[g][r][k] * w[g][n][k] + bias[g][n]) + residual.
 // Sums are fp32 in the matrix cores. x and w are both stored with k innermost,
 // so both operands of an MFMA load the same way: a lane of a 16-row fragment
-// takes 32 consecutive bytes of row lane % 16 from every 128-byte slab of k
-// (any assignment of k to lanes gives the same sum as long as both operands
-// share it). w is the A operand: a lane's accumulators are consecutive output
+// takes two 16-byte chunks of row lane % 16 from every 128-byte slab of k (any
+// assignment of k to lanes gives the same sum as long as both operands share
+// it). w is the A operand: a lane's accumulators are consecutive output
 // columns of one row of x, so the epilogue works on vectors.
 //
 // silu_gated: w holds N gate rows, then N up rows; a tile takes both rows of
@@ -1253,8 +1253,8 @@ __global__ __launch_bounds__(kThreads, 2) void matmul_kernel(const MatmulArgs a,
     if constexpr (EB == 2) {
         // Few enough of them that even cut in parts they would leave CUs idle
         // or share their weights' bytes among them: middle tiles, where one
-        // round does (8 experts of 115 rows, 7168 -> 2 x 2048: 106 us with them,
-        // 112 without; one of 200: 29 and 62).
+        // round does (8 experts of 115 rows, 7168 -> 2 x 2048: 101 us with them,
+        // 113 without; one of 200: 31 and 73).
         constexpr int G = GATED ? 2 : 1;
         const int nt64 = (a.N * G + 63) / 64, nt128 = (a.N * G + 127) / 128;
         if (total > 0 && total <= kGrid / 2) {
@@ -1341,8 +1341,10 @@ __global__ __launch_bounds__(kThreads, 2) void small_kernel(const MatmulArgs a) 
 // What a product over all tokens takes with each kind of tile, in us, from the
 // tiles' measured times: rounds of the grid times a tile's start and its pairs
 // of slabs. Both sides measured where the choice turns, in us: 4096 x 7168 by
-// 256 rows of w: 64 x 64 tiles 37, big 82, 16 x 16 135; 128 rows of that: 16 x 16
-// 10, 64 x 64 24; 2048 x 7168 by 4096 rows: big 99, 128 x 128 125 to 129.
+// 256 rows of w: 64 x 64 tiles 37, big 39, 16 x 16 138; 128 rows of that: 16 x 16
+// 8, 64 x 64 26; 2048 x 7168 by 4096 rows: big 99, 128 x 128 127; 576 x 2048 by
+// 7168 rows: big 29 to 31 (parts of 96 rows, priced so, in 128-row tiles), 128 x
+// 128 37 to 39.
 struct Estimate {
     double small, mid64, mid128, big;
 };

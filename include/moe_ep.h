@@ -631,6 +631,8 @@ MOE_EP_API int moe_ep_expert_matmul_fp8(const void* x, int64_t x_stride, const f
  *   residual      [T, N] of out_dtype, nullable; residual_stride elements
  *                 between tokens (>= N). May be out itself (same stride).
  *   out           bf16 or fp32 [T, N], out_stride elements between tokens.
+ *                 Shares no element with x, w or bias, nor with a residual that
+ *                 is not out itself.
  * Rows, strides and pointers are multiples of 16 bytes (EALIGN). Strides of
  * x, residual and out are below 2^23 bytes; limits as for
  * moe_ep_expert_matmul (Nw * w_stride * 2 < 2^31 bytes).
