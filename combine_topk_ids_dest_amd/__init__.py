@@ -9,6 +9,8 @@ exchange between ranks is a rank-stride view of the send buffers.
 from .binding import (  # noqa: F401
     MoeEpError,
     load,
+    moe_ep_balance_loss,
+    moe_ep_balance_workspace_bytes,
     moe_ep_capacities,
     moe_ep_combine_reduce,
     moe_ep_combine_reduce_peers,
@@ -22,7 +24,10 @@ from .binding import (  # noqa: F401
     moe_ep_expert_batch_plan,
     moe_ep_expert_matmul,
     moe_ep_expert_matmul_fp8,
+    moe_ep_expert_matmul_w4,
     moe_ep_matmul,
+    moe_ep_matmul_w4,
+    moe_ep_route_backward,
     moe_ep_route_topk,
     moe_ep_sanitize_expert_ids,
     moe_ep_workspace_bytes,

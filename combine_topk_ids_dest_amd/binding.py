@@ -47,6 +47,11 @@ EXPORTED = (
     "moe_ep_expert_matmul",
     "moe_ep_expert_matmul_fp8",
     "moe_ep_matmul",
+    "moe_ep_expert_matmul_w4",
+    "moe_ep_matmul_w4",
+    "moe_ep_balance_workspace_bytes",
+    "moe_ep_balance_loss",
+    "moe_ep_route_backward",
 )
 
 
@@ -129,6 +134,18 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         _P, _I64, _I32, _P, _I64, _P]
     lib.moe_ep_matmul.argtypes = [
         _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64, _I32, _P]
+    lib.moe_ep_expert_matmul_w4.argtypes = [
+        _P, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _I64, _P, _I32, _I64, _I64, _I64, _I32,
+        _P, _I64, _I32, _P]
+    lib.moe_ep_matmul_w4.argtypes = [
+        _P, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _I64, _I64, _I64, _I32, _P, _I64, _P, _I64,
+        _I32, _P]
+    lib.moe_ep_balance_workspace_bytes.argtypes = [_I64, _I32, _I32, _P]
+    lib.moe_ep_balance_loss.argtypes = [
+        _P, _I64, _I32, _P, _I64, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P, _SZ, _P]
+    lib.moe_ep_route_backward.argtypes = [
+        _P, _I64, _I32, _P, _I64, _I32, _I32, _I32, _I32, _F32, _P, _P, _I32, _P, _P, _P,
+        _P, _I64, _I32, _P]
     for name in EXPORTED:
         if name != "moe_ep_status_string":
             getattr(lib, name).restype = ctypes.c_int
@@ -1068,3 +1085,227 @@ def prepare_matmul(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, act: str
 
 def moe_ep_matmul(x, w, out, act="none", bias=None, residual=None, stream=None) -> None:
     prepare_matmul(x, w, out, act, bias, residual)(stream)
+
+
+# ---------------------------------------------------------------------------
+# Products with 4-bit weights
+# ---------------------------------------------------------------------------
+
+# what a group of columns' scales may be held in: E4M3 codes per 16, E8M0 per 32
+_W4_SCALE_T = {16: (torch.uint8, torch.float8_e4m3fn), 32: (torch.uint8, torch.float8_e8m0fnu)}
+
+
+def w4_scale_pitch(H: int, group: int) -> int:
+    """Bytes of a row of 4-bit weights' scales: H/group rounded up to 16."""
+    return (H // group + 15) // 16 * 16
+
+
+def _w4(x, w, w_scale, group, act, N, w_global, lead):
+    """Shapes that the products with 4-bit weights share; lead: the dims in
+    front of a matrix. Returns the act code and the rows of w."""
+    if group not in _W4_SCALE_T:
+        raise ValueError(f"group must be one of {sorted(_W4_SCALE_T)}, not {group!r}")
+    if x.dtype != torch.bfloat16:
+        raise ValueError("x must be bfloat16")
+    H = x.size(-1)
+    if H % 32:
+        raise ValueError(f"x: {H} columns, a multiple of 32 expected")
+    code = _choice(ACTS, act, "act")
+    halves = 2 if act == "silu_gated" else 1
+    nw = halves * N
+    _shape(w, (*lead, nw, H // 2), "w", (torch.uint8,))
+    if w_scale.dim() != w.dim() or w_scale.dtype not in _W4_SCALE_T[group]:
+        raise ValueError(f"w_scale: {w.dim()} dims of {_W4_SCALE_T[group]} expected")
+    if w_global is not None:
+        _shape(w_global, (*lead, halves), "w_global", _F32T)
+        _dense_from(w_global, 0, "w_global")
+    return code, nw
+
+
+def prepare_expert_matmul_w4(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                             expert_num_tokens: torch.Tensor, out: torch.Tensor, group: int = 16,
+                             act: str = "none", bias: Optional[torch.Tensor] = None,
+                             w_global: Optional[torch.Tensor] = None) -> PreparedCall:
+    """x, out, bias, expert_num_tokens as for prepare_expert_matmul; w: E2M1
+    codes, uint8 [e_local, N, H / 2] (2N rows for silu_gated); w_scale:
+    [e_local, N, w4_scale_pitch(H, group)] E4M3 codes (group 16: uint8 or
+    float8_e4m3fn) or E8M0 codes (group 32: uint8 or float8_e8m0fnu); w_global:
+    fp32 [e_local, 1] ([e_local, 2] for silu_gated: gate, up)."""
+    if x.dim() != 3 or w.dim() != 3 or out.dim() != 3:
+        raise ValueError("x, w and out must be [e_local, ., .]")
+    e, rows, H = x.shape
+    N = out.size(2)
+    code, nw = _w4(x, w, w_scale, group, act, N, w_global, (e,))
+    _shape(w_scale, (e, nw, w4_scale_pitch(H, group)), "w_scale")
+    _shape(out, (e, rows, N), "out", (torch.bfloat16, torch.float32))
+    for t, n in ((x, "x"), (w, "w"), (w_scale, "w_scale"), (out, "out")):
+        _rows_dense(t, 1, n)
+    if bias is not None:
+        _shape(bias, (e, nw), "bias", _F32T)
+        _rows_dense(bias, 1, "bias")
+    _shape(expert_num_tokens, (e,), "expert_num_tokens", _I32T)
+    _dense_from(expert_num_tokens, 0, "expert_num_tokens")
+    args = (_ptr(x), _lead_stride(x), _ptr(w), _lead_stride(w), _ptr(w_scale),
+            _lead_stride(w_scale), group, _ptr(w_global), _ptr(bias),
+            0 if bias is None else _lead_stride(bias), _ptr(expert_num_tokens), e, rows, H, N,
+            code, _ptr(out), _lead_stride(out), _dtype_code(out))
+    return PreparedCall("moe_ep_expert_matmul_w4", args,
+                        (x, w, w_scale, expert_num_tokens, out, bias, w_global))
+
+
+def moe_ep_expert_matmul_w4(x, w, w_scale, expert_num_tokens, out, group=16, act="none",
+                            bias=None, w_global=None, stream=None) -> None:
+    prepare_expert_matmul_w4(x, w, w_scale, expert_num_tokens, out, group, act, bias,
+                             w_global)(stream)
+
+
+def prepare_matmul_w4(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, out: torch.Tensor,
+                      group: int = 16, act: str = "none", bias: Optional[torch.Tensor] = None,
+                      residual: Optional[torch.Tensor] = None,
+                      w_global: Optional[torch.Tensor] = None) -> PreparedCall:
+    """x, out, bias, residual as for prepare_matmul; w: E2M1 codes, uint8
+    [N, H / 2] (2N rows for silu_gated); w_scale: [N, >= H / group] of the types
+    of prepare_expert_matmul_w4; w_global: fp32 [1] ([2] for silu_gated). The
+    row stride of each is free."""
+    for t, n in ((x, "x"), (w, "w"), (out, "out")):
+        if t.dim() != 2:
+            raise ValueError(f"{n} must have two dims")
+        _rows_dense(t, 1, n)
+    T, H = x.shape
+    N = out.size(1)
+    code, nw = _w4(x, w, w_scale, group, act, N, w_global, ())
+    _lead_at_least(w_scale, (nw, H // group), "w_scale")
+    if w_scale.size(0) != nw:
+        raise ValueError(f"w_scale: {w_scale.size(0)} rows, expected {nw}")
+    _rows_dense(w_scale, 1, "w_scale")
+    _shape(out, (T, N), "out", (torch.bfloat16, torch.float32))
+    if bias is not None:
+        _shape(bias, (nw,), "bias", _F32T)
+        _dense_from(bias, 0, "bias")
+    if residual is not None:
+        _shape(residual, (T, N), "residual", (out.dtype,))
+        _rows_dense(residual, 1, "residual")
+    args = (_ptr(x), _lead_stride(x), _ptr(w), _lead_stride(w), _ptr(w_scale),
+            _lead_stride(w_scale), group, _ptr(w_global), _ptr(bias), T, H, N, code,
+            _ptr(residual), 0 if residual is None else _lead_stride(residual), _ptr(out),
+            _lead_stride(out), _dtype_code(out))
+    return PreparedCall("moe_ep_matmul_w4", args, (x, w, w_scale, out, bias, residual, w_global))
+
+
+def moe_ep_matmul_w4(x, w, w_scale, out, group=16, act="none", bias=None, residual=None,
+                     w_global=None, stream=None) -> None:
+    prepare_matmul_w4(x, w, w_scale, out, group, act, bias, residual, w_global)(stream)
+
+
+# ---------------------------------------------------------------------------
+# The router's training terms
+# ---------------------------------------------------------------------------
+
+def moe_ep_balance_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_ep_balance_workspace_bytes",
+           load().moe_ep_balance_workspace_bytes(T, E, S, ctypes.byref(b)))
+    return b.value
+
+
+def _routed(logits, topk_ids):
+    """Checks logits [T, E] (token stride free) and topk_ids [T, K]; returns
+    (T, E, K, dtype code)."""
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits must be [T, E] and topk_ids [T, K]")
+    T, E = logits.shape
+    K = topk_ids.size(1)
+    dtype = _dtype_code(logits)
+    _rows_dense(logits, 1, "logits")
+    _shape(topk_ids, (T, K), "topk_ids", _I32T)
+    _dense_from(topk_ids, 0, "topk_ids")
+    return T, E, K, dtype
+
+
+def _sequences(seq_start, S, *dense):
+    """seq_start int32 [S + 1] (None: S must be 1) and dense (tensor, shape,
+    name, types)."""
+    if seq_start is None:
+        if S != 1:
+            raise ValueError("several sequences need seq_start")
+    else:
+        _shape(seq_start, (S + 1,), "seq_start", _I32T)
+        _dense_from(seq_start, 0, "seq_start")
+    for t, shape, name, types in dense:
+        _shape(t, shape, name, types)
+        _dense_from(t, 0, name)
+
+
+def prepare_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, counts: torch.Tensor,
+                         tokens: torch.Tensor, mean_score: torch.Tensor, loss: torch.Tensor,
+                         workspace: Optional[torch.Tensor] = None, score: str = "softmax",
+                         seq_start: Optional[torch.Tensor] = None) -> PreparedCall:
+    """logits: bf16 or fp32 [T, E] (token stride free); topk_ids: int32 [T, K];
+    out: counts int32 [S, E], tokens int32 [S], mean_score fp32 [S, E], loss
+    fp32 [S]; workspace: moe_ep_balance_workspace_bytes(T, E, S) bytes;
+    seq_start: int32 [S + 1] (None: one sequence of all tokens)."""
+    T, E, K, dtype = _routed(logits, topk_ids)
+    if loss.dim() != 1:
+        raise ValueError("loss must be [S]")
+    S = loss.size(0)
+    _sequences(seq_start, S, (counts, (S, E), "counts", _I32T), (tokens, (S,), "tokens", _I32T),
+               (mean_score, (S, E), "mean_score", _F32T), (loss, (S,), "loss", _F32T))
+    if workspace is not None:
+        _dense_from(workspace, 0, "workspace")
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    args = (_ptr(logits), _lead_stride(logits), dtype, _ptr(topk_ids), T, E, K,
+            _choice(SCORES, score, "score"), _ptr(seq_start), S, _ptr(counts), _ptr(tokens),
+            _ptr(mean_score), _ptr(loss), _ptr(workspace), size)
+    return PreparedCall("moe_ep_balance_loss", args,
+                        (logits, topk_ids, counts, tokens, mean_score, loss, workspace, seq_start))
+
+
+def moe_ep_balance_loss(logits, topk_ids, counts, tokens, mean_score, loss, workspace=None,
+                        score="softmax", seq_start=None, stream=None) -> None:
+    prepare_balance_loss(logits, topk_ids, counts, tokens, mean_score, loss, workspace, score,
+                         seq_start)(stream)
+
+
+def prepare_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor,
+                           grad_logits: torch.Tensor, score: str = "softmax",
+                           renormalize: bool = True, scale: float = 1.0,
+                           grad_weights: Optional[torch.Tensor] = None,
+                           grad_loss: Optional[torch.Tensor] = None,
+                           counts: Optional[torch.Tensor] = None,
+                           tokens: Optional[torch.Tensor] = None,
+                           seq_start: Optional[torch.Tensor] = None) -> PreparedCall:
+    """logits, topk_ids, score, renormalize, scale: those of the forward calls;
+    grad_logits: bf16 or fp32 [T, E] (token stride free; may be logits);
+    grad_weights: fp32 [T, K]; grad_loss: fp32 [S], with counts [S, E], tokens
+    [S] and seq_start of prepare_balance_loss."""
+    T, E, K, dtype = _routed(logits, topk_ids)
+    _shape(grad_logits, (T, E), "grad_logits")
+    _rows_dense(grad_logits, 1, "grad_logits")
+    if grad_weights is None and grad_loss is None:
+        raise ValueError("a gradient is needed: grad_weights, grad_loss or both")
+    if grad_weights is not None:
+        _shape(grad_weights, (T, K), "grad_weights", _F32T)
+        _dense_from(grad_weights, 0, "grad_weights")
+    S = 1
+    if grad_loss is not None:
+        if grad_loss.dim() != 1:
+            raise ValueError("grad_loss must be [S]")
+        S = grad_loss.size(0)
+        _sequences(seq_start, S, (grad_loss, (S,), "grad_loss", _F32T),
+                   (counts, (S, E), "counts", _I32T), (tokens, (S,), "tokens", _I32T))
+    elif counts is not None or tokens is not None or seq_start is not None:
+        raise ValueError("counts, tokens and seq_start go with grad_loss")
+    args = (_ptr(logits), _lead_stride(logits), dtype, _ptr(topk_ids), T, E, K,
+            _choice(SCORES, score, "score"), int(bool(renormalize)), float(scale),
+            _ptr(grad_weights), _ptr(seq_start), S, _ptr(counts), _ptr(tokens), _ptr(grad_loss),
+            _ptr(grad_logits), _lead_stride(grad_logits), _dtype_code(grad_logits))
+    return PreparedCall("moe_ep_route_backward", args,
+                        (logits, topk_ids, grad_logits, grad_weights, grad_loss, counts, tokens,
+                         seq_start))
+
+
+def moe_ep_route_backward(logits, topk_ids, grad_logits, score="softmax", renormalize=True,
+                          scale=1.0, grad_weights=None, grad_loss=None, counts=None, tokens=None,
+                          seq_start=None, stream=None) -> None:
+    prepare_route_backward(logits, topk_ids, grad_logits, score, renormalize, scale, grad_weights,
+                           grad_loss, counts, tokens, seq_start)(stream)

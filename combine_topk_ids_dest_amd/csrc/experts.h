@@ -60,4 +60,63 @@ struct MatmulArgs {
 
 hipError_t launch_matmul(const MatmulArgs& a, hipStream_t stream);
 
+// The same with 4-bit weights: m.w holds E2M1 codes (m.w_stride, m.w_row bytes),
+// s one scale per `group` columns (E4M3 for 16, E8M0 for 32). m.row_bytes is
+// that of x.
+struct W4Args {
+    MatmulArgs m;
+    const uint8_t* s;
+    int64_t s_stride, s_row;     // bytes
+    int group;
+    const float* whole;          // nullable: [groups][1, or gate and up]
+};
+
+hipError_t launch_matmul_w4(const W4Args& a, hipStream_t stream);
+
+// A router's training terms over S sequences of tokens (start: nullable, one
+// sequence of all).
+struct BalanceArgs {
+    const uint8_t* logits;
+    int64_t logits_stride;       // bytes between rows
+    bool bf16;
+    const int32_t* ids;
+    int64_t T;
+    int E, K, score;
+    const int32_t* start;
+    int S;
+    int64_t tile;                // tokens of a block
+    int32_t* counts;
+    float* mean;
+    int32_t* tokens;
+    float* loss;
+    int32_t* slot_count;         // [slots][E]; nullptr: a block per sequence, no slots
+    float* slot_score;           // [slots][E]
+    int32_t* slot_tokens;        // [slots]
+};
+
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t stream);
+
+struct RouteGradArgs {
+    const uint8_t* logits;
+    int64_t logits_stride;
+    bool bf16;
+    const int32_t* ids;
+    int64_t T;
+    int E, K, score;
+    bool renormalize;
+    float scale;
+    const float* grad_weights;   // nullable
+    const float* grad_loss;      // nullable, with the four below
+    const int32_t* start;
+    int S;
+    const int32_t* counts;
+    const int32_t* tokens;
+    uint8_t* grad;
+    int64_t grad_stride;
+    bool grad_bf16;
+    int64_t tile;
+};
+
+hipError_t launch_route_backward(const RouteGradArgs& a, hipStream_t stream);
+
 }  // namespace moe_ep

@@ -642,6 +642,114 @@ MOE_EP_API int moe_ep_matmul(const void* x, int64_t x_stride, const void* w, int
                              const void* residual, int64_t residual_stride, void* out,
                              int64_t out_stride, int32_t out_dtype, void* stream);
 
+/*
+ * The same products with 4-bit weights: moe_ep_matmul over all tokens of a rank
+ * and moe_ep_expert_matmul over the batched rows, on OCP E2M1 codes (the ones
+ * that moe_ep_dispatch_pack_fp4 makes of rows) with a scale per group of columns:
+ *   out = act(f * sum_h x[h] * code(w[n, h]) * s[n, h / group] + bias) + residual
+ * A code times its scale is exact in bf16; products and sums are fp32, f goes
+ * to the sum, the result is rounded once.
+ *
+ *   w             codes, two a byte, the even column in the low nibble: rows of
+ *                 H / 2 bytes; w_stride bytes between experts, or, over all
+ *                 tokens, between rows.
+ *   group         16: w_scale holds E4M3 codes; 32: E8M0 codes, 2^(code - 127)
+ *                 (255: NaN; a weight past bf16's range is infinite).
+ *   w_scale       one byte per group of columns. By expert rows of
+ *                 Sp = H / group rounded up to 16 bytes, w_scale_stride bytes
+ *                 between experts (>= Nw * Sp); over all tokens w_scale_stride
+ *                 bytes between rows (>= H / group). Bytes behind a row's last
+ *                 scale have no effect.
+ *   w_global      f: fp32, one for an expert's matrix, or for
+ *                 MOE_EP_ACT_SILU_GATED two, of its gate and its up rows
+ *                 ([e_local] or [e_local, 2], dense); NULL: 1.
+ * H % 32 == 0; pointers (w_global: 4 bytes) and strides of w and w_scale are
+ * multiples of 16 bytes (EALIGN). w_stride and w_scale_stride of rows are below
+ * 2^30 and Nw times either below 2^31. EINVAL for another group. Everything else
+ * as for the products above.
+ */
+MOE_EP_API int moe_ep_expert_matmul_w4(const void* x, int64_t x_stride, const void* w,
+                                       int64_t w_stride, const void* w_scale,
+                                       int64_t w_scale_stride, int32_t group,
+                                       const float* w_global, const float* bias,
+                                       int64_t bias_stride, const int32_t* expert_num_tokens,
+                                       int32_t e_local, int64_t rows, int64_t H, int64_t N,
+                                       int32_t act, void* out, int64_t out_stride,
+                                       int32_t out_dtype, void* stream);
+
+MOE_EP_API int moe_ep_matmul_w4(const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                                const void* w_scale, int64_t w_scale_stride, int32_t group,
+                                const float* w_global, const float* bias, int64_t T, int64_t H,
+                                int64_t N, int32_t act, const void* residual,
+                                int64_t residual_stride, void* out, int64_t out_stride,
+                                int32_t out_dtype, void* stream);
+
+/*
+ * How evenly a router's picks fall, and the loss that asks for it. The T tokens
+ * hold S sequences, sequence s the tokens [seq_start[s], seq_start[s + 1]); a
+ * token counts if one of its picks is in [0, E) (others are no picks, so a
+ * padding token does not count). For each sequence
+ *   counts[s, e]      picks of expert e.
+ *   tokens[s]         tokens that count.
+ *   mean_score[s, e]  sum over those of q[t, e], divided by tokens[s]; q is the
+ *                     softmax of the logits, or sigmoid(x[e]) over the sum of all
+ *                     experts' (MOE_EP_SIGMOID).
+ *   loss[s]           E * sum_e counts[s, e] / (sum_e counts[s, e]) *
+ *                     mean_score[s, e]: 1 where picks or scores are even.
+ * A sequence without a token that counts has zeros. An expert whose logit is
+ * -inf or NaN has q = 0, +inf counts as the largest fp32 value. Exponentials and
+ * a token's sums are fp32; equal calls give equal bits.
+ *
+ *   logits        as for moe_ep_route_topk.   topk_ids  int32 [T, K].
+ *   seq_start     int32 [S + 1] on the device, ascending, values outside [0, T]
+ *                 are clamped; tokens before the first and behind the last
+ *                 sequence take no part. NULL (S = 1): all T tokens.
+ *   counts        int32 [S, E], tokens int32 [S], mean_score fp32 [S, E] and
+ *                 loss fp32 [S] out, dense, all written.
+ *   workspace     moe_ep_balance_workspace_bytes(T, E, S) bytes (0 for few
+ *                 tokens), 16-B aligned, in use until the call's work is done.
+ * Over several ranks' tokens: the counts may be summed over ranks before the
+ * backward pass, which then takes each rank's own tokens and the common counts.
+ * Limits: E <= 1024, K <= 64, T * K < 2^31, S * E < 2^30.
+ */
+MOE_EP_API int moe_ep_balance_workspace_bytes(int64_t T, int32_t E, int32_t S, size_t* bytes);
+
+MOE_EP_API int moe_ep_balance_loss(const void* logits, int64_t logits_stride, int32_t dtype,
+                                   const int32_t* topk_ids, int64_t T, int32_t E, int32_t K,
+                                   int32_t score, const int32_t* seq_start, int32_t S,
+                                   int32_t* counts, int32_t* tokens, float* mean_score,
+                                   float* loss, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * The router's backward pass: the gradient of the logits behind
+ * moe_ep_route_topk and moe_ep_balance_loss.
+ *   grad_logits[t, e] = sum_k grad_weights[t, k] * d topk_weights[t, k] / d x[t, e]
+ *                     + sum_s grad_loss[s] * d loss[s] / d x[t, e]
+ * The picks and the counts are constants (so is a selection bias, which only
+ * chooses). The picks' part is computed in fp64, the rest in fp32, rounded once.
+ * Every row is written; a token without a pick, and an expert whose logit is
+ * -inf or NaN, get +0.0; picks outside [0, E) have no part, whatever their
+ * gradient holds. An expert that a token picks twice counts twice.
+ *
+ *   logits, topk_ids, score, renormalize, scale   those of the forward calls.
+ *   grad_weights  fp32 [T, K], nullable.
+ *   grad_loss     fp32 [S], nullable (not both NULL); with it seq_start, S,
+ *                 counts [S, E] and tokens [S] of moe_ep_balance_loss. Without
+ *                 it these are not read.
+ *   grad_logits   [T, E] of grad_dtype (MOE_EP_BF16 or MOE_EP_F32), grad_stride
+ *                 elements between tokens (>= E). May be logits itself (same
+ *                 type and stride).
+ * Limits as for moe_ep_balance_loss.
+ */
+MOE_EP_API int moe_ep_route_backward(const void* logits, int64_t logits_stride, int32_t dtype,
+                                     const int32_t* topk_ids, int64_t T, int32_t E, int32_t K,
+                                     int32_t score, int32_t renormalize, float scale,
+                                     const float* grad_weights, const int32_t* seq_start,
+                                     int32_t S, const int32_t* counts, const int32_t* tokens,
+                                     const float* grad_loss, void* grad_logits,
+                                     int64_t grad_stride, int32_t grad_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
