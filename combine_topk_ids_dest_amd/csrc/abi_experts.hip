@@ -130,7 +130,10 @@ int check_balance(int64_t T, int32_t E, int32_t S, int64_t* slots, size_t* bytes
         return MOE_EP_EINVAL;
     const int64_t tile = balance_tile(T);
     *slots = tile ? (T + tile - 1) / tile + S : 0;
-    *bytes = ((size_t)*slots * ((size_t)E * 8 + 4) + 15) / 16 * 16;
+    // the sums, per sequence the parts of its loss (16 bytes per 64 experts) and a ticket
+    *bytes = tile ? ((size_t)S * (((size_t)E + 63) / 64 * 16 + 4) +
+                     (size_t)*slots * ((size_t)E * 8 + 4) + 15) / 16 * 16
+                  : 0;
     return MOE_EP_OK;
 }
 
@@ -412,9 +415,11 @@ int moe_ep_balance_loss(const void* logits, int64_t logits_stride, int32_t dtype
     a.loss = loss;
     if (need) {
         a.tile = balance_tile(T);
-        a.slot_count = static_cast<int32_t*>(workspace);
+        a.part = static_cast<double*>(workspace);
+        a.slot_count = reinterpret_cast<int32_t*>(a.part + (int64_t)S * ((E + 63) / 64) * 2);
         a.slot_score = reinterpret_cast<float*>(a.slot_count + slots * E);
         a.slot_tokens = reinterpret_cast<int32_t*>(a.slot_score + slots * E);
+        a.ticket = a.slot_tokens + slots;
     }
     return hip_status(launch_balance(a, static_cast<hipStream_t>(stream)));
 }
@@ -469,9 +474,8 @@ int moe_ep_route_backward(const void* logits, int64_t logits_stride, int32_t dty
     a.grad = static_cast<uint8_t*>(grad_logits);
     a.grad_stride = grad_stride * gb;
     a.grad_bf16 = grad_dtype == MOE_EP_BF16;
-    // blocks of four waves: a token each where there are few, up to 16 each
-    const int64_t per = (T + 2047) / 2048;
-    a.tile = per <= 4 ? 4 : per >= 64 ? 64 : (per + 3) / 4 * 4;
+    // blocks of four waves of up to eight tokens at once
+    a.tile = 32;
     return hip_status(launch_route_backward(a, static_cast<hipStream_t>(stream)));
 }
 

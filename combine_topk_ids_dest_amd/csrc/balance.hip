@@ -21,6 +21,13 @@ namespace {
 constexpr int kTokenWaves = 16;                  // of a block of the sums
 constexpr int kTokenThreads = kTokenWaves * 64;
 constexpr int kGradWaves = 4;
+constexpr float kLargest = 3.402823466e38f;
+const float kNothing = -__builtin_huge_valf();
+
+// Tokens that a wave has at once, so that their loads and their sums over lanes
+// (chains of dependent steps) run side by side.
+template <int V>
+constexpr int kAtOnce = V >= 16 ? 2 : V >= 8 ? 4 : 8;
 
 // v of the lane that CTRL names (`none` where there is none, or in the rows
 // that ROWS leaves out).
@@ -62,14 +69,20 @@ __device__ __forceinline__ double wave_sum(double v) {
     return v;
 }
 
+// A logit as the scores take it: -inf for one that belongs to no expert (-inf
+// or NaN), the largest fp32 for +inf.
 __device__ __forceinline__ float load_logit(const uint8_t* row, bool bf16, int e) {
-    return bf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16)
-                : reinterpret_cast<const float*>(row)[e];
+    const float x =
+        bf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16)
+             : reinterpret_cast<const float*>(row)[e];
+    return x > kNothing ? fminf(x, kLargest) : kNothing;
 }
 
-// A logit of -inf or NaN belongs to no expert; +inf counts as the largest fp32.
-__device__ __forceinline__ bool is_live(float x) { return x > -__builtin_huge_valf(); }
-__device__ __forceinline__ float finite(float x) { return x < 3.402823466e38f ? x : 3.402823466e38f; }
+// The hardware's 2^x, within a place. v's rounding times log2 e, half a place
+// of a product, is that of the difference in front of it once more.
+__device__ __forceinline__ float exp_fast(float v) {
+    return __builtin_amdgcn_exp2f(v * 1.44269504f);
+}
 
 // Where sequence s of T tokens begins and ends.
 struct Span {
@@ -98,41 +111,36 @@ __device__ __forceinline__ int first_behind(const int32_t* start, int S, int64_t
     return lo;
 }
 
-// A token's scores q, and for sigmoid scores rest = 1 - sigmoid(x). x: the
-// lane's logits (-inf or NaN: 0). Sigmoid scores are taken times e^-m with
-// m = min(0, the largest logit), so that a token of far negative logits has
-// scores too.
+// A token's scores before their sum divides them, and 1 / sum (0 without a
+// score). For sigmoid scores also rest = 1 - sigmoid(x), and they are taken
+// times e^-m, m = min(0, the largest logit), so that a token of far negative
+// logits has scores too. top: the largest logit.
 template <int V, bool SIGMOID>
-__device__ __forceinline__ void scores(const float (&x)[V], float (&q)[V], float (&rest)[V],
-                                       float& top, float& inv) {
-    float m = -__builtin_huge_valf();
+__device__ __forceinline__ float scores(const float (&x)[V], float (&q)[V], float (&rest)[V],
+                                        float& top) {
+    float m = x[0];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (is_live(x[i])) m = fmaxf(m, finite(x[i]));
-    m = wave_max(m);
+    for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
+    m = fmaxf(wave_max(m), -kLargest);
+    top = m;
     if (SIGMOID) m = fminf(m, 0.f);
-    const float em = SIGMOID ? expf(m) : 0.f;
+    const float em = SIGMOID ? exp_fast(m) : 0.f;
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float v = finite(x[i]);
         if (SIGMOID) {
-            const float z = expf(v > 0.f ? -v : v - m);
-            const float d = 1.f + (v > 0.f ? z : z * em);
-            q[i] = (v > 0.f ? 1.f : z) / d;
-            rest[i] = (v > 0.f ? z : 1.f) / d;
+            const bool up = x[i] > 0.f;
+            const float z = exp_fast(up ? -x[i] : x[i] - m);
+            const float d = __builtin_amdgcn_rcpf(1.f + (up ? z : z * em));
+            q[i] = (up ? 1.f : z) * d;
+            rest[i] = (up ? z : 1.f) * d;
         } else {
-            q[i] = expf(v - m);
-            rest[i] = 1.f;
+            q[i] = exp_fast(x[i] - m);
         }
-        if (!is_live(x[i])) q[i] = 0.f;
         sum += q[i];
     }
     sum = wave_sum(sum);
-    top = m;
-    inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) q[i] *= inv;
+    return sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
 }
 
 // Sums over a block of a per-thread value pair.
@@ -184,6 +192,8 @@ __global__ __launch_bounds__(kTokenThreads) void balance_kernel(const BalanceArg
     __shared__ double sums[2 * kTokenWaves];
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
+    if (TILES && blockIdx.x == 0)
+        for (int s = threadIdx.x; s < a.S; s += kTokenThreads) a.ticket[s] = 0;
     const int64_t t0 = TILES ? (int64_t)blockIdx.x * a.tile : 0;
     const int64_t t1 = TILES ? (t0 + a.tile < a.T ? t0 + a.tile : a.T) : a.T;
     for (int s = TILES ? first_behind(a.start, a.S, a.T, t0) : (int)blockIdx.x;;
@@ -197,22 +207,33 @@ __global__ __launch_bounds__(kTokenThreads) void balance_kernel(const BalanceArg
         __syncthreads();
         float acc[V] = {};
         int32_t tokens = 0;
-        for (int64_t t = lo + wave; t < hi; t += kTokenWaves) {
-            const int32_t id = lane < a.K ? a.ids[t * a.K + lane] : -1;
-            const uint8_t* row = a.logits + t * a.logits_stride;
-            float x[V], q[V], rest[V], top, inv;
+        constexpr int B = kAtOnce<V> / 2;
+        for (int64_t t = lo + wave; t < hi; t += kTokenWaves * B) {
+            float x[B][V];
+            int32_t id[B];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane + 64 * i;
-                x[i] = e < a.E ? load_logit(row, a.bf16, e) : -__builtin_huge_valf();
+            for (int b = 0; b < B; ++b) {        // behind the last token: that one again
+                const int64_t u = t + b * kTokenWaves < hi ? t + b * kTokenWaves : hi - 1;
+                id[b] = lane < a.K ? a.ids[u * a.K + lane] : -1;
+                const uint8_t* row = a.logits + u * a.logits_stride;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const int e = lane + 64 * i;
+                    x[b][i] = load_logit(row, a.bf16, e < a.E ? e : 0);
+                    if (e >= a.E) x[b][i] = kNothing;
+                }
             }
-            const bool pick = id >= 0 && id < a.E;
-            if (!__ballot(pick)) continue;       // a padding token
-            ++tokens;
-            if (pick) atomicAdd(&hist[id], 1);
-            scores<V, SIGMOID>(x, q, rest, top, inv);
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] += q[i];
+            for (int b = 0; b < B; ++b) {
+                const bool pick = id[b] >= 0 && id[b] < a.E && t + b * kTokenWaves < hi;
+                const bool count = __ballot(pick) != 0;       // no padding token
+                tokens += count;
+                if (pick) atomicAdd(&hist[id[b]], 1);
+                float q[V], rest[V], top;
+                const float inv = scores<V, SIGMOID>(x[b], q, rest, top);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] += q[i] * (count ? inv : 0.f);
+            }
         }
         // the upper half of the waves first, then both (LDS holds half of them)
         if (lane == 0) counted[wave] = tokens;
@@ -247,25 +268,85 @@ __global__ __launch_bounds__(kTokenThreads) void balance_kernel(const BalanceArg
     }
 }
 
-// One block per sequence: its tiles' sums, in tile order.
+// The sums of a sequence's tiles, a block for 64 experts: its waves share out
+// the tiles, each in their order, and are added in theirs. The block that comes
+// last adds up the blocks' parts of the loss, in the experts' order. (One block
+// for all experts took 40 us for 256 tiles of 256 experts: 512 KB through one
+// CU.)
 __global__ __launch_bounds__(kTokenThreads) void balance_join_kernel(const BalanceArgs a) {
-    __shared__ double sums[2 * kTokenWaves];
-    const int s = blockIdx.x;
+    __shared__ double scores_of[kTokenWaves][64];
+    __shared__ int32_t counts_of[kTokenWaves][64];
+    constexpr int U = 16;                        // loads on their way
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    const int s = blockIdx.y, slices = gridDim.x;
+    const int e = blockIdx.x * 64 + lane;
+    const int col = e < a.E ? e : a.E - 1;
     const Span span = span_of(a.start, a.T, s);
-    int64_t count = 0, tokens = 0;
+    const bool any = span.hi > span.lo;
+    const int64_t first = span.lo / a.tile + s;  // slots [first, end)
+    const int64_t end = any ? (span.hi - 1) / a.tile + 1 + s : first;
+    int32_t count = 0;
     double score = 0.0;
-    if (span.hi > span.lo) {
-        const int64_t first = span.lo / a.tile, last = (span.hi - 1) / a.tile;
-        for (int64_t b = first; b <= last; ++b) {
-            const int64_t slot = b + s;
-            tokens += a.slot_tokens[slot];
-            if ((int)threadIdx.x < a.E) {
-                count += a.slot_count[slot * a.E + threadIdx.x];
-                score += (double)a.slot_score[slot * a.E + threadIdx.x];
-            }
+    for (int64_t b = first + wave; b < end; b += kTokenWaves * U) {
+        int32_t c[U];
+        float v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t slot = b + i * kTokenWaves < end ? b + i * kTokenWaves : end - 1;
+            c[i] = a.slot_count[slot * a.E + col];
+            v[i] = a.slot_score[slot * a.E + col];
         }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (b + i * kTokenWaves < end) {
+                count += c[i];
+                score += (double)v[i];
+            }
     }
-    finish_sequence(a, s, count, score, tokens, sums);
+    scores_of[wave][lane] = score;
+    counts_of[wave][lane] = count;
+    __syncthreads();
+    if (wave != 0) return;
+    double n = 0.0;
+    for (int64_t b = first + lane; b < end; b += 64) n += (double)a.slot_tokens[b];
+    n = wave_sum(n);
+    for (int w = 1; w < kTokenWaves; ++w) {
+        score += scores_of[w][lane];
+        count += counts_of[w][lane];
+    }
+    const double mean = n > 0.0 ? score / n : 0.0;
+    if (e < a.E) {
+        a.counts[(int64_t)s * a.E + e] = count;
+        a.mean[(int64_t)s * a.E + e] = (float)mean;
+    }
+    double picks = wave_sum(e < a.E ? (double)count : 0.0);
+    double both = wave_sum(e < a.E ? (double)count * mean : 0.0);
+    if (slices > 1) {
+        double* const parts = a.part + (int64_t)s * slices * 2;
+        int before = 0;
+        if (lane == 0) {
+            __hip_atomic_store(parts + 2 * blockIdx.x, picks, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(parts + 2 * blockIdx.x + 1, both, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+            before = __hip_atomic_fetch_add(a.ticket + s, 1, __ATOMIC_ACQ_REL,
+                                            __HIP_MEMORY_SCOPE_AGENT);
+        }
+        if (__builtin_amdgcn_readfirstlane(before) != slices - 1) return;
+        picks = both = 0.0;
+        if (lane == 0)
+            for (int i = 0; i < slices; ++i) {
+                picks += __hip_atomic_load(parts + 2 * i, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+                both += __hip_atomic_load(parts + 2 * i + 1, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT);
+            }
+    }
+    if (lane == 0) {
+        a.tokens[s] = (int32_t)n;
+        a.loss[s] = (float)(picks > 0.0 ? (double)a.E * both / picks : 0.0);
+    }
 }
 
 // The gradient of the logits. Through the picks' weights w = scale * p[pick]
@@ -274,111 +355,155 @@ __global__ __launch_bounds__(kTokenThreads) void balance_join_kernel(const Balan
 //   softmax                  dx[e]    += sum over picks of e of w g - p[e] sum w g
 //   sigmoid                  the first form (plain: w g) times 1 - sigmoid(x[pick])
 // The picks' part, one exponential a token, is fp64: g - sum g w cancels.
-template <int V, bool SIGMOID>
+//
+// A wave has B tokens at once, and 64 / B lanes have the picks of each (KP), so
+// that the fp64 part is done for all of them in one go.
+template <int V, bool SIGMOID, int KP>
 __global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const RouteGradArgs a) {
+    constexpr int B = 64 / KP < kAtOnce<V> ? 64 / KP : kAtOnce<V>;
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
+    const int of = lane / KP, pk = lane % KP;    // the lane's token and pick
     float each[V] = {};                          // a[e] of the sequence at hand
     int s = -1, at_s = -1;
     Span span = {0, 0};                          // of sequence s
     const int64_t t0 = (int64_t)blockIdx.x * a.tile;
     const int64_t t1 = t0 + a.tile < a.T ? t0 + a.tile : a.T;
-    for (int64_t t = t0 + wave; t < t1; t += kGradWaves) {
-        const int32_t id = lane < a.K ? a.ids[t * a.K + lane] : -1;
-        const uint8_t* row = a.logits + t * a.logits_stride;
-        float x[V], q[V], rest[V], top, inv;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 64 * i;
-            x[i] = e < a.E ? load_logit(row, a.bf16, e) : -__builtin_huge_valf();
-        }
+    for (int64_t t = t0 + wave * B; t < t1; t += kGradWaves * B) {
+        // all loads first; behind the last token that one again
+        const bool mine = of < B && pk < a.K && t + of < t1;
+        const int64_t tp = mine ? t + of : t;
+        const int32_t id = mine ? a.ids[tp * a.K + pk] : -1;
         const bool pick = id >= 0 && id < a.E;
-        const bool counted = __ballot(pick) != 0;
-        float xp = -__builtin_huge_valf();
-        if (pick) xp = load_logit(row, a.bf16, id);
         float g = 0.f;
-        if (pick && a.grad_weights) g = a.grad_weights[t * a.K + lane];
-        scores<V, SIGMOID>(x, q, rest, top, inv);
-
-        float dx[V] = {};
-        float through = 0.f;                     // sum_j q[j] (what reaches q[j])
-        bool aux = false;
-        if (a.grad_loss && counted) {
-            if (s < 0 || span.hi <= t) {
-                if (s < a.S) s = s < 0 ? first_behind(a.start, a.S, a.T, t) : s + 1;
-                for (; s < a.S && (span = span_of(a.start, a.T, s)).hi <= t; ++s) {}
+        if (pick && a.grad_weights) g = a.grad_weights[tp * a.K + pk];
+        float q[B][V], rest[B][SIGMOID ? V : 1], xs[B][V];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const uint8_t* row = a.logits + (t + b < t1 ? t + b : t1 - 1) * a.logits_stride;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane + 64 * i;
+                xs[b][i] = load_logit(row, a.bf16, e < a.E ? e : 0);
+                if (e >= a.E) xs[b][i] = kNothing;
             }
-            aux = s < a.S && span.lo <= t;
         }
-        if (aux) {
-            if (at_s != s) {
+        float xp = kNothing;
+        if (pick) xp = load_logit(a.logits + tp * a.logits_stride, a.bf16, id);
+        const uint64_t picks = __ballot(pick);
+
+        float my_top = 0.f, my_inv = 0.f;        // of the lane's token
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            float top, left[V];
+            const float inv = scores<V, SIGMOID>(xs[b], q[b], left, top);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                q[b][i] *= inv;
+                if (SIGMOID) rest[b][i] = left[i];
+            }
+            if (of == b) {
+                my_top = top;
+                my_inv = inv;
+            }
+        }
+
+        float back = 0.f, backs = 0.f;           // what reaches the logit of the lane's pick
+        if (a.grad_weights) {
+            auto group_sum = [](double v) {
+#pragma unroll
+                for (int off = 1; off < KP; off <<= 1) v += __shfl_xor(v, off, 64);
+                return v;
+            };
+            const bool live = pick && xp > kNothing;
+            const double v = live ? (double)xp : 0.0;
+            double w, left = 1.0;
+            if (SIGMOID) {
+                const double z = exp(-fabs(v));
+                w = (v >= 0.0 ? 1.0 : z) / (1.0 + z);
+                left = (v >= 0.0 ? z : 1.0) / (1.0 + z);
+            } else {
+                w = exp(v - (double)my_top);     // times 1 / sum, left out of a ratio
+            }
+            if (!live) w = 0.0;
+            double gw = live ? (double)g : 0.0;
+            if (a.renormalize) {
+                const double all = group_sum(w);
+                w = all > 0.0 ? w / all : 0.0;
+                gw -= group_sum(gw * w);
+            } else if (!SIGMOID) {
+                w *= (double)my_inv;
+            }
+            back = live ? (float)((double)a.scale * w * gw * left) : 0.f;
+            if (!SIGMOID && !a.renormalize) backs = (float)group_sum((double)back);
+        }
+
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (t + b >= t1) break;
+            constexpr uint64_t kGroup = KP == 64 ? ~0ull : (1ull << (KP & 63)) - 1;
+            uint64_t mask = picks >> (b * KP & 63) & kGroup;
+            bool aux = false;
+            if (a.grad_loss && mask) {
+                if (s < 0 || span.hi <= t + b) {
+                    if (s < a.S) s = s < 0 ? first_behind(a.start, a.S, a.T, t + b) : s + 1;
+                    for (; s < a.S && (span = span_of(a.start, a.T, s)).hi <= t + b; ++s) {}
+                }
+                aux = s < a.S && span.lo <= t + b;
+            }
+            if (aux && at_s != s) {
                 const int32_t* c = a.counts + (int64_t)s * a.E;
-                float n[V], picks = 0.f;
-                int64_t all = 0;
+                float n[V];
+                double all = 0.0;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int e = lane + 64 * i;
                     const int32_t v = e < a.E ? c[e] : 0;
                     n[i] = (float)v;
-                    all += v;
+                    all += (double)v;
                 }
-                picks = (float)wave_sum((double)all);
+                all = wave_sum(all);
                 const int32_t tokens = a.tokens[s];
-                const float f = picks > 0.f && tokens > 0
-                                    ? a.grad_loss[s] * (float)a.E / picks / (float)tokens
+                const float f = all > 0.0 && tokens > 0
+                                    ? a.grad_loss[s] * (float)a.E / (float)all / (float)tokens
                                     : 0.f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) each[i] = f * n[i];
                 at_s = s;
             }
+            float through = 0.f;                 // sum_j q[j] (what reaches q[j])
+            if (aux) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) through += q[i] * each[i];
-            through = wave_sum(through);
-        }
-        float back = 0.f;                        // lane k: what reaches the logit of pick k
-        if (a.grad_weights && counted) {
-            const bool live = pick && is_live(xp);
-            const double v = (double)finite(xp);
-            double w = 0.0, left = 1.0;
-            if (SIGMOID) {
-                const double z = live ? exp(-fabs(v)) : 0.0;
-                w = live ? (v >= 0.0 ? 1.0 : z) / (1.0 + z) : 0.0;
-                left = (v >= 0.0 ? z : 1.0) / (1.0 + z);
-            } else if (live) {
-                w = exp(v - (double)top);        // times 1 / sum, left out of a ratio
+                for (int i = 0; i < V; ++i) through += q[b][i] * each[i];
+                through = wave_sum(through);
             }
-            double gw = (double)g;
-            if (a.renormalize) {
-                const double all = wave_sum(w);
-                w = all > 0.0 ? w / all : 0.0;
-                gw -= wave_sum(live ? gw * w : 0.0);
-            } else if (!SIGMOID) {
-                w *= (double)inv;
+            if (!SIGMOID) through += lane_value(backs, b * KP & 63);
+            float dx[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                dx[i] = q[b][i] * ((aux ? each[i] : 0.f) - through);
+                if (SIGMOID) dx[i] *= rest[b][i];
+                if (q[b][i] == 0.f) dx[i] = 0.f; // also where `through` is no number
             }
-            back = live ? (float)((double)a.scale * w * gw * left) : 0.f;
-            if (!SIGMOID && !a.renormalize) through += wave_sum(back);
-        }
+            if (a.grad_weights)
+                for (; mask; mask &= mask - 1) {
+                    const int from = b * KP + __builtin_ctzll(mask);
+                    const int e = __builtin_amdgcn_readlane(id, from);
+                    const float v = (e & 63) == lane ? lane_value(back, from) : 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            dx[i] = q[i] != 0.f ? q[i] * ((aux ? each[i] : 0.f) - through) * rest[i] : 0.f;
-        if (a.grad_weights && counted)
-            for (int k = 0; k < a.K; ++k) {
-                const int e = __builtin_amdgcn_readlane(pick ? id : -1, k);
-                if (e < 0) continue;
-                const float v = lane_value(back, k);
+                    for (int i = 0; i < V; ++i)
+                        if (e >> 6 == i) dx[i] += v;
+                }
+            uint8_t* out = a.grad + (t + b) * a.grad_stride;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (e >> 6 == i && (e & 63) == lane) dx[i] += v;
+            for (int i = 0; i < V; ++i) {
+                const int e = lane + 64 * i;
+                if (e >= a.E) continue;
+                if (a.grad_bf16)
+                    reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)to_bf16_rne(dx[i]);
+                else
+                    reinterpret_cast<float*>(out)[e] = dx[i];
             }
-        uint8_t* out = a.grad + t * a.grad_stride;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 64 * i;
-            if (e >= a.E) continue;
-            if (a.grad_bf16)
-                reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)to_bf16_rne(dx[i]);
-            else
-                reinterpret_cast<float*>(out)[e] = dx[i];
         }
     }
 }
@@ -412,7 +537,8 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
         else run(std::false_type{});
     });
     if (rc != hipSuccess || !tiles) return rc;
-    balance_join_kernel<<<(unsigned)a.S, kTokenThreads, 0, st>>>(a);
+    balance_join_kernel<<<dim3((unsigned)((a.E + 63) / 64), (unsigned)a.S), kTokenThreads, 0,
+                          st>>>(a);
     return hipGetLastError();
 }
 
@@ -420,10 +546,17 @@ hipError_t launch_route_backward(const RouteGradArgs& a, hipStream_t st) {
     const unsigned grid = (unsigned)((a.T + a.tile - 1) / a.tile);
     return by_width(a.E, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        if (a.score == MOE_EP_SIGMOID)
-            route_backward_kernel<V, true><<<grid, kGradWaves * 64, 0, st>>>(a);
-        else
-            route_backward_kernel<V, false><<<grid, kGradWaves * 64, 0, st>>>(a);
+        auto run = [&](auto sigmoid, auto kp) {
+            route_backward_kernel<V, decltype(sigmoid)::value, decltype(kp)::value>
+                <<<grid, kGradWaves * 64, 0, st>>>(a);
+        };
+        auto by_picks = [&](auto sigmoid) {
+            if (a.K <= 8) run(sigmoid, std::integral_constant<int, 8>{});
+            else if (a.K <= 16) run(sigmoid, std::integral_constant<int, 16>{});
+            else run(sigmoid, std::integral_constant<int, 64>{});
+        };
+        if (a.score == MOE_EP_SIGMOID) by_picks(std::true_type{});
+        else by_picks(std::false_type{});
     });
 }
 

@@ -92,6 +92,8 @@ struct BalanceArgs {
     int32_t* slot_count;         // [slots][E]; nullptr: a block per sequence, no slots
     float* slot_score;           // [slots][E]
     int32_t* slot_tokens;        // [slots]
+    double* part;                // [S][ceil(E / 64)][2]: picks, picks times mean scores
+    int32_t* ticket;             // [S], cleared by the call itself
 };
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t stream);
