@@ -69,67 +69,288 @@ __device__ __forceinline__ void finish_value(const W4Args& a, int g, int64_t row
 }
 
 // ---------------------------------------------------------------------
-// Tiles of 16 rows of x by 16 of w (gated: 8 gate rows and their 8 up rows).
-// Four waves share out k in runs of 128 columns, a lane has 32 of them of a row
-// of each operand.
+// Tiles of a few rows: up to 16 of x by 16 WN of w (gated: half gate rows, half
+// up rows). Bound by the weights' bytes, so what counts is loads in flight. A
+// wave has 16 rows of w and every WK-th block of 256 columns (WN WK = 8 waves:
+// few rows of w leave CUs idle, so there the waves share out k and their sums
+// are added through LDS, in wave order). Codes and scales go straight from
+// memory into LDS of the wave's own, four steps of 256 columns always on their
+// way, with no barrier between them; behind the last step of a tile come the
+// first of the block's next tile.
+//
+// x is read by all waves: segments of 32 KB (2 to 16 rows of 8192 to 1024
+// columns), the next one on its way while one is in use, a barrier between them.
+//
+// LDS: a wave's 128-byte row of codes holds chunk c at c ^ (r / 2 & 7), a
+// 512-byte row of x chunk c at c ^ place_few(r): a lane takes chunks q and q + 4
+// of the codes (q = lane / 16), so chunks 4 q + t and 16 + 4 q + t of x, and the
+// sets of 16 lanes that a 16-byte read is served in (see the big tiles) meet on
+// no bank.
 // ---------------------------------------------------------------------
-constexpr int kPlainWaves = 4;
+constexpr int kFewCols = 256;                    // columns of a step of a wave
+constexpr int kFewStep = kSmall * kFewCols / 2 + 256;    // codes and scales of one
+constexpr int kFewRing = 4;
+constexpr int kSegment = 32 << 10;
+constexpr int kFewX = kWaves * kFewRing * kFewStep;      // segments behind the rings,
+constexpr int kFewPart = kFewX + 2 * kSegment;           // the waves' sums, twice
+constexpr int kFewPitch = kSmall + 4;
+constexpr int kFewSums = kWaves * kSmall * kFewPitch * 4;
+constexpr int kFewLds = kFewPart + 2 * kFewSums;
+
+__device__ __forceinline__ int place_few(int r) {
+    const int j = (r >> 2) & 3;                  // 0, 1, 2, 3 -> 0, 2, 3, 1
+    return (r & 3) | (j >> 1) << 2 | ((j >> 1) ^ (j & 1)) << 3;
+}
+
+// What a wave needs to load a tile.
+struct FewTile {
+    i32x4 rx, rw, rs;
+    uint32_t vw[2], vs;
+    int g, m0, left, n0;
+    int lx;                                      // x in 2^lx rows
+};
 
 template <int GROUP, bool GATED>
-__global__ __launch_bounds__(kPlainWaves * 64) void w4_kernel(const W4Args a) {
-    __shared__ float part[kPlainWaves][kSmall][kSmall + 1];
+__device__ __forceinline__ FewTile few_setup(const W4Args& a, int g, int m0, int rows, int n0,
+                                             int wn) {
     const MatmulArgs& m = a.m;
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = lane & 15, q = lane >> 4;
-    const int nt = (m.N + BO - 1) / BO;
+    const int lane = threadIdx.x & 63;
     const int H = m.row_bytes / 2;
-    const int rows0 = lane_rows(m, 0);
-    int n[kKinds];
-    count_runs(m, rows0, INT32_MAX, n);
-    const int total = n[0] * nt;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        const Place at = find_tile(m, rows0, INT32_MAX, 0, nt, t);
-        const int mt = cut_rows(at.rows, INT32_MAX).runs;
-        const int m0 = at.l % mt * kSmall, n0 = at.l / mt * BO;
-        const int col = GATED ? n0 + (r & 7) : n0 + r;
-        const int64_t row = GATED && r >= 8 ? (int64_t)m.N + col : col;
-        const uint8_t* px = m.x + at.g * m.x_stride + (int64_t)(m0 + r) * m.x_row;
-        const uint8_t* pw = m.w + at.g * m.w_stride + row * m.w_row;
-        const uint8_t* ps = a.s + at.g * a.s_stride + row * a.s_row;
-        const bool has_x = m0 + r < at.rows, has_w = col < m.N;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        for (int k0 = wave * 128; k0 < H; k0 += kPlainWaves * 128) {
-            const int k = k0 + q * 32;
-            u32x4 c = {0, 0, 0, 0}, x[4] = {};
-            float s[2] = {0.f, 0.f};
-            if (k < H && has_w) {
-                c = *reinterpret_cast<const u32x4*>(pw + k / 2);
-                s[0] = scale_of<GROUP>(ps[k / GROUP]);
-                s[1] = scale_of<GROUP>(ps[(k + 16) / GROUP]);
-            }
-            if (k < H && has_x)
+    const int nw = GATED ? 2 * m.N : m.N;
+    FewTile t;
+    t.g = g;
+    t.m0 = m0;
+    t.left = rows - m0 < kSmall ? rows - m0 : kSmall;
+    t.n0 = n0;
+    t.lx = t.left > 8 ? 4 : t.left > 4 ? 3 : t.left > 2 ? 2 : 1;
+    t.rx = row_rsrc4(m.x + g * m.x_stride + (int64_t)m0 * m.x_row,
+                     (int64_t)(t.left - 1) * m.x_row + m.row_bytes);
+    t.rw = row_rsrc4(m.w + g * m.w_stride, (int64_t)(nw - 1) * m.w_row + H / 2);
+    t.rs = row_rsrc4(a.s + g * a.s_stride,
+                     (int64_t)(nw - 1) * a.s_row + (H / GROUP + 15) / 16 * 16);
+    auto row = [&](int r, bool& in) {
+        const int n = n0 + wn * BO + (GATED ? r & 7 : r);
+        in = n < m.N;
+        return GATED && r >= 8 ? (uint32_t)(m.N + n) : (uint32_t)n;
+    };
+    bool in;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[i] = *reinterpret_cast<const u32x4*>(px + k * 2 + i * 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc = mma_bf16(widen4<GROUP>(c[i], s[i / 2]), x[i], acc);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) part[wave][r][q * 4 + i] = acc[i];
-        __syncthreads();
-        for (int i = threadIdx.x; i < kSmall * BO; i += kPlainWaves * 64) {
-            const int o = i % BO, mr = i / BO;
-            if (m0 + mr >= at.rows || n0 + o >= m.N) continue;
-            float v = 0.f, up = 0.f;
-            for (int w = 0; w < kPlainWaves; ++w) {
-                v += part[w][mr][o];
-                if (GATED) up += part[w][mr][o + 8];
-            }
-            finish_value<GATED>(a, at.g, m0 + mr, n0 + o, v, up);
-        }
-        __syncthreads();
+    for (int h = 0; h < 2; ++h) {
+        const int r = h * 8 + (lane >> 3);
+        const uint32_t at = row(r, in) * (uint32_t)m.w_row;
+        t.vw[h] = in ? at + ((lane & 7) ^ ((r >> 1) & 7)) * 16 : kOutside;
     }
+    // E4M3: 16 bytes of a row to a lane; powers of two: 4 of 8
+    const uint32_t at = row(GROUP == 16 ? lane & 15 : (lane >> 1) & 15, in) * (uint32_t)a.s_row;
+    t.vs = in ? at + (GROUP == 16 ? 0 : (lane & 1) * 4) : kOutside;
+    return t;
+}
+
+// Works through the block's tiles, number t of `total` at place(t): 16 rows each
+// by WN = 2^lw runs of 16 rows of w.
+template <int GROUP, bool GATED, class Next>
+__device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int total, int lw,
+                                          const Next& place) {
+    const MatmulArgs& m = a.m;
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int wn = wave & ((1 << lw) - 1), wk = wave >> lw, lk = 3 - lw;     // WK = 2^lk
+    const int H = m.row_bytes / 2;
+    const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
+    const uint32_t ring = lds0 + wave * kFewRing * kFewStep;
+    const uint8_t* mine = lds + wave * kFewRing * kFewStep;
+    const int r = lane & 15, q = lane >> 4;
+    const int steps = (H + (kFewCols << lk) - 1) >> (8 + lk);
+    const int nsteps = steps > kFewRing ? steps : kFewRing;
+
+    auto tile_at = [&](int t0) {
+        const int t = t0 < total ? tile_of(blockIdx.x, gridDim.x, total - t0) : -1;
+        return t < 0 ? -1 : t + t0;
+    };
+    // Step i of a tile into place j of the wave's ring.
+    auto fetch = [&](const FewTile& t, int i, int j) {
+        const int k = ((i << lk) + wk) * kFewCols;
+        const bool any = k < H;
+        const uint32_t at = ring + j * kFewStep;
+        if (lane < (GROUP == 16 ? 16 : 32)) {
+            if (GROUP == 16)
+                load_to_lds(uniform(t.rs), at + 2048, any ? t.vs : kOutside, any ? k / 16 : 0);
+            else
+                load4_to_lds(uniform(t.rs), at + 2048,
+                             k + (lane & 1) * 128 < H ? t.vs : kOutside, any ? k / 32 : 0);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int chunk = (lane & 7) ^ ((h * 4 + (lane >> 4)) & 7);
+            load_to_lds(uniform(t.rw), at + h * 1024, k + chunk * 32 < H ? t.vw[h] : kOutside,
+                        any ? k / 2 : 0);
+        }
+    };
+    // Segment n of a tile's x into buffer `to`.
+    auto fetch_x = [&](const FewTile& t, int n, int to) {
+#pragma unroll
+        for (int i = 0; i < kSegment / 1024 / kWaves; ++i) {
+            const int load = wave * (kSegment / 1024 / kWaves) + i, at = load * 64 + lane;
+            const int row = (at >> 5) & ((1 << t.lx) - 1);
+            const int k = (n << (14 - t.lx)) + (at >> (5 + t.lx)) * kFewCols +
+                          ((at & 31) ^ place_few(row)) * 8;
+            load_to_lds(uniform(t.rx), lds0 + kFewX + to * kSegment + load * 1024,
+                        row < t.left && k < H ? (uint32_t)row * (uint32_t)m.x_row + k * 2 : kOutside,
+                        0);
+        }
+    };
+    auto finish = [&](const FewTile& t, int odd) {
+        constexpr int BO = GATED ? kSmall / 2 : kSmall;
+        const float* part = reinterpret_cast<const float*>(lds + kFewPart + odd * kFewSums);
+        const int wide = BO << lw;
+        for (int i = threadIdx.x; i < wide * t.left; i += kThreads) {
+            const int o = i & (wide - 1), row = i / wide;
+            const int n = t.n0 + o;
+            if (n >= m.N) continue;
+            float v = 0.f, up = 0.f;
+            for (int w = o / BO; w < kWaves; w += 1 << lw) {
+                const float* p = part + (w * kSmall + row) * kFewPitch + o % BO;
+                v += p[0];
+                if (GATED) up += p[8];
+            }
+            finish_value<GATED>(a, t.g, t.m0 + row, n, v, up);
+        }
+    };
+
+    int t0 = 0, at = tile_at(0);
+    if (at < 0) return;
+    FewTile cur = place(at, wn);
+    fetch_x(cur, 0, 0);
+#pragma unroll
+    for (int j = 0; j < kFewRing; ++j) fetch(cur, j, j);
+    FewTile old = cur;
+    bool owed = false;                           // old's sums are still to be added up
+    int odd = 0, to = 0, j = 0;
+    int since = kFewRing;                        // steps asked for behind the next segment
+    for (;;) {
+        t0 += gridDim.x;
+        at = tile_at(t0);
+        FewTile nxt = cur;
+        if (at >= 0) nxt = place(at, wn);
+        else nxt.left = 0;                       // nothing more to load
+        const int lseg = 14 - cur.lx - 8 - lk;   // 2^lseg steps of a segment
+        const int row = r & ((1 << cur.lx) - 1);
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < nsteps; ++i) {
+            if ((i & ((1 << lseg) - 1)) == 0) {
+                // the segment at hand has arrived: behind it are `since` steps
+                // of three loads
+                if (since >= 4) wait_and_barrier<3 * 4>();
+                else if (since >= 2) wait_and_barrier<3 * 2>();
+                else wait_and_barrier<3>();
+                since = 0;
+                const int n = (i >> lseg) + 1;   // the next
+                if (n << lseg < nsteps) fetch_x(cur, n, to ^ 1);
+                else fetch_x(nxt, 0, to ^ 1);
+                if (owed) finish(old, odd ^ 1);
+                owed = false;
+                to ^= 1;
+            }
+            // the oldest step has arrived: behind it are three steps
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kFewRing - 1) * 3) : "memory");
+            const uint8_t* p = mine + j * kFewStep;
+            const int k = ((i << lk) + wk) * kFewCols;
+            u32x4 c[2];
+            uint32_t sc[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                c[h] = *reinterpret_cast<const u32x4*>(p + r * 128 +
+                                                       (((q + 4 * h) ^ (r >> 1)) & 7) * 16);
+                sc[h] = GROUP == 16
+                            ? *reinterpret_cast<const uint16_t*>(p + 2048 + r * 16 + h * 8 + q * 2)
+                            : p[2048 + r * 8 + h * 4 + q];
+            }
+            // read, so its place can be filled again
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (i + kFewRing < nsteps) fetch(cur, i + kFewRing, j);
+            else fetch(nxt, at >= 0 ? i + kFewRing - nsteps : nsteps, j);
+            ++since;
+            j = j + 1 < kFewRing ? j + 1 : 0;
+            if (k < H) {
+                const uint8_t* px = lds + kFewX + (to ^ 1) * kSegment + row * 512 +
+                                    ((((i & ((1 << lseg) - 1)) << lk) + wk) << (9 + cur.lx));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // what follows the last scale may be anything
+                    const bool in = k + h * 128 + q * 32 < H;
+                    const float s0 = in ? scale_of<GROUP>(sc[h] & 0xFF) : 0.f;
+                    const float s1 = GROUP == 32 ? s0 : in ? scale_of<GROUP>(sc[h] >> 8) : 0.f;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const u32x4 x = *reinterpret_cast<const u32x4*>(
+                            px + ((h * 16 + q * 4 + t) ^ place_few(row)) * 16);
+                        acc = mma_bf16(widen4<GROUP>(c[h][t], t < 2 ? s0 : s1), x, acc);
+                    }
+                }
+            }
+        }
+        float* part = reinterpret_cast<float*>(lds + kFewPart + odd * kFewSums);
+        *reinterpret_cast<f32x4*>(part + (wave * kSmall + r) * kFewPitch + q * 4) = acc;
+        old = cur;
+        owed = true;
+        odd ^= 1;
+        if (at < 0) break;
+        cur = nxt;
+    }
+    // nothing of this block's is on its way into LDS when the block ends
+    wait_and_barrier<0>();
+    finish(old, odd ^ 1);
+}
+
+// Runs of 16 rows of w side by side (as a power of two) for `runs` runs of up to
+// 16 rows, some of more than 8 (`wide`): the least rounds of the grid times a
+// tile's time, by its bytes and about 2048 columns' worth of start and end.
+template <bool GATED>
+__device__ __forceinline__ int few_across(int runs, int N, int H, bool wide) {
+    constexpr int BO = GATED ? kSmall / 2 : kSmall;
+    int best = 3;
+    int64_t least = INT64_MAX;
+#pragma unroll
+    for (int lw = 3; lw >= 0; --lw) {
+        if (lw == 0 && wide) break;              // a step of 2048 columns of 16 rows is no segment
+        const int64_t tiles = (int64_t)runs * ((N + (BO << lw) - 1) / (BO << lw));
+        const int64_t cost = (tiles + kGrid - 1) / kGrid * (((int64_t)H << lw) + 2048);
+        if (cost < least) {
+            least = cost;
+            best = lw;
+        }
+    }
+    return best;
+}
+
+template <int GROUP, bool GATED>
+__device__ __forceinline__ void few_rows(const W4Args& a, uint8_t* lds, int rows0, int small_to,
+                                         int runs) {
+    const MatmulArgs& m = a.m;
+    constexpr int BO = GATED ? kSmall / 2 : kSmall;
+    bool wide = false;
+    for (int g0 = 0; g0 < m.groups; g0 += 64) {
+        const int rows = g0 ? lane_rows(m, g0) : rows0;
+        wide |= __ballot(rows <= small_to && rows > 8) != 0;
+    }
+    const int lw = few_across<GATED>(runs, m.N, m.row_bytes / 2, wide);
+    const int nt = (m.N + (BO << lw) - 1) / (BO << lw);
+    few_tiles<GROUP, GATED>(a, lds, runs * nt, lw, [&](int t, int wn) {
+        const Place at = find_tile(m, rows0, small_to, 0, nt, t);
+        const int mt = cut_rows(at.rows, small_to).runs;
+        return few_setup<GROUP, GATED>(a, at.g, at.l % mt * kSmall, at.rows,
+                                       at.l / mt * (BO << lw), wn);
+    });
+}
+
+template <int GROUP, bool GATED>
+__global__ __launch_bounds__(kThreads, 2) void w4_few_kernel(const W4Args a) {
+    __shared__ __align__(1024) uint8_t lds[kFewLds];
+    const int rows0 = lane_rows(a.m, 0);
+    int n[kKinds];
+    count_runs(a.m, rows0, INT32_MAX, n);
+    if (n[0] > 0) few_rows<GROUP, GATED>(a, lds, rows0, INT32_MAX, n[0]);
 }
 
 // ---------------------------------------------------------------------
@@ -319,12 +540,18 @@ __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
     constexpr int BB = GATED ? kCols / 2 : kCols;
     const int ntb = (m.N + BB - 1) / BB;
     const int rows0 = lane_rows(m, 0);
-    int n[kKinds], total = 0;
-    count_runs(m, rows0, 0, n);
+    int n[kKinds], total = 0, small_to = m.counts ? kSmall : 0;
+    for (;;) {
+        count_runs(m, rows0, small_to, n);
+        total = 0;
 #pragma unroll
-    for (int k = 1; k < kKinds; ++k) {
-        n[k] *= ntb;
-        total += n[k];
+        for (int k = 1; k < kKinds; ++k) {
+            n[k] *= ntb;
+            total += n[k];
+        }
+        // a few rows beside so much else: in part-filled tiles
+        if (!small_to || total <= kGrid) break;
+        small_to = 0;
     }
     const int parts = last_parts(total);
     for (int t0 = 0; t0 < total; t0 += kGrid) {
@@ -338,8 +565,8 @@ __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
                 t -= n[k];
                 --kind;
             }
-        const Place at = find_tile(m, rows0, 0, kind, ntb, t);
-        const int runs = cut_rows(at.rows, 0).runs;
+        const Place at = find_tile(m, rows0, small_to, kind, ntb, t);
+        const int runs = cut_rows(at.rows, small_to).runs;
         const Piece p = piece_of(at.l, at.rows, runs, kind, ntb, turn.sub, turn.cut);
         if (p.m0 >= p.end) continue;
         const int n0 = p.col * BB;
@@ -355,12 +582,13 @@ __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
         else if (f == 2) run(std::integral_constant<int, 64>{});
         else run(std::integral_constant<int, 32>{});
     }
+    if (n[0] > 0) few_rows<GROUP, GATED>(a, lds, rows0, small_to, n[0]);
 }
 
 template <int GROUP, bool GATED>
 hipError_t launch(const W4Args& a, hipStream_t st) {
-    if (a.m.rows <= kSmall)
-        w4_kernel<GROUP, GATED><<<2048, kPlainWaves * 64, 0, st>>>(a);
+    if (a.m.rows <= 2 * kSmall)
+        w4_few_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(a);
     else
         w4_big_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(a);
     return hipGetLastError();
