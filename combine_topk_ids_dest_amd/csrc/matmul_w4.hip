@@ -95,7 +95,9 @@ constexpr int kFewX = kWaves * kFewRing * kFewStep;      // segments behind the 
 constexpr int kFewPart = kFewX + 2 * kSegment;           // the waves' sums, twice
 constexpr int kFewPitch = kSmall + 4;
 constexpr int kFewSums = kWaves * kSmall * kFewPitch * 4;
-constexpr int kFewLds = kFewPart + 2 * kFewSums;
+constexpr int kFewZero = kFewPart + 2 * kFewSums;        // 512 bytes of zeros
+constexpr int kFewLds = kFewZero + 512;
+static_assert(kFewLds <= 160 << 10, "");
 
 __device__ __forceinline__ int place_few(int r) {
     const int j = (r >> 2) & 3;                  // 0, 1, 2, 3 -> 0, 2, 3, 1
@@ -177,15 +179,12 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
             if (GROUP == 16)
                 load_to_lds(uniform(t.rs), at + 2048, any ? t.vs : kOutside, any ? k / 16 : 0);
             else
-                load4_to_lds(uniform(t.rs), at + 2048,
-                             k + (lane & 1) * 128 < H ? t.vs : kOutside, any ? k / 32 : 0);
+                load4_to_lds(uniform(t.rs), at + 2048, any ? t.vs : kOutside, any ? k / 32 : 0);
         }
+        // (codes behind a row's end meet x's zeros and a scale of zero)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int chunk = (lane & 7) ^ ((h * 4 + (lane >> 4)) & 7);
-            load_to_lds(uniform(t.rw), at + h * 1024, k + chunk * 32 < H ? t.vw[h] : kOutside,
-                        any ? k / 2 : 0);
-        }
+        for (int h = 0; h < 2; ++h)
+            load_to_lds(uniform(t.rw), at + h * 1024, any ? t.vw[h] : kOutside, any ? k / 2 : 0);
     };
     // Segment n of a tile's x into buffer `to`.
     auto fetch_x = [&](const FewTile& t, int n, int to) {
@@ -220,6 +219,8 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
 
     int t0 = 0, at = tile_at(0);
     if (at < 0) return;
+    // (read behind the first segment's barrier)
+    if (threadIdx.x < 128) reinterpret_cast<uint32_t*>(lds + kFewZero)[threadIdx.x] = 0;
     FewTile cur = place(at, wn);
     fetch_x(cur, 0, 0);
 #pragma unroll
@@ -235,63 +236,134 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
         if (at >= 0) nxt = place(at, wn);
         else nxt.left = 0;                       // nothing more to load
         const int lseg = 14 - cur.lx - 8 - lk;   // 2^lseg steps of a segment
-        const int row = r & ((1 << cur.lx) - 1);
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        for (int i = 0; i < nsteps; ++i) {
-            if ((i & ((1 << lseg) - 1)) == 0) {
-                // the segment at hand has arrived: behind it are `since` steps
-                // of three loads
-                if (since >= 4) wait_and_barrier<3 * 4>();
-                else if (since >= 2) wait_and_barrier<3 * 2>();
-                else wait_and_barrier<3>();
-                since = 0;
-                const int n = (i >> lseg) + 1;   // the next
-                if (n << lseg < nsteps) fetch_x(cur, n, to ^ 1);
-                else fetch_x(nxt, 0, to ^ 1);
-                if (owed) finish(old, odd ^ 1);
-                owed = false;
-                to ^= 1;
-            }
-            // the oldest step has arrived: behind it are three steps
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kFewRing - 1) * 3) : "memory");
-            const uint8_t* p = mine + j * kFewStep;
-            const int k = ((i << lk) + wk) * kFewCols;
-            u32x4 c[2];
-            uint32_t sc[2];
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f}, acc2 = acc;
+        // The steps of the tile. Up to four rows with E4M3 scales (SPLIT): products
+        // of bare codes, each group's apart. x is the first operand, its row
+        // 4 g + i row g of x in the columns of lane quarter i and zero in the
+        // others, so that sum 4 g + i of a row of w is over one group of columns;
+        // it is scaled and added. That takes an instruction a weight, weights
+        // widened with their scales two.
+        auto all_steps = [&](auto split) {
+            constexpr bool SPLIT = decltype(split)::value;
+            const int row = SPLIT ? r >> 2 : r & ((1 << cur.lx) - 1);
+            const bool has = !SPLIT || (q == (r & 3) && row < cur.left);
+            const uint32_t real = has ? ~0u : 0u;
+            uint32_t from[4];                    // where the lane reads x, chunks 4 q + t
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                c[h] = *reinterpret_cast<const u32x4*>(p + r * 128 +
-                                                       (((q + 4 * h) ^ (r >> 1)) & 7) * 16);
-                sc[h] = GROUP == 16
-                            ? *reinterpret_cast<const uint16_t*>(p + 2048 + r * 16 + h * 8 + q * 2)
-                            : p[2048 + r * 8 + h * 4 + q];
-            }
-            // read, so its place can be filled again
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-            if (i + kFewRing < nsteps) fetch(cur, i + kFewRing, j);
-            else fetch(nxt, at >= 0 ? i + kFewRing - nsteps : nsteps, j);
-            ++since;
-            j = j + 1 < kFewRing ? j + 1 : 0;
-            if (k < H) {
-                const uint8_t* px = lds + kFewX + (to ^ 1) * kSegment + row * 512 +
-                                    ((((i & ((1 << lseg) - 1)) << lk) + wk) << (9 + cur.lx));
+            for (int t = 0; t < 4; ++t)
+                from[t] = has ? row * 512 + ((q * 4 + t) ^ place_few(row)) * 16
+                              : kFewZero - kFewX;
+            for (int i = 0; i < nsteps; ++i) {
+                const int in_segment = i & ((1 << lseg) - 1);
+                if (in_segment == 0) {
+                    // the segment at hand has arrived: behind it are `since`
+                    // steps of three loads
+                    if (since >= 4) wait_and_barrier<3 * 4>();
+                    else if (since >= 2) wait_and_barrier<3 * 2>();
+                    else wait_and_barrier<3>();
+                    since = 0;
+                    const int n = (i >> lseg) + 1;   // the next
+                    if (n << lseg < nsteps) fetch_x(cur, n, to ^ 1);
+                    else fetch_x(nxt, 0, to ^ 1);
+                    if (owed) finish(old, odd ^ 1);
+                    owed = false;
+                    to ^= 1;
+                }
+                // the oldest step has arrived: behind it are three steps
+                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kFewRing - 1) * 3) : "memory");
+                const uint8_t* p = mine + j * kFewStep;
+                const int k = ((i << lk) + wk) * kFewCols;
+                u32x4 c[2], x[8];
+                uint32_t sc[4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    // what follows the last scale may be anything
-                    const bool in = k + h * 128 + q * 32 < H;
-                    const float s0 = in ? scale_of<GROUP>(sc[h] & 0xFF) : 0.f;
-                    const float s1 = GROUP == 32 ? s0 : in ? scale_of<GROUP>(sc[h] >> 8) : 0.f;
+                    c[h] = *reinterpret_cast<const u32x4*>(p + r * 128 +
+                                                           (((q + 4 * h) ^ (r >> 1)) & 7) * 16);
+                    const uint8_t* ps = p + 2048 + r * (256 / GROUP) + h * (128 / GROUP);
+                    if (SPLIT) {
+                        const u32x2 v = *reinterpret_cast<const u32x2*>(ps);
+                        sc[2 * h] = v[0];
+                        sc[2 * h + 1] = v[1];
+                    } else {
+                        sc[2 * h] = GROUP == 32 ? ps[q]
+                                                : *reinterpret_cast<const uint16_t*>(ps + q * 2);
+                    }
+                }
+                // (of a step behind the last column: not used)
+                const uint32_t at_x = (uint32_t)((to ^ 1) * kSegment) +
+                                      ((uint32_t)((in_segment << lk) + wk) << (9 + cur.lx));
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const u32x4 x = *reinterpret_cast<const u32x4*>(
-                            px + ((h * 16 + q * 4 + t) ^ place_few(row)) * 16);
-                        acc = mma_bf16(widen4<GROUP>(c[h][t], t < 2 ? s0 : s1), x, acc);
+                for (int t = 0; t < 8; ++t)
+                    x[t] = *reinterpret_cast<const u32x4*>(lds + kFewX + from[t & 3] +
+                                                           (at_x & real) + (t >> 2) * 256);
+                // all of them on their way before the first is waited for; read, so
+                // the codes' place can be filled again
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+                if (i + kFewRing < nsteps) fetch(cur, i + kFewRing, j);
+                else fetch(nxt, at >= 0 ? i + kFewRing - nsteps : nsteps, j);
+                ++since;
+                j = j + 1 < kFewRing ? j + 1 : 0;
+                if (k >= H) continue;
+                // what follows the last scale may be anything
+                if constexpr (SPLIT) {
+                    f32x4 d[4];
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+                        d[b] = mma_bf16(x[2 * b], widen4<32>(c[b >> 1][2 * b & 3], 1.0f), zero);
+                    }
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        d[b] = mma_bf16(x[2 * b + 1], widen4<32>(c[b >> 1][(2 * b & 3) + 1], 1.0f),
+                                        d[b]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int n = (H - k - h * 128) / 16;
+                        const uint64_t mask = n >= 8 ? ~0ull : n > 0 ? (1ull << (8 * n)) - 1 : 0;
+                        sc[2 * h] &= (uint32_t)mask;
+                        sc[2 * h + 1] &= (uint32_t)(mask >> 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int v = (int)sc[2 * h + (e >> 1)];
+                            // group 2 e + b of the half: byte 2 (e & 1) + b
+                            const float f0 = e & 1 ? __builtin_amdgcn_cvt_f32_fp8(v, 2)
+                                                   : __builtin_amdgcn_cvt_f32_fp8(v, 0);
+                            const float f1 = e & 1 ? __builtin_amdgcn_cvt_f32_fp8(v, 3)
+                                                   : __builtin_amdgcn_cvt_f32_fp8(v, 1);
+                            acc[e] = __builtin_fmaf(d[2 * h][e], f0, acc[e]);
+                            acc2[e] = __builtin_fmaf(d[2 * h + 1][e], f1, acc2[e]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bool in = k + h * 128 + q * 32 < H;
+                        const uint32_t v = in ? sc[2 * h] : 0;
+                        const float s0 = GROUP == 16 ? __builtin_amdgcn_cvt_f32_fp8((int)v, 0)
+                                                     : __uint_as_float(v << 23);
+                        const float s1 = GROUP == 16 ? __builtin_amdgcn_cvt_f32_fp8((int)v, 1) : s0;
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const u32x4 w = widen4<GROUP>(c[h][t], t < 2 ? s0 : s1);
+                            if (t & 1) acc2 = mma_bf16(w, x[4 * h + t], acc2);
+                            else acc = mma_bf16(w, x[4 * h + t], acc);
+                        }
                     }
                 }
             }
+        };
+        const bool split = GROUP == 16 && cur.left <= 4;
+        if constexpr (GROUP == 16) {
+            if (split) all_steps(std::true_type{});
+            else all_steps(std::false_type{});
+        } else {
+            all_steps(std::false_type{});
         }
         float* part = reinterpret_cast<float*>(lds + kFewPart + odd * kFewSums);
-        *reinterpret_cast<f32x4*>(part + (wave * kSmall + r) * kFewPitch + q * 4) = acc;
+        acc += acc2;
+        if (split) part[(wave * kSmall + q) * kFewPitch + r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        else *reinterpret_cast<f32x4*>(part + (wave * kSmall + r) * kFewPitch + q * 4) = acc;
         old = cur;
         owed = true;
         odd ^= 1;
