@@ -110,17 +110,23 @@ struct FewTile {
     uint32_t vw[2], vs;
     int g, m0, left, n0;
     int lx;                                      // x in 2^lx rows
+    int lk, wk, nsteps;                          // 2^lk waves share out k, this one the wk-th
 };
 
 template <int GROUP, bool GATED>
 __device__ __forceinline__ FewTile few_setup(const W4Args& a, int g, int m0, int rows, int n0,
-                                             int wn) {
+                                             int lw) {
     const MatmulArgs& m = a.m;
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
     const int lane = threadIdx.x & 63;
     const int H = m.row_bytes / 2;
     const int nw = GATED ? 2 * m.N : m.N;
+    const int wave = uniform(threadIdx.x >> 6), wn = wave & ((1 << lw) - 1);
     FewTile t;
+    t.lk = 3 - lw;
+    t.wk = wave >> lw;
+    const int steps = (H + (kFewCols << t.lk) - 1) >> (8 + t.lk);
+    t.nsteps = steps > kFewRing ? steps : kFewRing;
     t.g = g;
     t.m0 = m0;
     t.left = rows - m0 < kSmall ? rows - m0 : kSmall;
@@ -149,22 +155,19 @@ __device__ __forceinline__ FewTile few_setup(const W4Args& a, int g, int m0, int
     return t;
 }
 
-// Works through the block's tiles, number t of `total` at place(t): 16 rows each
-// by WN = 2^lw runs of 16 rows of w.
+// Works through the block's tiles, number t of `total` at place(t): up to 16 rows
+// each by WN = 8 / WK runs of 16 rows of w.
 template <int GROUP, bool GATED, class Next>
-__device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int total, int lw,
+__device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int total,
                                           const Next& place) {
     const MatmulArgs& m = a.m;
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
-    const int wn = wave & ((1 << lw) - 1), wk = wave >> lw, lk = 3 - lw;     // WK = 2^lk
     const int H = m.row_bytes / 2;
     const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
     const uint32_t ring = lds0 + wave * kFewRing * kFewStep;
     const uint8_t* mine = lds + wave * kFewRing * kFewStep;
     const int r = lane & 15, q = lane >> 4;
-    const int steps = (H + (kFewCols << lk) - 1) >> (8 + lk);
-    const int nsteps = steps > kFewRing ? steps : kFewRing;
 
     auto tile_at = [&](int t0) {
         const int t = t0 < total ? tile_of(blockIdx.x, gridDim.x, total - t0) : -1;
@@ -172,7 +175,7 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
     };
     // Step i of a tile into place j of the wave's ring.
     auto fetch = [&](const FewTile& t, int i, int j) {
-        const int k = ((i << lk) + wk) * kFewCols;
+        const int k = ((i << t.lk) + t.wk) * kFewCols;
         const bool any = k < H;
         const uint32_t at = ring + j * kFewStep;
         if (lane < (GROUP == 16 ? 16 : 32)) {
@@ -202,7 +205,7 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
     auto finish = [&](const FewTile& t, int odd) {
         constexpr int BO = GATED ? kSmall / 2 : kSmall;
         const float* part = reinterpret_cast<const float*>(lds + kFewPart + odd * kFewSums);
-        const int wide = BO << lw;
+        const int lw = 3 - t.lk, wide = BO << lw;
         for (int i = threadIdx.x; i < wide * t.left; i += kThreads) {
             const int o = i & (wide - 1), row = i / wide;
             const int n = t.n0 + o;
@@ -221,7 +224,7 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
     if (at < 0) return;
     // (read behind the first segment's barrier)
     if (threadIdx.x < 128) reinterpret_cast<uint32_t*>(lds + kFewZero)[threadIdx.x] = 0;
-    FewTile cur = place(at, wn);
+    FewTile cur = place(at);
     fetch_x(cur, 0, 0);
 #pragma unroll
     for (int j = 0; j < kFewRing; ++j) fetch(cur, j, j);
@@ -233,8 +236,9 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
         t0 += gridDim.x;
         at = tile_at(t0);
         FewTile nxt = cur;
-        if (at >= 0) nxt = place(at, wn);
+        if (at >= 0) nxt = place(at);
         else nxt.left = 0;                       // nothing more to load
+        const int lk = cur.lk, wk = cur.wk, nsteps = cur.nsteps;
         const int lseg = 14 - cur.lx - 8 - lk;   // 2^lseg steps of a segment
         f32x4 acc = {0.f, 0.f, 0.f, 0.f}, acc2 = acc;
         // The steps of the tile. Up to four rows with E4M3 scales (SPLIT): products
@@ -301,7 +305,7 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
                 if (i + kFewRing < nsteps) fetch(cur, i + kFewRing, j);
-                else fetch(nxt, at >= 0 ? i + kFewRing - nsteps : nsteps, j);
+                else fetch(nxt, at >= 0 ? i + kFewRing - nsteps : nxt.nsteps, j);
                 ++since;
                 j = j + 1 < kFewRing ? j + 1 : 0;
                 if (k >= H) continue;
@@ -375,22 +379,42 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
     finish(old, odd ^ 1);
 }
 
-// Runs of 16 rows of w side by side (as a power of two) for `runs` runs of up to
-// 16 rows, some of more than 8 (`wide`): the least rounds of the grid times a
-// tile's time, by its bytes and about 2048 columns' worth of start and end.
+// How the tiles of `runs` runs of up to 16 rows are cut: 2^lw runs of 16 rows of
+// w each, but in the grid's last, partial round 2^last, so that it is shorter
+// where CUs would be idle.
+struct FewCut {
+    int lw, last;
+    int nt;                                      // tiles of a run, over all columns
+    int whole, total;                            // tiles before the last round, and of all rounds
+};
+
+// The cut of least rounds times a tile's time, by its bytes and about 2048
+// columns' worth of start and end. least: lw for runs of more than 8 rows (a
+// step of 2048 columns of 16 rows is no segment).
 template <bool GATED>
-__device__ __forceinline__ int few_across(int runs, int N, int H, bool wide) {
+__device__ __forceinline__ FewCut few_cut(int runs, int N, int H, int least) {
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
-    int best = 3;
-    int64_t least = INT64_MAX;
+    FewCut best = {};
+    int64_t best_cost = INT64_MAX;
 #pragma unroll
     for (int lw = 3; lw >= 0; --lw) {
-        if (lw == 0 && wide) break;              // a step of 2048 columns of 16 rows is no segment
-        const int64_t tiles = (int64_t)runs * ((N + (BO << lw) - 1) / (BO << lw));
-        const int64_t cost = (tiles + kGrid - 1) / kGrid * (((int64_t)H << lw) + 2048);
-        if (cost < least) {
-            least = cost;
-            best = lw;
+        if (lw < least) break;
+        FewCut c;
+        c.lw = c.last = lw;
+        c.nt = (N + (BO << lw) - 1) / (BO << lw);
+        const int tiles = runs * c.nt;
+        c.whole = tiles / kGrid * kGrid;
+        int rest = tiles - c.whole;
+        while (c.last > least && rest * 2 <= kGrid) {
+            rest *= 2;
+            --c.last;
+        }
+        c.total = c.whole + rest;
+        const int64_t cost = c.whole / kGrid * (((int64_t)H << lw) + 2048) +
+                             (rest ? ((int64_t)H << c.last) + 2048 : 0);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = c;
         }
     }
     return best;
@@ -406,13 +430,33 @@ __device__ __forceinline__ void few_rows(const W4Args& a, uint8_t* lds, int rows
         const int rows = g0 ? lane_rows(m, g0) : rows0;
         wide |= __ballot(rows <= small_to && rows > 8) != 0;
     }
-    const int lw = few_across<GATED>(runs, m.N, m.row_bytes / 2, wide);
-    const int nt = (m.N + (BO << lw) - 1) / (BO << lw);
-    few_tiles<GROUP, GATED>(a, lds, runs * nt, lw, [&](int t, int wn) {
-        const Place at = find_tile(m, rows0, small_to, 0, nt, t);
-        const int mt = cut_rows(at.rows, small_to).runs;
-        return few_setup<GROUP, GATED>(a, at.g, at.l % mt * kSmall, at.rows,
-                                       at.l / mt * (BO << lw), wn);
+    const FewCut cut = few_cut<GATED>(runs, m.N, m.row_bytes / 2, wide ? 1 : 0);
+    // the first 64 groups' runs, added up: where a tile is without a scan of its own
+    const int runs0 = runs_of(rows0, small_to, 0);
+    const int upto = wave_inclusive_scan(runs0);
+    const int covered = __builtin_amdgcn_readlane(upto, 63);
+    few_tiles<GROUP, GATED>(a, lds, cut.total, [&](int t) {
+        int lw = cut.lw, n0 = 0;
+        if (t >= cut.whole) {
+            const int split = cut.lw - cut.last, u = t - cut.whole;
+            lw = cut.last;
+            n0 = (u & ((1 << split) - 1)) * (BO << lw);
+            t = cut.whole + (u >> split);
+        }
+        Place at;
+        if (t < covered * cut.nt) {
+            const int l = __builtin_ctzll(__ballot(upto * cut.nt > t));
+            const int mine = __builtin_amdgcn_readlane(runs0, l);
+            at.g = l;
+            at.rows = __builtin_amdgcn_readlane(rows0, l);
+            at.l = t - (__builtin_amdgcn_readlane(upto, l) - mine) * cut.nt;
+        } else {
+            at = find_tile(m, rows0, small_to, 0, cut.nt, t);
+        }
+        const int mt = (at.rows + kSmall - 1) / kSmall;
+        const int col = mt == 1 ? at.l : at.l / mt;
+        return few_setup<GROUP, GATED>(a, at.g, (at.l - col * mt) * kSmall, at.rows,
+                                       col * (BO << cut.lw) + n0, lw);
     });
 }
 
