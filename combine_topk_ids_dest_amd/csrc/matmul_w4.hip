@@ -189,14 +189,18 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
         for (int h = 0; h < 2; ++h)
             load_to_lds(uniform(t.rw), at + h * 1024, any ? t.vw[h] : kOutside, any ? k / 2 : 0);
     };
-    // Segment n of a tile's x into buffer `to`.
+    // Segment n of a tile's x into buffer `to`: two rows of 256 columns a load
+    // (none for rows and columns that no wave reads).
     auto fetch_x = [&](const FewTile& t, int n, int to) {
-#pragma unroll
+        const int pairs = t.lx - 1;              // 2^pairs pairs of rows
+#pragma unroll 1
         for (int i = 0; i < kSegment / 1024 / kWaves; ++i) {
-            const int load = wave * (kSegment / 1024 / kWaves) + i, at = load * 64 + lane;
-            const int row = (at >> 5) & ((1 << t.lx) - 1);
-            const int k = (n << (14 - t.lx)) + (at >> (5 + t.lx)) * kFewCols +
-                          ((at & 31) ^ place_few(row)) * 8;
+            const int load = i * kWaves + wave;
+            const int k0 = (n << (14 - t.lx)) + (load >> pairs) * kFewCols;
+            const int row0 = (load & ((1 << pairs) - 1)) * 2;
+            if (k0 >= H || row0 >= t.left) continue;
+            const int row = row0 + (lane >> 5);
+            const int k = k0 + ((lane & 31) ^ place_few(row)) * 8;
             load_to_lds(uniform(t.rx), lds0 + kFewX + to * kSegment + load * 1024,
                         row < t.left && k < H ? (uint32_t)row * (uint32_t)m.x_row + k * 2 : kOutside,
                         0);
@@ -225,8 +229,9 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
     // (read behind the first segment's barrier)
     if (threadIdx.x < 128) reinterpret_cast<uint32_t*>(lds + kFewZero)[threadIdx.x] = 0;
     FewTile cur = place(at);
+    // (rolled: at the start every line of code is a miss)
     fetch_x(cur, 0, 0);
-#pragma unroll
+#pragma unroll 1
     for (int j = 0; j < kFewRing; ++j) fetch(cur, j, j);
     FewTile old = cur;
     bool owed = false;                           // old's sums are still to be added up
@@ -237,7 +242,6 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
         at = tile_at(t0);
         FewTile nxt = cur;
         if (at >= 0) nxt = place(at);
-        else nxt.left = 0;                       // nothing more to load
         const int lk = cur.lk, wk = cur.wk, nsteps = cur.nsteps;
         const int lseg = 14 - cur.lx - 8 - lk;   // 2^lseg steps of a segment
         f32x4 acc = {0.f, 0.f, 0.f, 0.f}, acc2 = acc;
@@ -264,21 +268,29 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
                     // steps of three loads
                     if (since >= 4) wait_and_barrier<3 * 4>();
                     else if (since >= 2) wait_and_barrier<3 * 2>();
-                    else wait_and_barrier<3>();
+                    else if (since == 1) wait_and_barrier<3>();
+                    else wait_and_barrier<0>();
                     since = 0;
                     const int n = (i >> lseg) + 1;   // the next
                     if (n << lseg < nsteps) fetch_x(cur, n, to ^ 1);
-                    else fetch_x(nxt, 0, to ^ 1);
+                    else if (at >= 0) fetch_x(nxt, 0, to ^ 1);
                     if (owed) finish(old, odd ^ 1);
                     owed = false;
                     to ^= 1;
                 }
-                // the oldest step has arrived: behind it are three steps
-                asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kFewRing - 1) * 3) : "memory");
+                // the oldest step has arrived: behind it are three steps, or what
+                // is left of the last tile
+                const int behind = at >= 0 ? kFewRing - 1 : nsteps - 1 - i;
+                static_assert(kFewRing == 4, "");
+                if (behind >= 3) asm volatile("s_waitcnt vmcnt(9)" ::: "memory");
+                else if (behind == 2) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+                else if (behind == 1) asm volatile("s_waitcnt vmcnt(3)" ::: "memory");
+                else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
                 const uint8_t* p = mine + j * kFewStep;
                 const int k = ((i << lk) + wk) * kFewCols;
                 u32x4 c[2], x[8];
                 uint32_t sc[4];
+                if (k < H) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     c[h] = *reinterpret_cast<const u32x4*>(p + r * 128 +
@@ -293,20 +305,24 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
                                                 : *reinterpret_cast<const uint16_t*>(ps + q * 2);
                     }
                 }
-                // (of a step behind the last column: not used)
                 const uint32_t at_x = (uint32_t)((to ^ 1) * kSegment) +
                                       ((uint32_t)((in_segment << lk) + wk) << (9 + cur.lx));
 #pragma unroll
                 for (int t = 0; t < 8; ++t)
                     x[t] = *reinterpret_cast<const u32x4*>(lds + kFewX + from[t & 3] +
                                                            (at_x & real) + (t >> 2) * 256);
+                }
                 // all of them on their way before the first is waited for; read, so
                 // the codes' place can be filled again
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
-                if (i + kFewRing < nsteps) fetch(cur, i + kFewRing, j);
-                else fetch(nxt, at >= 0 ? i + kFewRing - nsteps : nxt.nsteps, j);
-                ++since;
+                if (i + kFewRing < nsteps) {
+                    fetch(cur, i + kFewRing, j);
+                    ++since;
+                } else if (at >= 0) {
+                    fetch(nxt, i + kFewRing - nsteps, j);
+                    ++since;
+                }
                 j = j + 1 < kFewRing ? j + 1 : 0;
                 if (k >= H) continue;
                 // what follows the last scale may be anything
@@ -374,47 +390,29 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
         if (at < 0) break;
         cur = nxt;
     }
-    // nothing of this block's is on its way into LDS when the block ends
     wait_and_barrier<0>();
     finish(old, odd ^ 1);
 }
 
-// How the tiles of `runs` runs of up to 16 rows are cut: 2^lw runs of 16 rows of
-// w each, but in the grid's last, partial round 2^last, so that it is shorter
-// where CUs would be idle.
-struct FewCut {
-    int lw, last;
-    int nt;                                      // tiles of a run, over all columns
-    int whole, total;                            // tiles before the last round, and of all rounds
-};
-
-// The cut of least rounds times a tile's time, by its bytes and about 2048
-// columns' worth of start and end. least: lw for runs of more than 8 rows (a
-// step of 2048 columns of 16 rows is no segment).
-template <bool GATED>
-__device__ __forceinline__ FewCut few_cut(int runs, int N, int H, int least) {
-    constexpr int BO = GATED ? kSmall / 2 : kSmall;
+// The cut of `runs` runs of up to 16 rows, of least rounds times a tile's time, by
+// its bytes and about 2048 columns' worth of start and end. least: lw for runs
+// of more than 8 rows (a step of 2048 columns of 16 rows is no segment).
+__host__ __device__ __forceinline__ FewCut few_cut(int runs, int N, int H, int bo, int least) {
     FewCut best = {};
-    int64_t best_cost = INT64_MAX;
+    float best_cost = 0.f;
 #pragma unroll
     for (int lw = 3; lw >= 0; --lw) {
         if (lw < least) break;
-        FewCut c;
-        c.lw = c.last = lw;
-        c.nt = (N + (BO << lw) - 1) / (BO << lw);
-        const int tiles = runs * c.nt;
-        c.whole = tiles / kGrid * kGrid;
-        int rest = tiles - c.whole;
-        while (c.last > least && rest * 2 <= kGrid) {
-            rest *= 2;
-            --c.last;
-        }
-        c.total = c.whole + rest;
-        const int64_t cost = c.whole / kGrid * (((int64_t)H << lw) + 2048) +
-                             (rest ? ((int64_t)H << c.last) + 2048 : 0);
-        if (cost < best_cost) {
+        const int nt = (N + (bo << lw) - 1) / (bo << lw);
+        const int tiles = runs * nt;
+        const int whole = tiles / kGrid * kGrid, rest = tiles - whole;
+        int split = rest * 8 <= kGrid ? 3 : rest * 4 <= kGrid ? 2 : rest * 2 <= kGrid ? 1 : 0;
+        if (split > lw - least) split = lw - least;
+        const float cost = (float)(whole / kGrid) * (float)((H << lw) + 2048) +
+                           (rest ? (float)((H << (lw - split)) + 2048) : 0.f);
+        if (lw == 3 || cost < best_cost) {
             best_cost = cost;
-            best = c;
+            best = FewCut{lw, lw - split, nt, whole, whole + (rest << split)};
         }
     }
     return best;
@@ -425,16 +423,22 @@ __device__ __forceinline__ void few_rows(const W4Args& a, uint8_t* lds, int rows
                                          int runs) {
     const MatmulArgs& m = a.m;
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
-    bool wide = false;
-    for (int g0 = 0; g0 < m.groups; g0 += 64) {
-        const int rows = g0 ? lane_rows(m, g0) : rows0;
-        wide |= __ballot(rows <= small_to && rows > 8) != 0;
+    FewCut cut = a.cut;                          // over all tokens the host's
+    if (m.counts) {
+        bool wide = false;
+        for (int g0 = 0; g0 < m.groups; g0 += 64) {
+            const int rows = g0 ? lane_rows(m, g0) : rows0;
+            wide |= __ballot(rows <= small_to && rows > 8) != 0;
+        }
+        cut = few_cut(runs, m.N, m.row_bytes / 2, BO, wide ? 1 : 0);
     }
-    const FewCut cut = few_cut<GATED>(runs, m.N, m.row_bytes / 2, wide ? 1 : 0);
     // the first 64 groups' runs, added up: where a tile is without a scan of its own
-    const int runs0 = runs_of(rows0, small_to, 0);
-    const int upto = wave_inclusive_scan(runs0);
-    const int covered = __builtin_amdgcn_readlane(upto, 63);
+    int runs0 = 0, upto = 0, covered = 0;
+    if (m.counts) {
+        runs0 = runs_of(rows0, small_to, 0);
+        upto = wave_inclusive_scan(runs0);
+        covered = __builtin_amdgcn_readlane(upto, 63);
+    }
     few_tiles<GROUP, GATED>(a, lds, cut.total, [&](int t) {
         int lw = cut.lw, n0 = 0;
         if (t >= cut.whole) {
@@ -444,7 +448,9 @@ __device__ __forceinline__ void few_rows(const W4Args& a, uint8_t* lds, int rows
             t = cut.whole + (u >> split);
         }
         Place at;
-        if (t < covered * cut.nt) {
+        if (!m.counts) {
+            at = Place{0, m.rows, t};
+        } else if (t < covered * cut.nt) {
             const int l = __builtin_ctzll(__ballot(upto * cut.nt > t));
             const int mine = __builtin_amdgcn_readlane(runs0, l);
             at.g = l;
@@ -463,10 +469,13 @@ __device__ __forceinline__ void few_rows(const W4Args& a, uint8_t* lds, int rows
 template <int GROUP, bool GATED>
 __global__ __launch_bounds__(kThreads, 2) void w4_few_kernel(const W4Args a) {
     __shared__ __align__(1024) uint8_t lds[kFewLds];
+    if (!a.m.counts) return few_rows<GROUP, GATED>(a, lds, 0, INT32_MAX, 0);
     const int rows0 = lane_rows(a.m, 0);
-    int n[kKinds];
-    count_runs(a.m, rows0, INT32_MAX, n);
-    if (n[0] > 0) few_rows<GROUP, GATED>(a, lds, rows0, INT32_MAX, n[0]);
+    int runs = 0;
+    for (int g0 = 0; g0 < a.m.groups; g0 += 64)
+        runs += __builtin_amdgcn_readlane(
+            wave_inclusive_scan(runs_of(g0 ? lane_rows(a.m, g0) : rows0, INT32_MAX, 0)), 63);
+    if (runs > 0) few_rows<GROUP, GATED>(a, lds, rows0, INT32_MAX, runs);
 }
 
 // ---------------------------------------------------------------------
@@ -703,9 +712,12 @@ __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
 
 template <int GROUP, bool GATED>
 hipError_t launch(const W4Args& a, hipStream_t st) {
-    if (a.m.rows <= 2 * kSmall)
-        w4_few_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(a);
-    else
+    if (a.m.rows <= 2 * kSmall) {
+        W4Args b = a;
+        b.cut = few_cut((a.m.rows + kSmall - 1) / kSmall, a.m.N, a.m.row_bytes / 2,
+                        GATED ? kSmall / 2 : kSmall, a.m.rows > 8 ? 1 : 0);
+        w4_few_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(b);
+    } else
         w4_big_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(a);
     return hipGetLastError();
 }
