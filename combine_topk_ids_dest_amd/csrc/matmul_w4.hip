@@ -11,28 +11,31 @@
 namespace moe_ep {
 namespace {
 
-// Eight codes (the first in the lowest bits) times their scale, as bf16.
-template <int GROUP>
-__device__ __forceinline__ u32x4 widen4(uint32_t c, float s) {
-    u32x4 r;
+// Four codes, the low (HALF 0) or high ones of c, times their scale, as bf16.
+template <int GROUP, int HALF>
+__device__ __forceinline__ u32x2 widen_half(uint32_t c, float s) {
     if constexpr (GROUP == 32) {
         // a power of two: the instruction's own scale
-        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
-        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
-        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
-        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
+        return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
+                                                      c, s, 2 * HALF)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
+                                                      c, s, 2 * HALF + 1))};
     } else {
         auto two = [s](auto v) {
             const float lo = v[0] * s, hi = v[1] * s;
             // exact in bf16: the upper halves
             return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
         };
-        r[0] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0));
-        r[1] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1));
-        r[2] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2));
-        r[3] = two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3));
+        return u32x2{two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2 * HALF)),
+                     two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2 * HALF + 1))};
     }
-    return r;
+}
+
+// Eight codes, the first in the lowest bits.
+template <int GROUP>
+__device__ __forceinline__ u32x4 widen4(uint32_t c, float s) {
+    const u32x2 lo = widen_half<GROUP, 0>(c, s), hi = widen_half<GROUP, 1>(c, s);
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
 // A scale from its code.
@@ -599,53 +602,77 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, int g, int m0, int rows
 #pragma unroll
         for (int j = 0; j < JF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    // Products go half a slab at a time (8 of a lane's 16 columns), and under each
+    // half's products the next half's fragments of x are read and its weights
+    // widened. The wait in the middle of slab s is for slab s + 1.
+    u32x4 fx[2][JF], fw[2][FRAGS];
+    u32x2 c[FRAGS];                              // of the slab whose half 1 is to come
+    float f[FRAGS];
+    auto read_codes = [&](int s, int stage) {
+        const uint8_t* pw = lds + rdw + stage * kPairCodes + ((((s & 1) * 2 + (q >> 1)) ^ swap) * 16);
+        const uint8_t* ps = lds + rds + ((s >> 1) / SP) % kScaleSets * kScaleSet +
+                            (s >> 1) % SP * (16 / SP) + (s & 1) * (8 / SP);
+        const bool in = s * 64 + q * 16 < H;     // what follows the last scale may be anything
+#pragma unroll
+        for (int i = 0; i < FRAGS; ++i) {
+            c[i] = *reinterpret_cast<const u32x2*>(pw + i * 16 * 64);
+            const uint32_t code = ps[i * 16 * 16];
+            f[i] = in ? scale_of<GROUP>(code) : 0.f;
+        }
+    };
+    // Part n of 2 FRAGS of a half's widening.
+    auto widen_part = [&](auto half, int n) {
+        constexpr int h = decltype(half)::value;
+        const int i = n >> 1;
+        const u32x2 v = n & 1 ? widen_half<GROUP, 1>(c[i][h], f[i]) : widen_half<GROUP, 0>(c[i][h], f[i]);
+        fw[h][i][(n & 1) * 2] = v[0];
+        fw[h][i][(n & 1) * 2 + 1] = v[1];
+    };
+    // Multiplies half `now` while reading and widening the other one (of x at px).
+    auto multiply = [&](auto now, const uint8_t* px) {
+        constexpr int h = decltype(now)::value, o = 1 - h;
+#pragma unroll
+        for (int j = 0; j < JF; ++j) {
+            fx[o][j] = *reinterpret_cast<const u32x4*>(px + (rdx ^ (o * 16)) + j * 16 * kSlab);
+#pragma unroll
+            for (int n = j * 2 * FRAGS / JF; n < (j + 1) * 2 * FRAGS / JF; ++n)
+                widen_part(std::integral_constant<int, o>{}, n);
+#pragma unroll
+            for (int i = 0; i < FRAGS; ++i) acc[i][j] = mma_bf16(fw[h][i], fx[h][j], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+
     if (is_x) {
 #pragma unroll
-        for (int v = 0; v < XS - 1; ++v) fetch_x(v, v);
+        for (int v = 0; v < XS; ++v) fetch_x(v, v);
+        wait_and_barrier<(XS - 1) * FX>();
     } else {
 #pragma unroll
-        for (int p = 0; p < WS - 1; ++p) fetch_w(p, p);
+        for (int p = 0; p < WS; ++p) fetch_w(p, p);
+        wait_and_barrier<(WS - 1) * 4>();
     }
+    read_codes(0, 0);
+#pragma unroll
+    for (int j = 0; j < JF; ++j)
+        fx[0][j] = *reinterpret_cast<const u32x4*>(lds + rdx + j * 16 * kSlab);
+#pragma unroll
+    for (int n = 0; n < 2 * FRAGS; ++n) widen_part(std::integral_constant<int, 0>{}, n);
     int ix = 0, iw = 0;                           // stages of slab s and of its pair
     for (int s = 0; s < nslab; ++s) {
-        const int p = s >> 1;
-        // Slab s (and its pair, with the scales asked for before it) has
-        // arrived, slab s - 1 is read. Behind them are the loads of XS - 2
-        // slabs, of WS - 2 pairs and now and then of scales.
+        multiply(std::integral_constant<int, 0>{}, lds + ix * SLAB_X);
+        // Slab s is read; slab s + 1 (and its pair, with the scales asked for
+        // before it) has arrived. Behind them are the loads of XS - 2 slabs, of
+        // WS - 2 pairs and now and then of scales.
         if (is_x) wait_and_barrier<(XS - 2) * FX>();
         else wait_and_barrier<(WS - 2) * 4>();
-        if (is_x) fetch_x(s + XS - 1, ix == 0 ? XS - 1 : ix - 1);
-        else if (!(s & 1)) fetch_w(p + WS - 1, iw == 0 ? WS - 1 : iw - 1);
-        const uint8_t* px = lds + ix * SLAB_X;
-        const uint8_t* pw = lds + iw * kPairCodes + ((((s & 1) * 2 + (q >> 1)) ^ swap) * 16);
-        const uint8_t* ps = lds + (p / SP) % kScaleSets * kScaleSet + p % SP * (16 / SP) +
-                            (s & 1) * (8 / SP);
-        const bool in = s * 64 + q * 16 < H;      // what follows the last scale may be anything
-        u32x2 c[FRAGS];
-        uint32_t sc[FRAGS];
-#pragma unroll
-        for (int i = 0; i < FRAGS; ++i) {
-            c[i] = *reinterpret_cast<const u32x2*>(pw + rdw + i * 16 * 64);
-            sc[i] = ps[rds + i * 16 * 16];
-        }
-        u32x4 w[FRAGS][2];
-#pragma unroll
-        for (int i = 0; i < FRAGS; ++i) {
-            const float f = in ? scale_of<GROUP>(sc[i]) : 0.f;
-            w[i][0] = widen4<GROUP>(c[i][0], f);
-            w[i][1] = widen4<GROUP>(c[i][1], f);
-        }
-#pragma unroll
-        for (int j = 0; j < JF; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u32x4 x =
-                    *reinterpret_cast<const u32x4*>(px + (rdx ^ (h * 16)) + j * 16 * kSlab);
-#pragma unroll
-                for (int i = 0; i < FRAGS; ++i) acc[i][j] = mma_bf16(w[i][h], x, acc[i][j]);
-            }
-        ix = ix + 1 < XS ? ix + 1 : 0;
-        if (s & 1) iw = iw + 1 < WS ? iw + 1 : 0;
+        const int nix = ix + 1 < XS ? ix + 1 : 0, niw = iw + 1 < WS ? iw + 1 : 0;
+        read_codes(s + 1, s & 1 ? niw : iw);
+        if (is_x) fetch_x(s + XS, ix);
+        else if (s & 1) fetch_w((s >> 1) + WS, iw);
+        multiply(std::integral_constant<int, 1>{}, lds + nix * SLAB_X);
+        ix = nix;
+        if (s & 1) iw = niw;
     }
     wait_and_barrier<0>();   // LDS is free for the next tile
     if (a.whole) {
