@@ -633,12 +633,12 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, int g, int m0, int rows
         constexpr int h = decltype(now)::value, o = 1 - h;
 #pragma unroll
         for (int j = 0; j < JF; ++j) {
+#pragma unroll
+            for (int i = 0; i < FRAGS; ++i) acc[i][j] = mma_bf16(fw[h][i], fx[h][j], acc[i][j]);
             fx[o][j] = *reinterpret_cast<const u32x4*>(px + (rdx ^ (o * 16)) + j * 16 * kSlab);
 #pragma unroll
             for (int n = j * 2 * FRAGS / JF; n < (j + 1) * 2 * FRAGS / JF; ++n)
                 widen_part(std::integral_constant<int, o>{}, n);
-#pragma unroll
-            for (int i = 0; i < FRAGS; ++i) acc[i][j] = mma_bf16(fw[h][i], fx[h][j], acc[i][j]);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -685,11 +685,197 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, int g, int m0, int rows
     finish_tile<2, GATED, FRAGS, JF, WN>(m, g, m0, left, n0, acc, lds);
 }
 
+// ---------------------------------------------------------------------
+// Middle tiles: BM = 32, 64 or 128 rows of x by 256 of w, where a slab's products
+// are over before LDS has answered. They go by pairs of slabs, one barrier each:
+// a lane has 32 consecutive columns of a pair, 16 bytes of codes and four chunks
+// of x, in two units of 16 columns (one E4M3 scale); under a unit's products the
+// next unit's x is on its way into registers, and behind the barrier the next
+// pair's codes.
+//
+// LDS: a 256-byte row of x holds chunk c at c ^ place_few(r), a 64-byte row of
+// codes at c ^ (-(r / 4) & 3); the sets of 16 lanes of a 16-byte read (see the
+// big tiles) meet on no bank.
+// ---------------------------------------------------------------------
+template <int BM>
+constexpr int kMidX = 3;                         // pairs of x in LDS
+template <int BM>
+constexpr int kMidW = BM == 128 ? 3 : 6;         // and of codes
+
+template <int GROUP, bool GATED, int BM, int WN>
+__device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int rows, int n0,
+                                            uint8_t* lds) {
+    constexpr int JF = BM * WN / 128;             // fragments of x of a wave
+    constexpr int FRAGS = 16 / WN;                // and of w
+    constexpr int XS = kMidX<BM>, WS = kMidW<BM>;
+    constexpr int PAIR_X = BM * 256;
+    constexpr int FX = BM / 16;                   // loads of a wave per pair of x
+    constexpr int AT_W = XS * PAIR_X, AT_S = AT_W + WS * kPairCodes;
+    constexpr int SP = GROUP / 8;                 // pairs under 16 bytes of scales
+    static_assert(AT_S + kScaleSets * kScaleSet <= kLds, "");
+    static_assert((WS + SP - 2) / SP + 1 <= kScaleSets && WS <= 3 * SP + 1, "");
+    const MatmulArgs& m = a.m;
+    const int lane = threadIdx.x & 63;
+    const int wave = uniform(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const bool is_x = wave < 4;
+    const int H = m.row_bytes / 2;
+    const int npair = (H + 127) / 128;
+    const int left = rows - m0 < BM ? rows - m0 : BM;
+    const int nw = GATED ? 2 * m.N : m.N;
+    const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
+    const i32x4 rx = row_rsrc4(m.x + g * m.x_stride + (int64_t)m0 * m.x_row,
+                               (int64_t)(left - 1) * m.x_row + m.row_bytes);
+    const i32x4 rw = row_rsrc4(m.w + g * m.w_stride, (int64_t)(nw - 1) * m.w_row + H / 2);
+    const i32x4 rs = row_rsrc4(a.s + g * a.s_stride,
+                               (int64_t)(nw - 1) * a.s_row + (H / GROUP + 15) / 16 * 16);
+
+    // Load i of x fills rows (i * 4 + wave) * 4 .. + 3, of codes rows
+    // (i * 4 + wave - 4) * 16 .. + 15 of the tile.
+    const int row = is_x ? wave * 4 + (lane >> 4) : (wave - 4) * 16 + (lane >> 2);
+    uint32_t at, at_s = kOutside;
+    int n = 0, chunk;
+    if (is_x) {
+        chunk = ((lane & 15) ^ place_few(row)) * 16;
+        at = (uint32_t)row * (uint32_t)m.x_row + chunk;
+    } else {
+        const int srow = wrow<GATED, FRAGS>((wave - 4) * 64 + lane, n0, m.N, n);
+        if (n < m.N) at_s = (uint32_t)srow * (uint32_t)a.s_row;
+        chunk = ((lane & 3) ^ (-(row >> 2) & 3)) * 16;
+        at = (uint32_t)wrow<GATED, FRAGS>(row, n0, m.N, n) * (uint32_t)m.w_row + chunk;
+    }
+    constexpr int STEP = GATED ? 32 : 64;         // output columns of 64 rows of w
+    const uint32_t step = is_x ? 16u * (uint32_t)m.x_row : (uint32_t)STEP * (uint32_t)m.w_row;
+    const int have = is_x ? (left - row + 15) / 16 : (m.N - n + STEP - 1) / STEP;
+    auto fetch_x = [&](int p, int stage) {
+        const bool in = p * 256 + chunk < m.row_bytes;
+        const uint32_t k = 2 * p * kSlab < m.row_bytes ? p * 256 : 0;
+#pragma unroll
+        for (int i = 0; i < FX; ++i)
+            load_to_lds(rx, lds0 + stage * PAIR_X + (i * 4 + wave) * 1024,
+                        in && i < have ? at + i * step : kOutside, k);
+    };
+    // (codes behind a row's end meet a scale of zero)
+    auto fetch_w = [&](int p, int stage) {
+        const bool any = p < npair;
+        if (p % SP == 0)
+            load_to_lds(rs, lds0 + AT_S + (p / SP) % kScaleSets * kScaleSet + (wave - 4) * 1024,
+                        any ? at_s : kOutside, any ? p / SP * 16 : 0);
+        const uint32_t k = any ? p * 64 : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            load_to_lds(rw, lds0 + AT_W + stage * kPairCodes + (i * 4 + wave - 4) * 1024,
+                        any && i < have ? at + i * step : kOutside, k);
+    };
+
+    const int r = lane & 15, q = lane >> 4;
+    const int rdx = (wm * (JF * 16) + r) * 256 + ((4 * q) ^ place_few(r)) * 16;
+    const int rdw = AT_W + (wn * (FRAGS * 16) + r) * 64 + (q ^ (-(r >> 2) & 3)) * 16;
+    const int rds = AT_S + (wn * (FRAGS * 16) + r) * 16 + q * (32 / GROUP);
+    f32x4 acc[FRAGS][JF];
+#pragma unroll
+    for (int i = 0; i < FRAGS; ++i)
+#pragma unroll
+        for (int j = 0; j < JF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 fx[2][2][JF];                           // of a unit's two chunks
+    u32x4 c[2][FRAGS];                            // codes of this pair and of the next
+    uint32_t sc[2][FRAGS];
+    auto read_x = [&](auto unit, const uint8_t* px) {
+        constexpr int u = decltype(unit)::value;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < JF; ++j)
+                fx[u][h][j] = *reinterpret_cast<const u32x4*>(px + (rdx ^ ((2 * u + h) * 16)) +
+                                                              j * 16 * 256);
+    };
+    auto read_codes = [&](int to, int p, int stage) {
+        const uint8_t* pw = lds + rdw + stage * kPairCodes;
+        const uint8_t* ps =
+            lds + rds + (p / SP) % kScaleSets * kScaleSet + p % SP * (16 / SP);
+#pragma unroll
+        for (int i = 0; i < FRAGS; ++i) {
+            c[to][i] = *reinterpret_cast<const u32x4*>(pw + i * 16 * 64);
+            sc[to][i] = GROUP == 16 ? *reinterpret_cast<const uint16_t*>(ps + i * 16 * 16)
+                                    : ps[i * 16 * 16];
+        }
+    };
+    auto multiply = [&](auto unit, int of) {
+        constexpr int u = decltype(unit)::value;
+#pragma unroll
+        for (int i = 0; i < FRAGS; ++i) {
+            const float f = GROUP == 16 ? __builtin_amdgcn_cvt_f32_fp8((int)sc[of][i], u)
+                                        : __uint_as_float(sc[of][i] << 23);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 w = widen4<GROUP>(c[of][i][2 * u + h], f);
+#pragma unroll
+                for (int j = 0; j < JF; ++j) acc[i][j] = mma_bf16(w, fx[u][h][j], acc[i][j]);
+            }
+        }
+    };
+    const std::integral_constant<int, 0> first;
+    const std::integral_constant<int, 1> second;
+
+    if (is_x) {
+#pragma unroll
+        for (int v = 0; v < XS; ++v) fetch_x(v, v);
+        wait_and_barrier<(XS - 1) * FX>();
+    } else {
+#pragma unroll
+        for (int v = 0; v < WS; ++v) fetch_w(v, v);
+        wait_and_barrier<(WS - 1) * 4>();
+    }
+    read_codes(0, 0, 0);
+    read_x(first, lds);
+    int ix = 0, iw = 0;                           // stages of pair p
+    auto one = [&](int p, auto of) {
+        constexpr int now = decltype(of)::value;
+        // what follows the last scale may be anything
+        if (p * 128 + q * 32 >= H)
+#pragma unroll
+            for (int i = 0; i < FRAGS; ++i) sc[now][i] = 0;
+        read_x(second, lds + ix * PAIR_X);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(first, now);
+        // Pair p is read; pair p + 1 (with the scales asked for before it) has
+        // arrived. Behind it are the loads of XS - 2 pairs of x, of WS - 2 of
+        // codes and now and then of scales.
+        if (is_x) wait_and_barrier<(XS - 2) * FX>();
+        else wait_and_barrier<(WS - 2) * 4>();
+        const int nix = ix + 1 < XS ? ix + 1 : 0, niw = iw + 1 < WS ? iw + 1 : 0;
+        read_codes(1 - now, p + 1, niw);
+        read_x(first, lds + nix * PAIR_X);
+        if (is_x) fetch_x(p + XS, ix);
+        else fetch_w(p + WS, iw);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(second, now);
+        ix = nix;
+        iw = niw;
+    };
+    for (int p = 0; p < npair; p += 2) {
+        one(p, first);
+        if (p + 1 < npair) one(p + 1, second);
+    }
+    wait_and_barrier<0>();   // LDS is free for the next tile
+    if (a.whole) {
+        const float* f = a.whole + g * (GATED ? 2 : 1);
+#pragma unroll
+        for (int i = 0; i < FRAGS; ++i)
+#pragma unroll
+            for (int j = 0; j < JF; ++j) acc[i][j] *= f[GATED ? i & 1 : 0];
+    }
+    finish_tile<2, GATED, FRAGS, JF, WN>(m, g, m0, left, n0, acc, lds);
+}
+
 template <int GROUP, bool GATED>
 __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
     __shared__ __align__(1024) uint8_t lds[kLds];
     const MatmulArgs& m = a.m;
     constexpr int BB = GATED ? kCols / 2 : kCols;
+    // 64 rows: each wave all of them, so that a weight is widened once, or with
+    // powers of two, which take little of that, half of them and less of LDS
+    constexpr int MID64 = GROUP == 16 ? 8 : 4;
     const int ntb = (m.N + BB - 1) / BB;
     const int rows0 = lane_rows(m, 0);
     int n[kKinds], total = 0, small_to = m.counts ? kSmall : 0;
@@ -730,9 +916,9 @@ __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
         else if (f == 7) run(std::integral_constant<int, 224>{});
         else if (f == 6) run(std::integral_constant<int, 192>{});
         else if (f == 5) run(std::integral_constant<int, 160>{});
-        else if (f > 2) run(std::integral_constant<int, 128>{});
-        else if (f == 2) run(std::integral_constant<int, 64>{});
-        else run(std::integral_constant<int, 32>{});
+        else if (f > 2) w4_mid_tile<GROUP, GATED, 128, 4>(a, at.g, p.m0, p.end, n0, lds);
+        else if (f == 2) w4_mid_tile<GROUP, GATED, 64, MID64>(a, at.g, p.m0, p.end, n0, lds);
+        else w4_mid_tile<GROUP, GATED, 32, 8>(a, at.g, p.m0, p.end, n0, lds);
     }
     if (n[0] > 0) few_rows<GROUP, GATED>(a, lds, rows0, small_to, n[0]);
 }
