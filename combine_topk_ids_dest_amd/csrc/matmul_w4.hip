@@ -691,16 +691,19 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, int g, int m0, int rows
 // a lane has 32 consecutive columns of a pair, 16 bytes of codes and four chunks
 // of x, in two units of 16 columns (one E4M3 scale); under a unit's products the
 // next unit's x is on its way into registers, and behind the barrier the next
-// pair's codes.
+// pair's codes. Bound by the weights' bytes as much as by widening them, so codes
+// come by quads of slabs, 128 bytes of a row at a time (with 64 the loads alone
+// of 8 experts of 115 rows, 7168 -> 2 x 2048, took 59 us, so 52).
 //
-// LDS: a 256-byte row of x holds chunk c at c ^ place_few(r), a 64-byte row of
-// codes at c ^ (-(r / 4) & 3); the sets of 16 lanes of a 16-byte read (see the
-// big tiles) meet on no bank.
+// LDS: a 256-byte row of x holds chunk c at c ^ place_few(r), a 128-byte row of
+// codes at c ^ (r / 2 & 7); the sets of 16 lanes of a 16-byte read (see the big
+// tiles) meet on no bank.
 // ---------------------------------------------------------------------
+constexpr int kQuad = kCols * 128;               // codes of a quad
 template <int BM>
-constexpr int kMidX = 3;                         // pairs of x in LDS
+constexpr int kMidX = BM == 128 ? 2 : 3;         // pairs of x in LDS
 template <int BM>
-constexpr int kMidW = BM == 128 ? 3 : 6;         // and of codes
+constexpr int kMidW = BM == 128 ? 2 : 3;         // and quads of codes
 
 template <int GROUP, bool GATED, int BM, int WN>
 __device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int rows, int n0,
@@ -710,10 +713,9 @@ __device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int 
     constexpr int XS = kMidX<BM>, WS = kMidW<BM>;
     constexpr int PAIR_X = BM * 256;
     constexpr int FX = BM / 16;                   // loads of a wave per pair of x
-    constexpr int AT_W = XS * PAIR_X, AT_S = AT_W + WS * kPairCodes;
-    constexpr int SP = GROUP / 8;                 // pairs under 16 bytes of scales
-    static_assert(AT_S + kScaleSets * kScaleSet <= kLds, "");
-    static_assert((WS + SP - 2) / SP + 1 <= kScaleSets && WS <= 3 * SP + 1, "");
+    constexpr int FW = 9;                         // and per quad of codes and scales
+    constexpr int AT_W = XS * PAIR_X, AT_S = AT_W + WS * kQuad;
+    static_assert(AT_S + WS * kScaleSet <= kLds, "");
     const MatmulArgs& m = a.m;
     const int lane = threadIdx.x & 63;
     const int wave = uniform(threadIdx.x >> 6);
@@ -731,8 +733,8 @@ __device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int 
                                (int64_t)(nw - 1) * a.s_row + (H / GROUP + 15) / 16 * 16);
 
     // Load i of x fills rows (i * 4 + wave) * 4 .. + 3, of codes rows
-    // (i * 4 + wave - 4) * 16 .. + 15 of the tile.
-    const int row = is_x ? wave * 4 + (lane >> 4) : (wave - 4) * 16 + (lane >> 2);
+    // (i * 4 + wave - 4) * 8 .. + 7 of the tile.
+    const int row = is_x ? wave * 4 + (lane >> 4) : (wave - 4) * 8 + (lane >> 3);
     uint32_t at, at_s = kOutside;
     int n = 0, chunk;
     if (is_x) {
@@ -741,36 +743,40 @@ __device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int 
     } else {
         const int srow = wrow<GATED, FRAGS>((wave - 4) * 64 + lane, n0, m.N, n);
         if (n < m.N) at_s = (uint32_t)srow * (uint32_t)a.s_row;
-        chunk = ((lane & 3) ^ (-(row >> 2) & 3)) * 16;
+        chunk = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
         at = (uint32_t)wrow<GATED, FRAGS>(row, n0, m.N, n) * (uint32_t)m.w_row + chunk;
     }
-    constexpr int STEP = GATED ? 32 : 64;         // output columns of 64 rows of w
-    const uint32_t step = is_x ? 16u * (uint32_t)m.x_row : (uint32_t)STEP * (uint32_t)m.w_row;
-    const int have = is_x ? (left - row + 15) / 16 : (m.N - n + STEP - 1) / STEP;
+    // output columns between the first row of w and the row 32 i further
+    auto apart = [](int i) {
+        return (FRAGS == 2 ? i * 32 : (i & 1) * 8 + (i >> 1) * 64) / (GATED ? 2 : 1);
+    };
     auto fetch_x = [&](int p, int stage) {
         const bool in = p * 256 + chunk < m.row_bytes;
         const uint32_t k = 2 * p * kSlab < m.row_bytes ? p * 256 : 0;
 #pragma unroll
         for (int i = 0; i < FX; ++i)
             load_to_lds(rx, lds0 + stage * PAIR_X + (i * 4 + wave) * 1024,
-                        in && i < have ? at + i * step : kOutside, k);
+                        in && row + i * 16 < left ? at + i * 16u * (uint32_t)m.x_row : kOutside,
+                        k);
     };
-    // (codes behind a row's end meet a scale of zero)
-    auto fetch_w = [&](int p, int stage) {
-        const bool any = p < npair;
-        if (p % SP == 0)
-            load_to_lds(rs, lds0 + AT_S + (p / SP) % kScaleSets * kScaleSet + (wave - 4) * 1024,
-                        any ? at_s : kOutside, any ? p / SP * 16 : 0);
-        const uint32_t k = any ? p * 64 : 0;
+    // Half h of quad p: the scales first, then half of the rows' codes (those
+    // behind a row's end meet a scale of zero).
+    auto fetch_w = [&](int p, int h, int stage) {
+        const bool any = 2 * p < npair;
+        if (h == 0)
+            load_to_lds(rs, lds0 + AT_S + stage * kScaleSet + (wave - 4) * 1024,
+                        any ? at_s : kOutside, any ? (GROUP == 16 ? p : p >> 1) * 16 : 0);
+        const uint32_t k = any ? p * 128 : 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            load_to_lds(rw, lds0 + AT_W + stage * kPairCodes + (i * 4 + wave - 4) * 1024,
-                        any && i < have ? at + i * step : kOutside, k);
+        for (int i = 4 * h; i < 4 * h + 4; ++i)
+            load_to_lds(rw, lds0 + AT_W + stage * kQuad + (i * 4 + wave - 4) * 1024,
+                        any && n + apart(i) < m.N ? at + apart(i) * (uint32_t)m.w_row : kOutside,
+                        k);
     };
 
     const int r = lane & 15, q = lane >> 4;
     const int rdx = (wm * (JF * 16) + r) * 256 + ((4 * q) ^ place_few(r)) * 16;
-    const int rdw = AT_W + (wn * (FRAGS * 16) + r) * 64 + (q ^ (-(r >> 2) & 3)) * 16;
+    const int rdw = AT_W + (wn * (FRAGS * 16) + r) * 128 + (q ^ (r >> 1)) * 16;
     const int rds = AT_S + (wn * (FRAGS * 16) + r) * 16 + q * (32 / GROUP);
     f32x4 acc[FRAGS][JF];
 #pragma unroll
@@ -790,12 +796,12 @@ __device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int 
                                                               j * 16 * 256);
     };
     auto read_codes = [&](int to, int p, int stage) {
-        const uint8_t* pw = lds + rdw + stage * kPairCodes;
+        const uint8_t* pw = lds + stage * kQuad;
         const uint8_t* ps =
-            lds + rds + (p / SP) % kScaleSets * kScaleSet + p % SP * (16 / SP);
+            lds + rds + stage * kScaleSet + (GROUP == 16 ? (p & 1) * 8 : (p & 3) * 4);
 #pragma unroll
         for (int i = 0; i < FRAGS; ++i) {
-            c[to][i] = *reinterpret_cast<const u32x4*>(pw + i * 16 * 64);
+            c[to][i] = *reinterpret_cast<const u32x4*>(pw + (rdw ^ ((p & 1) * 64)) + i * 16 * 128);
             sc[to][i] = GROUP == 16 ? *reinterpret_cast<const uint16_t*>(ps + i * 16 * 16)
                                     : ps[i * 16 * 16];
         }
@@ -823,12 +829,15 @@ __device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int 
         wait_and_barrier<(XS - 1) * FX>();
     } else {
 #pragma unroll
-        for (int v = 0; v < WS; ++v) fetch_w(v, v);
-        wait_and_barrier<(WS - 1) * 4>();
+        for (int v = 0; v < WS; ++v) {
+            fetch_w(v, 0, v);
+            fetch_w(v, 1, v);
+        }
+        wait_and_barrier<(WS - 1) * FW>();
     }
     read_codes(0, 0, 0);
     read_x(first, lds);
-    int ix = 0, iw = 0;                           // stages of pair p
+    int ix = 0, iw = 0;                           // stages of pair p and of its quad
     auto one = [&](int p, auto of) {
         constexpr int now = decltype(of)::value;
         // what follows the last scale may be anything
@@ -838,16 +847,20 @@ __device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int 
         read_x(second, lds + ix * PAIR_X);
         __builtin_amdgcn_sched_barrier(0);
         multiply(first, now);
-        // Pair p is read; pair p + 1 (with the scales asked for before it) has
-        // arrived. Behind it are the loads of XS - 2 pairs of x, of WS - 2 of
-        // codes and now and then of scales.
+        // Pair p is read; pair p + 1 (and its quad) has arrived. Behind it are the
+        // loads of XS - 2 pairs of x, of WS - 2 quads of codes.
         if (is_x) wait_and_barrier<(XS - 2) * FX>();
-        else wait_and_barrier<(WS - 2) * 4>();
-        const int nix = ix + 1 < XS ? ix + 1 : 0, niw = iw + 1 < WS ? iw + 1 : 0;
+        else if (now == 1) wait_and_barrier<(WS - 2) * FW>();
+        else asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        const int nix = ix + 1 < XS ? ix + 1 : 0;
+        const int niw = now == 0 ? iw : iw + 1 < WS ? iw + 1 : 0;
         read_codes(1 - now, p + 1, niw);
         read_x(first, lds + nix * PAIR_X);
+        // a quad's codes are all read before its second pair's barrier: from
+        // there on its place is filled again, half of it at a time
         if (is_x) fetch_x(p + XS, ix);
-        else fetch_w(p + WS, iw);
+        else if (now == 1) fetch_w((p >> 1) + WS, 0, iw);
+        else if (p > 0) fetch_w((p >> 1) + WS - 1, 1, iw == 0 ? WS - 1 : iw - 1);
         __builtin_amdgcn_sched_barrier(0);
         multiply(second, now);
         ix = nix;
