@@ -38,6 +38,15 @@ __device__ __forceinline__ u32x4 widen4(uint32_t c, float s) {
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
 }
 
+// The lane, made anew for each tile: what is derived from it would otherwise be
+// held in registers over all kinds of tiles, spilled, and loaded back in their
+// loops, each time behind all loads in flight.
+__device__ __forceinline__ int tile_lane() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // A scale from its code.
 template <int GROUP>
 __device__ __forceinline__ float scale_of(uint32_t code) {
@@ -121,7 +130,7 @@ __device__ __forceinline__ FewTile few_setup(const W4Args& a, int g, int m0, int
                                              int lw) {
     const MatmulArgs& m = a.m;
     constexpr int BO = GATED ? kSmall / 2 : kSmall;
-    const int lane = threadIdx.x & 63;
+    const int lane = tile_lane();
     const int H = m.row_bytes / 2;
     const int nw = GATED ? 2 * m.N : m.N;
     const int wave = uniform(threadIdx.x >> 6), wn = wave & ((1 << lw) - 1);
@@ -164,7 +173,7 @@ template <int GROUP, bool GATED, class Next>
 __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int total,
                                           const Next& place) {
     const MatmulArgs& m = a.m;
-    const int lane = threadIdx.x & 63;
+    const int lane = tile_lane();
     const int wave = uniform(threadIdx.x >> 6);
     const int H = m.row_bytes / 2;
     const uint32_t lds0 = uniform((int)(uint32_t)(uintptr_t)(lds_byte*)lds);
@@ -532,7 +541,7 @@ __device__ __forceinline__ void w4_tile(const W4Args& a, int g, int m0, int rows
     static_assert(AT_S + kScaleSets * kScaleSet <= kLds, "");
     static_assert((WS + SP - 2) / SP + 1 <= kScaleSets, "");
     const MatmulArgs& m = a.m;
-    const int lane = threadIdx.x & 63;
+    const int lane = tile_lane();
     const int wave = uniform(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const bool is_x = wave < 4;
@@ -717,7 +726,7 @@ __device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int 
     constexpr int AT_W = XS * PAIR_X, AT_S = AT_W + WS * kQuad;
     static_assert(AT_S + WS * kScaleSet <= kLds, "");
     const MatmulArgs& m = a.m;
-    const int lane = threadIdx.x & 63;
+    const int lane = tile_lane();
     const int wave = uniform(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
     const bool is_x = wave < 4;
