@@ -406,8 +406,14 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
     finish(old, odd ^ 1);
 }
 
-// The cut of `runs` runs of up to 16 rows, of least rounds times a tile's time, by
-// its bytes and about 2048 columns' worth of start and end. least: lw for runs
+// A cut's rounds times a tile's time, in columns of 16 rows of w: a tile's own and
+// about 2048 for its start and end.
+__host__ __device__ __forceinline__ float few_columns(const FewCut& c, int H) {
+    return (float)(c.whole / kGrid) * (float)((H << c.lw) + 2048) +
+           (c.total > c.whole ? (float)((H << c.last) + 2048) : 0.f);
+}
+
+// The cut of `runs` runs of up to 16 rows that takes least. least: lw for runs
 // of more than 8 rows (a step of 2048 columns of 16 rows is no segment).
 __host__ __device__ __forceinline__ FewCut few_cut(int runs, int N, int H, int bo, int least) {
     FewCut best = {};
@@ -420,14 +426,31 @@ __host__ __device__ __forceinline__ FewCut few_cut(int runs, int N, int H, int b
         const int whole = tiles / kGrid * kGrid, rest = tiles - whole;
         int split = rest * 8 <= kGrid ? 3 : rest * 4 <= kGrid ? 2 : rest * 2 <= kGrid ? 1 : 0;
         if (split > lw - least) split = lw - least;
-        const float cost = (float)(whole / kGrid) * (float)((H << lw) + 2048) +
-                           (rest ? (float)((H << (lw - split)) + 2048) : 0.f);
+        const FewCut c = {lw, lw - split, nt, whole, whole + (rest << split)};
+        const float cost = few_columns(c, H);
         if (lw == 3 || cost < best_cost) {
             best_cost = cost;
-            best = FewCut{lw, lw - split, nt, whole, whole + (rest << split)};
+            best = c;
         }
     }
     return best;
+}
+
+// What a product takes with tiles of a few rows, in us, and with big ones (`turns`
+// whole rounds of the grid of `rows` rows each, then one of `last`; 0: none), from
+// measured times. Both sides where the choice turns, in us, few and big: 7168 ->
+// 2 x 2048, E4M3, 64 rows 23 and 57, 256 rows 65 and 73, 512 rows 125 and 73;
+// 2048 -> 7168, 96 rows 22 and 22, 128 rows 26 and 22.
+__host__ __device__ __forceinline__ float few_time(const FewCut& c, int H, int group) {
+    return 6.f + few_columns(c, H) * (group == 16 ? 16.f / 29300.f : 16.f / 39000.f);
+}
+
+__host__ __device__ __forceinline__ float big_time(int turns, int rows, int last, int H,
+                                                   int group) {
+    const float pairs = (float)((H + 127) / 128);
+    const float start = group == 16 ? 0.55f : 0.4f, row = group == 16 ? 0.0135f : 0.0125f;
+    return 8.f + (float)turns * pairs * (start + row * (float)rows) +
+           (last ? pairs * (start + row * (float)last) : 0.f);
 }
 
 template <int GROUP, bool GATED>
@@ -909,9 +932,27 @@ __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
             n[k] *= ntb;
             total += n[k];
         }
-        // a few rows beside so much else: in part-filled tiles
-        if (!small_to || total <= kGrid) break;
-        small_to = 0;
+        if (!small_to || small_to == INT32_MAX) break;
+        if (total > kGrid) {
+            // a few rows beside so much else: in part-filled tiles
+            small_to = 0;
+            continue;
+        }
+        if (total == 0) break;
+        // one round of big tiles, in parts of these rows, or few-row tiles for all
+        int most = 0, runs = 0;
+#pragma unroll
+        for (int k = 1; k < kKinds; ++k)
+            if (n[k]) most = k;
+        const int cut = last_parts(total);
+        for (int g0 = 0; g0 < m.groups; g0 += 64)
+            runs += __builtin_amdgcn_readlane(
+                wave_inclusive_scan(runs_of(g0 ? lane_rows(m, g0) : rows0, INT32_MAX, 0)), 63);
+        const int H = m.row_bytes / 2;
+        if (few_time(few_cut(runs, m.N, H, GATED ? kSmall / 2 : kSmall, 1), H, GROUP) >=
+            big_time(0, 0, (most + cut - 1) / cut * 32, H, GROUP))
+            break;
+        small_to = INT32_MAX;
     }
     const int parts = last_parts(total);
     for (int t0 = 0; t0 < total; t0 += kGrid) {
@@ -947,13 +988,22 @@ __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
 
 template <int GROUP, bool GATED>
 hipError_t launch(const W4Args& a, hipStream_t st) {
-    if (a.m.rows <= 2 * kSmall) {
-        W4Args b = a;
-        b.cut = few_cut((a.m.rows + kSmall - 1) / kSmall, a.m.N, a.m.row_bytes / 2,
-                        GATED ? kSmall / 2 : kSmall, a.m.rows > 8 ? 1 : 0);
-        w4_few_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(b);
-    } else
-        w4_big_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(a);
+    const MatmulArgs& m = a.m;
+    const int H = m.row_bytes / 2;
+    bool few = m.rows <= 2 * kSmall;
+    W4Args b = a;
+    if (!m.counts) {
+        b.cut = few_cut((m.rows + kSmall - 1) / kSmall, m.N, H, GATED ? kSmall / 2 : kSmall,
+                        m.rows > 8 ? 1 : 0);
+        const Cut c = cut_rows(m.rows, 0);
+        const int tiles = c.runs * ((m.N * (GATED ? 2 : 1) + kCols - 1) / kCols);
+        const int rest = tiles % kGrid, parts = last_parts(tiles);
+        few = few_time(b.cut, H, GROUP) <
+              big_time(tiles / kGrid, c.kind * 32, rest ? (c.kind + parts - 1) / parts * 32 : 0, H,
+                       GROUP);
+    }
+    if (few) w4_few_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(b);
+    else w4_big_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(b);
     return hipGetLastError();
 }
 
