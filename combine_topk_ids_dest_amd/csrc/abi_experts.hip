@@ -474,8 +474,9 @@ int moe_ep_route_backward(const void* logits, int64_t logits_stride, int32_t dty
     a.grad = static_cast<uint8_t*>(grad_logits);
     a.grad_stride = grad_stride * gb;
     a.grad_bf16 = grad_dtype == MOE_EP_BF16;
-    // blocks of four waves of up to eight tokens at once
-    a.tile = 32;
+    // blocks of four waves: a token each where there are few, up to eight
+    const int64_t per = (T + 2047) / 2048;
+    a.tile = per <= 4 ? 4 : per >= 32 ? 32 : (per + 3) / 4 * 4;
     return hip_status(launch_route_backward(a, static_cast<hipStream_t>(stream)));
 }
 

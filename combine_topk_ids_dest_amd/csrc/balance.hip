@@ -27,7 +27,7 @@ const float kNothing = -__builtin_huge_valf();
 // Tokens that a wave has at once, so that their loads and their sums over lanes
 // (chains of dependent steps) run side by side.
 template <int V>
-constexpr int kAtOnce = V >= 16 ? 2 : V >= 8 ? 4 : 8;
+constexpr int kAtOnce = V >= 16 ? 2 : 4;
 
 // v of the lane that CTRL names (`none` where there is none, or in the rows
 // that ROWS leaves out).
@@ -71,11 +71,41 @@ __device__ __forceinline__ double wave_sum(double v) {
 
 // A logit as the scores take it: -inf for one that belongs to no expert (-inf
 // or NaN), the largest fp32 for +inf.
-__device__ __forceinline__ float load_logit(const uint8_t* row, bool bf16, int e) {
-    const float x =
-        bf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16)
-             : reinterpret_cast<const float*>(row)[e];
+__device__ __forceinline__ float clean(float x) {
     return x > kNothing ? fminf(x, kLargest) : kNothing;
+}
+
+__device__ __forceinline__ float load_logit(const uint8_t* row, bool bf16, int e) {
+    return clean(bf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16)
+                      : reinterpret_cast<const float*>(row)[e]);
+}
+
+// The logits of B tokens, number b at row(b): one branch for the type, so that
+// all loads are on their way together.
+template <int B, int V, class Row>
+__device__ __forceinline__ void load_tokens(const Row& row, bool bf16, int E, int lane,
+                                            float (&x)[B][V]) {
+    auto each = [&](auto value) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const uint8_t* p = row(b);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane + 64 * i;
+                x[b][i] = value(p, e < E ? e : 0);
+            }
+        }
+    };
+    if (bf16)
+        each([](const uint8_t* p, int e) {
+            return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << 16);
+        });
+    else
+        each([](const uint8_t* p, int e) { return reinterpret_cast<const float*>(p)[e]; });
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[b][i] = lane + 64 * i < E ? clean(x[b][i]) : kNothing;
 }
 
 // The hardware's 2^x, within a place. v's rounding times log2 e, half a place
@@ -214,15 +244,15 @@ __global__ __launch_bounds__(kTokenThreads) void balance_kernel(const BalanceArg
 #pragma unroll
             for (int b = 0; b < B; ++b) {        // behind the last token: that one again
                 const int64_t u = t + b * kTokenWaves < hi ? t + b * kTokenWaves : hi - 1;
-                id[b] = lane < a.K ? a.ids[u * a.K + lane] : -1;
-                const uint8_t* row = a.logits + u * a.logits_stride;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const int e = lane + 64 * i;
-                    x[b][i] = load_logit(row, a.bf16, e < a.E ? e : 0);
-                    if (e >= a.E) x[b][i] = kNothing;
-                }
+                id[b] = a.ids[u * a.K + (lane < a.K ? lane : 0)];
+                if (lane >= a.K) id[b] = -1;
             }
+            load_tokens<B, V>(
+                [&](int b) {
+                    const int64_t u = t + b * kTokenWaves < hi ? t + b * kTokenWaves : hi - 1;
+                    return a.logits + u * a.logits_stride;
+                },
+                a.bf16, a.E, lane, x);
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 const bool pick = id[b] >= 0 && id[b] < a.E && t + b * kTokenWaves < hi;
@@ -378,16 +408,11 @@ __global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const R
         float g = 0.f;
         if (pick && a.grad_weights) g = a.grad_weights[tp * a.K + pk];
         float q[B][V], rest[B][SIGMOID ? V : 1], xs[B][V];
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const uint8_t* row = a.logits + (t + b < t1 ? t + b : t1 - 1) * a.logits_stride;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane + 64 * i;
-                xs[b][i] = load_logit(row, a.bf16, e < a.E ? e : 0);
-                if (e >= a.E) xs[b][i] = kNothing;
-            }
-        }
+        load_tokens<B, V>(
+            [&](int b) {
+                return a.logits + (t + b < t1 ? t + b : t1 - 1) * a.logits_stride;
+            },
+            a.bf16, a.E, lane, xs);
         float xp = kNothing;
         if (pick) xp = load_logit(a.logits + tp * a.logits_stride, a.bf16, id);
         const uint64_t picks = __ballot(pick);
@@ -495,14 +520,17 @@ __global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const R
                         if (e >> 6 == i) dx[i] += v;
                 }
             uint8_t* out = a.grad + (t + b) * a.grad_stride;
+            if (a.grad_bf16) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane + 64 * i;
-                if (e >= a.E) continue;
-                if (a.grad_bf16)
-                    reinterpret_cast<uint16_t*>(out)[e] = (uint16_t)to_bf16_rne(dx[i]);
-                else
-                    reinterpret_cast<float*>(out)[e] = dx[i];
+                for (int i = 0; i < V; ++i)
+                    if (lane + 64 * i < a.E)
+                        reinterpret_cast<uint16_t*>(out)[lane + 64 * i] =
+                            (uint16_t)to_bf16_rne(dx[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (lane + 64 * i < a.E)
+                        reinterpret_cast<float*>(out)[lane + 64 * i] = dx[i];
             }
         }
     }
@@ -551,9 +579,11 @@ hipError_t launch_route_backward(const RouteGradArgs& a, hipStream_t st) {
                 <<<grid, kGradWaves * 64, 0, st>>>(a);
         };
         auto by_picks = [&](auto sigmoid) {
-            if (a.K <= 8) run(sigmoid, std::integral_constant<int, 8>{});
-            else if (a.K <= 16) run(sigmoid, std::integral_constant<int, 16>{});
-            else run(sigmoid, std::integral_constant<int, 64>{});
+            // few tokens: one a wave, over more of the CUs (256 experts, 8 picks:
+            // 8192 tokens 12.5 us, 20 with eight a wave; 65536 tokens 62 and 51)
+            if (a.T <= 16384 || a.K > 16) run(sigmoid, std::integral_constant<int, 64>{});
+            else if (a.K <= 8) run(sigmoid, std::integral_constant<int, 8>{});
+            else run(sigmoid, std::integral_constant<int, 16>{});
         };
         if (a.score == MOE_EP_SIGMOID) by_picks(std::true_type{});
         else by_picks(std::false_type{});
