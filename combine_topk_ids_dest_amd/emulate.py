@@ -31,6 +31,9 @@ expert that every token passes through is added to out behind the unpack:
   hidden          [e_local, W*cap, I]      a lane's expert rows between their
                                            two products (fp8: codes + scales)
   shared          [T, I_shared]            a lane's, the same for that expert
+and where the router is trained (balance), of each source rank's picks
+  counts, mean    [W_src, 1, E]            int32 / fp32
+  tokens, loss    [W_src, 1]               int32 / fp32
 
 Lanes: rank i uses lane i % lanes for the buffers that ranks share (the
 workspace, b and Y), so no two lanes read or write the same expert rows. With several lanes, step(streams=...) runs the ranks of
@@ -181,7 +184,10 @@ class LogicalEP:
                   w2_scale: Optional[torch.Tensor] = None,
                   gate: Optional[torch.Tensor] = None, route: Optional[dict] = None,
                   shared13: Optional[torch.Tensor] = None,
-                  shared2: Optional[torch.Tensor] = None):
+                  shared2: Optional[torch.Tensor] = None,
+                  w4_group: Optional[int] = None,
+                  w13_global: Optional[torch.Tensor] = None,
+                  w2_global: Optional[torch.Tensor] = None, balance: bool = False):
         """The weights of a layer whose step() then runs whole.
 
         w13 [E, 2I, H] (gate rows, then up rows), w2 [E, H, I]: every rank's
@@ -190,11 +196,16 @@ class LogicalEP:
         [E, 2 ceil(I/128), H/128] and w2_scale [E, ceil(H/128), I/128]
         (copied here if a rank's experts do not start on a 16-byte boundary
         in them; an expert stride of a multiple of 4 saves that).
+        w4_group (16 or 32), with bf16 rows: w13 [E, 2I, H/2] and w2 [E, H, I/2]
+        are packed E2M1 codes, w13_scale and w2_scale [E, ., w4_scale_pitch(., w4_group)]
+        their scales as moe_ep_expert_matmul_w4 takes them, w13_global [E, 2] and
+        w2_global [E, 1] (fp32) factors over each expert's matrices.
         gate: bf16 [E, H], the router (without it the ids and weights of
         set_source stand); route: further arguments of moe_ep_route_topk
         (score, bias, n_group, topk_group, renormalize, scale). shared13
         [2S, H], shared2 [H, S]: bf16, the expert that every token passes
-        through.
+        through. balance: each rank's step also leaves its picks' counts, mean
+        scores and balance loss (balance_terms); needs the gate.
 
         A new layer ends the graphs of capture_lane_graphs: they read and
         write the buffers of the layer that they were captured with. So do
@@ -208,18 +219,26 @@ class LogicalEP:
         if w13.dim() != 3 or w13.size(0) != self.E or w13.size(1) % 2:
             raise ValueError("w13 must be [E, 2I, H]")
         inter = w13.size(1) // 2
-        if tuple(w13.shape) != (self.E, 2 * inter, self.H) or \
+        w4 = w4_group is not None
+        if w4:
+            self._check_w4(w13, w2, w13_scale, w2_scale, w13_global, w2_global, w4_group, inter)
+        elif tuple(w13.shape) != (self.E, 2 * inter, self.H) or \
                 tuple(w2.shape) != (self.E, self.H, inter):
             raise ValueError("w13 must be [E, 2I, H] and w2 [E, H, I]")
-        if fp8 != (w13_scale is not None) or fp8 != (w2_scale is not None):
+        elif w13_global is not None or w2_global is not None:
+            raise ValueError("factors over a matrix go with 4-bit weights")
+        if not w4 and (fp8 != (w13_scale is not None) or fp8 != (w2_scale is not None)):
             raise ValueError("block scales go with rows that the pack quantises")
+        if balance and gate is None:
+            raise ValueError("the balance loss is that of the router: it needs the gate")
         if (shared13 is None) != (shared2 is None):
             raise ValueError("shared13 and shared2 go together")
         if fp8:
             w13_scale, w2_scale = self._aligned_scales(w13_scale), self._aligned_scales(w2_scale)
         el, ecap, dev = self.e_local, self.expert_cap, self.device
         layer = dict(w13=w13, w2=w2, w13_scale=w13_scale, w2_scale=w2_scale, gate=gate,
-                     route=dict(route or {}), shared13=shared13, shared2=shared2)
+                     route=dict(route or {}), shared13=shared13, shared2=shared2,
+                     w4_group=w4_group, w13_global=w13_global, w2_global=w2_global)
         if fp8:
             layer["hidden"] = [
                 (torch.empty((el, ecap, inter), dtype=torch.uint8, device=dev),
@@ -230,6 +249,16 @@ class LogicalEP:
                                for _ in range(self.lanes)]
         if gate is not None:
             layer["logits"] = torch.empty((self.W, self.T, self.E), device=dev)
+        if balance:
+            W, E = self.W, self.E
+            size = max(16, B.moe_ep_balance_workspace_bytes(self.T, E))
+            layer["balance"] = dict(
+                counts=torch.zeros((W, 1, E), dtype=torch.int32, device=dev),
+                tokens=torch.zeros((W, 1), dtype=torch.int32, device=dev),
+                mean_score=torch.zeros((W, 1, E), device=dev),
+                loss=torch.zeros((W, 1), device=dev))
+            layer["balance_workspaces"] = [torch.empty(size, dtype=torch.uint8, device=dev)
+                                           for _ in range(self.lanes)]
         if shared13 is not None:
             layer["shared"] = [torch.empty((self.T, shared13.size(0) // 2),
                                            dtype=torch.bfloat16, device=dev)
@@ -237,6 +266,21 @@ class LogicalEP:
         self._layer = layer
         self._calls = {}
         self._lane_graphs = None
+
+    def _check_w4(self, w13, w2, w13_scale, w2_scale, w13_global, w2_global, group, inter):
+        if self.quant_group is not None:
+            raise ValueError("4-bit weights go with bf16 rows")
+        if group not in (16, 32) or self.H % 32 or inter % 32:
+            raise ValueError("w4_group must be 16 or 32, H and I multiples of 32")
+        for w, scale, whole, rows, cols, halves in (
+                (w13, w13_scale, w13_global, 2 * inter, self.H, 2),
+                (w2, w2_scale, w2_global, self.H, inter, 1)):
+            if tuple(w.shape) != (self.E, rows, cols // 2):
+                raise ValueError("4-bit w13 must be [E, 2I, H/2] and w2 [E, H, I/2]")
+            if scale is None or tuple(scale.shape) != (self.E, rows, B.w4_scale_pitch(cols, group)):
+                raise ValueError("4-bit weights need scales [E, ., w4_scale_pitch(., w4_group)]")
+            if whole is not None and tuple(whole.shape) != (self.E, halves):
+                raise ValueError("w13_global must be [E, 2] and w2_global [E, 1]")
 
     def _aligned_scales(self, scale: torch.Tensor) -> torch.Tensor:
         """scale [E, ., .] itself if every rank's experts start on a 16-byte
@@ -257,11 +301,26 @@ class LogicalEP:
         return (B.prepare_matmul(self._source_rows(s), y["gate"], y["logits"][s]),
                 B.prepare_route_topk(y["logits"][s], self.ids[s], self.wts[s], **y["route"]))
 
+    def _prep_balance(self, s: int):
+        y = self._layer
+        t = self.balance_terms(s)
+        return B.prepare_balance_loss(y["logits"][s], self.ids[s], t["counts"], t["tokens"],
+                                      t["mean_score"], t["loss"],
+                                      y["balance_workspaces"][s % self.lanes],
+                                      y["route"].get("score", "softmax"))
+
     def _prep_experts(self, r: int):
         y, lane = self._layer, r % self.lanes
         mine = slice(r * self.e_local, (r + 1) * self.e_local)
         w13, w2, cnt = y["w13"][mine], y["w2"][mine], self.expert_num_tokens[r]
         b, Y, h = self.b_lanes[lane], self.Y_lanes[lane], y["hidden"][lane]
+        if y["w4_group"] is not None:
+            f13, f2 = (None if f is None else f[mine] for f in (y["w13_global"], y["w2_global"]))
+            return (B.prepare_expert_matmul_w4(b[0].view(torch.bfloat16), w13,
+                                               y["w13_scale"][mine], cnt, h, y["w4_group"],
+                                               "silu_gated", w_global=f13),
+                    B.prepare_expert_matmul_w4(h, w2, y["w2_scale"][mine], cnt, Y, y["w4_group"],
+                                               w_global=f2))
         if self.quant_group is None:
             return (B.prepare_expert_matmul(b[0].view(torch.bfloat16), w13, cnt, h, "silu_gated"),
                     B.prepare_expert_matmul(h, w2, cnt, Y))
@@ -280,6 +339,32 @@ class LogicalEP:
         """The router of source rank s: its rows' logits, then ids and wts."""
         for call in self._prepared("route", s):
             call(stream)
+
+    def balance_terms(self, s: int) -> dict:
+        """Source rank s's counts [1, E], tokens [1], mean_score [1, E] and loss
+        [1] of a layer with balance, as the last step left them."""
+        if self._layer is None or "balance" not in self._layer:
+            raise ValueError("the layer has no balance loss: set_layer(..., balance=True)")
+        return {k: v[s] for k, v in self._layer["balance"].items()}
+
+    def balance(self, s: int, stream=None):
+        """Counts, mean scores and balance loss of source rank s's picks."""
+        self._prepared("balance", s)(stream)
+
+    def router_grad(self, s: int, grad_logits: torch.Tensor,
+                    grad_weights: Optional[torch.Tensor] = None,
+                    grad_loss: Optional[torch.Tensor] = None, stream=None):
+        """The gradient of source rank s's logits behind a step: grad_logits
+        [T, E], from the gradient of its wts [T, K] and, with balance, of its
+        loss [1]."""
+        y = self._layer
+        if y is None or y["gate"] is None:
+            raise ValueError("the layer has no router")
+        t = self.balance_terms(s) if grad_loss is not None else {}
+        kw = {k: y["route"][k] for k in ("score", "renormalize", "scale") if k in y["route"]}
+        B.moe_ep_route_backward(y["logits"][s], self.ids[s], grad_logits, grad_weights=grad_weights,
+                                grad_loss=grad_loss, counts=t.get("counts"),
+                                tokens=t.get("tokens"), stream=stream, **kw)
 
     def experts(self, r: int, stream=None):
         """The experts of destination rank r, from its lane's batched rows to
@@ -301,6 +386,8 @@ class LogicalEP:
     def _send(self, s: int, stream=None):
         if self._layer is not None and self._layer["gate"] is not None:
             self.route(s, stream)
+            if "balance" in self._layer:
+                self.balance(s, stream)
         self.pack(s, stream)
 
     def _serve(self, r: int, fused_local: bool, stream=None):
