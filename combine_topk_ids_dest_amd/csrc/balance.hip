@@ -226,9 +226,8 @@ __global__ __launch_bounds__(kTokenThreads) void balance_kernel(const BalanceArg
         for (int s = threadIdx.x; s < a.S; s += kTokenThreads) a.ticket[s] = 0;
     const int64_t t0 = TILES ? (int64_t)blockIdx.x * a.tile : 0;
     const int64_t t1 = TILES ? (t0 + a.tile < a.T ? t0 + a.tile : a.T) : a.T;
-    for (int s = TILES ? first_behind(a.start, a.S, a.T, t0) : (int)blockIdx.x;;
-         ++s) {
-        if (s >= a.S) break;
+    for (int s = TILES ? first_behind(a.start, a.S, a.T, t0) : (int)blockIdx.x; s < a.S;
+         s += TILES ? 1 : (int)gridDim.x) {
         const Span span = span_of(a.start, a.T, s);
         if (TILES && span.lo >= t1) break;
         const int64_t lo = span.lo > t0 ? span.lo : t0, hi = span.hi < t1 ? span.hi : t1;
@@ -286,7 +285,7 @@ __global__ __launch_bounds__(kTokenThreads) void balance_kernel(const BalanceArg
         const int32_t count = e < a.E ? hist[e] : 0;
         if (!TILES) {
             finish_sequence(a, s, count, (double)score, all, sums);
-            break;
+            continue;                            // behind a barrier that all have passed
         }
         const int64_t slot = (int64_t)blockIdx.x + s;
         if (e < a.E) {
@@ -309,73 +308,77 @@ __global__ __launch_bounds__(kTokenThreads) void balance_join_kernel(const Balan
     constexpr int U = 16;                        // loads on their way
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
-    const int s = blockIdx.y, slices = gridDim.x;
-    const int e = blockIdx.x * 64 + lane;
-    const int col = e < a.E ? e : a.E - 1;
-    const Span span = span_of(a.start, a.T, s);
-    const bool any = span.hi > span.lo;
-    const int64_t first = span.lo / a.tile + s;  // slots [first, end)
-    const int64_t end = any ? (span.hi - 1) / a.tile + 1 + s : first;
-    int32_t count = 0;
-    double score = 0.0;
-    for (int64_t b = first + wave; b < end; b += kTokenWaves * U) {
-        int32_t c[U];
-        float v[U];
+    const int slices = (a.E + 63) / 64;
+    for (int64_t u = blockIdx.x; u < (int64_t)a.S * slices; u += gridDim.x) {
+        const int s = (int)(u / slices), slice = (int)(u % slices);
+        const int e = slice * 64 + lane;
+        const int col = e < a.E ? e : a.E - 1;
+        const Span span = span_of(a.start, a.T, s);
+        const bool any = span.hi > span.lo;
+        const int64_t first = span.lo / a.tile + s;      // slots [first, end)
+        const int64_t end = any ? (span.hi - 1) / a.tile + 1 + s : first;
+        int32_t count = 0;
+        double score = 0.0;
+        for (int64_t b = first + wave; b < end; b += kTokenWaves * U) {
+            int32_t c[U];
+            float v[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int64_t slot = b + i * kTokenWaves < end ? b + i * kTokenWaves : end - 1;
-            c[i] = a.slot_count[slot * a.E + col];
-            v[i] = a.slot_score[slot * a.E + col];
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-            if (b + i * kTokenWaves < end) {
-                count += c[i];
-                score += (double)v[i];
+            for (int i = 0; i < U; ++i) {
+                const int64_t slot = b + i * kTokenWaves < end ? b + i * kTokenWaves : end - 1;
+                c[i] = a.slot_count[slot * a.E + col];
+                v[i] = a.slot_score[slot * a.E + col];
             }
-    }
-    scores_of[wave][lane] = score;
-    counts_of[wave][lane] = count;
-    __syncthreads();
-    if (wave != 0) return;
-    double n = 0.0;
-    for (int64_t b = first + lane; b < end; b += 64) n += (double)a.slot_tokens[b];
-    n = wave_sum(n);
-    for (int w = 1; w < kTokenWaves; ++w) {
-        score += scores_of[w][lane];
-        count += counts_of[w][lane];
-    }
-    const double mean = n > 0.0 ? score / n : 0.0;
-    if (e < a.E) {
-        a.counts[(int64_t)s * a.E + e] = count;
-        a.mean[(int64_t)s * a.E + e] = (float)mean;
-    }
-    double picks = wave_sum(e < a.E ? (double)count : 0.0);
-    double both = wave_sum(e < a.E ? (double)count * mean : 0.0);
-    if (slices > 1) {
-        double* const parts = a.part + (int64_t)s * slices * 2;
-        int before = 0;
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (b + i * kTokenWaves < end) {
+                    count += c[i];
+                    score += (double)v[i];
+                }
+        }
+        __syncthreads();                         // the sums before are read
+        scores_of[wave][lane] = score;
+        counts_of[wave][lane] = count;
+        __syncthreads();
+        if (wave != 0) continue;
+        double n = 0.0;
+        for (int64_t b = first + lane; b < end; b += 64) n += (double)a.slot_tokens[b];
+        n = wave_sum(n);
+        for (int w = 1; w < kTokenWaves; ++w) {
+            score += scores_of[w][lane];
+            count += counts_of[w][lane];
+        }
+        const double mean = n > 0.0 ? score / n : 0.0;
+        if (e < a.E) {
+            a.counts[(int64_t)s * a.E + e] = count;
+            a.mean[(int64_t)s * a.E + e] = (float)mean;
+        }
+        double picks = wave_sum(e < a.E ? (double)count : 0.0);
+        double both = wave_sum(e < a.E ? (double)count * mean : 0.0);
+        if (slices > 1) {
+            double* const parts = a.part + (int64_t)s * slices * 2;
+            int before = 0;
+            if (lane == 0) {
+                __hip_atomic_store(parts + 2 * slice, picks, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(parts + 2 * slice + 1, both, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+                before = __hip_atomic_fetch_add(a.ticket + s, 1, __ATOMIC_ACQ_REL,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+            }
+            if (__builtin_amdgcn_readfirstlane(before) != slices - 1) continue;
+            picks = both = 0.0;
+            if (lane == 0)
+                for (int i = 0; i < slices; ++i) {
+                    picks += __hip_atomic_load(parts + 2 * i, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+                    both += __hip_atomic_load(parts + 2 * i + 1, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+                }
+        }
         if (lane == 0) {
-            __hip_atomic_store(parts + 2 * blockIdx.x, picks, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-            __hip_atomic_store(parts + 2 * blockIdx.x + 1, both, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-            before = __hip_atomic_fetch_add(a.ticket + s, 1, __ATOMIC_ACQ_REL,
-                                            __HIP_MEMORY_SCOPE_AGENT);
+            a.tokens[s] = (int32_t)n;
+            a.loss[s] = (float)(picks > 0.0 ? (double)a.E * both / picks : 0.0);
         }
-        if (__builtin_amdgcn_readfirstlane(before) != slices - 1) return;
-        picks = both = 0.0;
-        if (lane == 0)
-            for (int i = 0; i < slices; ++i) {
-                picks += __hip_atomic_load(parts + 2 * i, __ATOMIC_RELAXED,
-                                           __HIP_MEMORY_SCOPE_AGENT);
-                both += __hip_atomic_load(parts + 2 * i + 1, __ATOMIC_RELAXED,
-                                          __HIP_MEMORY_SCOPE_AGENT);
-            }
-    }
-    if (lane == 0) {
-        a.tokens[s] = (int32_t)n;
-        a.loss[s] = (float)(picks > 0.0 ? (double)a.E * both / picks : 0.0);
     }
 }
 
@@ -551,7 +554,9 @@ hipError_t by_width(int E, F&& f) {
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
     const size_t lds = (size_t)(kTokenWaves / 2 + 1) * a.E * 4;
     const bool tiles = a.slot_count != nullptr;
-    const unsigned grid = tiles ? (unsigned)((a.T + a.tile - 1) / a.tile) : (unsigned)a.S;
+    // a grid has fewer than 2^32 threads: blocks stride over many sequences
+    auto at_most = [](int64_t n) { return (unsigned)(n < 1 << 20 ? n : 1 << 20); };
+    const unsigned grid = tiles ? (unsigned)((a.T + a.tile - 1) / a.tile) : at_most(a.S);
     const hipError_t rc = by_width(a.E, [&](auto v) {
         constexpr int V = decltype(v)::value;
         auto run = [&](auto sigmoid) {
@@ -565,8 +570,7 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t st) {
         else run(std::false_type{});
     });
     if (rc != hipSuccess || !tiles) return rc;
-    balance_join_kernel<<<dim3((unsigned)((a.E + 63) / 64), (unsigned)a.S), kTokenThreads, 0,
-                          st>>>(a);
+    balance_join_kernel<<<at_most((int64_t)a.S * ((a.E + 63) / 64)), kTokenThreads, 0, st>>>(a);
     return hipGetLastError();
 }
 

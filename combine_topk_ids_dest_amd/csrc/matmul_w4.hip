@@ -304,25 +304,25 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
                 uint32_t sc[4];
                 if (k < H) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    c[h] = *reinterpret_cast<const u32x4*>(p + r * 128 +
-                                                           (((q + 4 * h) ^ (r >> 1)) & 7) * 16);
-                    const uint8_t* ps = p + 2048 + r * (256 / GROUP) + h * (128 / GROUP);
-                    if (SPLIT) {
-                        const u32x2 v = *reinterpret_cast<const u32x2*>(ps);
-                        sc[2 * h] = v[0];
-                        sc[2 * h + 1] = v[1];
-                    } else {
-                        sc[2 * h] = GROUP == 32 ? ps[q]
-                                                : *reinterpret_cast<const uint16_t*>(ps + q * 2);
+                    for (int h = 0; h < 2; ++h) {
+                        c[h] = *reinterpret_cast<const u32x4*>(p + r * 128 +
+                                                               (((q + 4 * h) ^ (r >> 1)) & 7) * 16);
+                        const uint8_t* ps = p + 2048 + r * (256 / GROUP) + h * (128 / GROUP);
+                        if (SPLIT) {
+                            const u32x2 v = *reinterpret_cast<const u32x2*>(ps);
+                            sc[2 * h] = v[0];
+                            sc[2 * h + 1] = v[1];
+                        } else {
+                            sc[2 * h] = GROUP == 32 ? ps[q]
+                                                    : *reinterpret_cast<const uint16_t*>(ps + q * 2);
+                        }
                     }
-                }
-                const uint32_t at_x = (uint32_t)((to ^ 1) * kSegment) +
-                                      ((uint32_t)((in_segment << lk) + wk) << (9 + cur.lx));
+                    const uint32_t at_x = (uint32_t)((to ^ 1) * kSegment) +
+                                          ((uint32_t)((in_segment << lk) + wk) << (9 + cur.lx));
 #pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    x[t] = *reinterpret_cast<const u32x4*>(lds + kFewX + from[t & 3] +
-                                                           (at_x & real) + (t >> 2) * 256);
+                    for (int t = 0; t < 8; ++t)
+                        x[t] = *reinterpret_cast<const u32x4*>(lds + kFewX + from[t & 3] +
+                                                               (at_x & real) + (t >> 2) * 256);
                 }
                 // all of them on their way before the first is waited for; read, so
                 // the codes' place can be filled again
@@ -514,8 +514,8 @@ __global__ __launch_bounds__(kThreads, 2) void w4_few_kernel(const W4Args a) {
 }
 
 // ---------------------------------------------------------------------
-// Big tiles: BM (32 to 256) rows of x by 256 rows of w, eight waves, WN of them
-// side by side over the rows of w, each with its part of the sums in registers.
+// Big tiles: BM (160 to 256) rows of x by 256 rows of w. Eight waves in two rows of
+// four, each with BM / 2 x 64 of the sums in registers.
 // A slab is 64 columns: 128 bytes of a row of x, 32 bytes of codes of a row of
 // w. x goes from memory into LDS by slabs, codes by pairs of slabs (a row's 64
 // bytes at a time), scales 16 bytes of a row at a time. Waves 0 to 3 load x,
@@ -541,9 +541,7 @@ constexpr int kScaleSets = 4;
 template <int BM>
 constexpr int kStagesX = BM > 224 ? 2 : BM > 160 ? 3 : 4;
 template <int BM>
-constexpr int kStagesW = BM == 224 ? 3 : BM > 128 ? 4 : BM == 128 ? 5 : 6;
-template <int BM>
-constexpr int kAcross = BM > 64 ? 4 : 8;         // waves over the rows of w
+constexpr int kStagesW = BM == 224 ? 3 : 4;
 
 __device__ __forceinline__ int place_x(int r) {
     const int j = (r >> 2) & 3;                  // 0, 1, 2, 3 -> 0, 2, 3, 1
@@ -553,7 +551,7 @@ __device__ __forceinline__ int place_x(int r) {
 template <int GROUP, bool GATED, int BM>
 __device__ __forceinline__ void w4_tile(const W4Args& a, int g, int m0, int rows, int n0,
                                         uint8_t* lds) {
-    constexpr int WN = kAcross<BM>;
+    constexpr int WN = 4;
     constexpr int JF = BM * WN / 128;             // fragments of x of a wave
     constexpr int FRAGS = 16 / WN;                // and of w
     constexpr int XS = kStagesX<BM>, WS = kStagesW<BM>;

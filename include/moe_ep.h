@@ -659,7 +659,8 @@ MOE_EP_API int moe_ep_matmul(const void* x, int64_t x_stride, const void* w, int
  *                 Sp = H / group rounded up to 16 bytes, w_scale_stride bytes
  *                 between experts (>= Nw * Sp); over all tokens w_scale_stride
  *                 bytes between rows (>= H / group). Bytes behind a row's last
- *                 scale have no effect.
+ *                 scale have no effect, but those of the last row are read up
+ *                 to the next multiple of 16.
  *   w_global      f: fp32, one for an expert's matrix, or for
  *                 MOE_EP_ACT_SILU_GATED two, of its gate and its up rows
  *                 ([e_local] or [e_local, 2], dense); NULL: 1.

@@ -358,3 +358,29 @@ def test_common_counts_of_several_ranks():
                                 tokens=o[1])
         torch.cuda.synchronize()
         check_grad(grad, x, ids, [0, T], common.cpu(), o[1].cpu(), None, gl, "softmax", True, 1.0)
+
+
+@pytest.mark.parametrize("T", [200, 70000])
+def test_more_sequences_than_a_grid_has_rows(T):
+    """Sequences of one token each, most of them empty or not, past 2^16 of
+    them."""
+    S, E, K = 66000, 8, 2
+    say(f"[balance] S={S} T={T}")
+    x, ids = inputs(T, E, K, F32, 0.0, gen(T))
+    bounds = [min(T, i) for i in range(S + 1)]
+    got = balance(x.to(DEV), ids.to(DEV), "softmax", bounds)
+    torch.cuda.synchronize()
+    n = min(S, T)
+    picked = torch.zeros(S, E, dtype=torch.int32)
+    for k in range(K):
+        real = ids[:n, k] >= 0
+        picked[:n][real, ids[:n, k][real].long()] += 1
+    assert torch.equal(got[0].cpu(), picked)
+    real = (ids[:n] >= 0).any(dim=1)
+    assert torch.equal(got[1].cpu()[:n], real.int()) and not bool(got[1][n:].any())
+    q = torch.softmax(x[:n].double(), dim=1) * real[:, None]
+    # one token: its scores, the largest off by their sum's and exponentials' places
+    assert bool(((got[2].cpu()[:n].double() - q).abs() <= 64 * U * q).all())
+    loss = E * (picked[:n].double() / K * q).sum(dim=1)
+    assert bool(((got[3].cpu()[:n].double() - loss).abs() <= 64 * U * loss).all())
+    assert not bool(got[2][n:].any()) and not bool(got[3][n:].any())
