@@ -115,10 +115,11 @@ int check_w4(const W4Args& a, int64_t H, int64_t N, int64_t rows, int ob) {
 inline int64_t w4_scale_row(int64_t H, int32_t group) { return (H / group + 15) / 16 * 16; }
 
 // Tokens of a block of the balance loss's sums, 0: few enough tokens for a
-// block per sequence, which ends the call in one launch (128 tokens of one
-// sequence, 256 experts: 12 us; with tiles and the join of them 14).
+// block per sequence, which ends the call in one launch (one sequence, 256
+// experts, softmax: 64 tokens 9.1 us, with tiles and the join of them 12.2; 128
+// tokens 10.5 and 12.4, 256 tokens 16.6 and 12.2).
 inline int64_t balance_tile(int64_t T) {
-    if (T <= 256) return 0;
+    if (T <= 128) return 0;
     const int64_t per = (T + 255) / 256;
     return per < 32 ? 32 : per;
 }

@@ -360,7 +360,7 @@ def test_common_counts_of_several_ranks():
         check_grad(grad, x, ids, [0, T], common.cpu(), o[1].cpu(), None, gl, "softmax", True, 1.0)
 
 
-@pytest.mark.parametrize("T", [200, 70000])
+@pytest.mark.parametrize("T", [100, 200, 70000])
 def test_more_sequences_than_a_grid_has_rows(T):
     """Sequences of one token each, most of them empty or not, past 2^16 of
     them."""
