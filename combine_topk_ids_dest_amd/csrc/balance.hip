@@ -11,6 +11,11 @@
 // and sums over a token's experts are fp32 (a result is used once, in fp32: no
 // choice hangs on its last bit); sums over tokens are fp32 within a block's
 // tokens and fp64 over blocks, always in the same order. Counts are integers.
+//
+// Bound by the logits' bytes only at many tokens (65536 x 256, fp32: the sums 19 us
+// at 3.6 TB/s and their join 7, the gradient 45, of some 300 instructions a token);
+// below by chains of loads and of sums over lanes, so a wave has several tokens at
+// once (8192 tokens: 15 us the loss, 11 the gradient; 128: 12 and 6).
 #include <type_traits>
 
 #include "experts.h"

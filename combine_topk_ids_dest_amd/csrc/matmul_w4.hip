@@ -5,7 +5,9 @@
 // code times scale, is exact in bf16 (as is a code times a power of two): the
 // weights are made there in registers and multiplied in the bf16 matrix cores,
 // with fp32 sums of exact products. f, one factor for a matrix, is applied to
-// the sum.
+// the sum. 32 experts of 15575 rows, 7168 -> 2 x 2048, E4M3: 880 to 950 us; 8 of
+// 917 rows 82; 25 of one or two rows 88 (4.7 TB/s); one token 9 (with 2048 -> 7168
+// and powers of two, 917 rows: 44).
 #include "product_tiles.h"
 
 namespace moe_ep {
