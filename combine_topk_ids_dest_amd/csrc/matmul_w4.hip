@@ -111,6 +111,7 @@ constexpr int kFewPitch = kSmall + 4;
 constexpr int kFewSums = kWaves * kSmall * kFewPitch * 4;
 constexpr int kFewZero = kFewPart + 2 * kFewSums;        // 512 bytes of zeros
 constexpr int kFewLds = kFewZero + 512;
+constexpr float kCodeUnit = 0x1p-7f;             // what a bare code of 1 is taken as
 static_assert(kFewLds <= 160 << 10, "");
 
 __device__ __forceinline__ int place_few(int r) {
@@ -264,7 +265,9 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
         // 4 g + i row g of x in the columns of lane quarter i and zero in the
         // others, so that sum 4 g + i of a row of w is over one group of columns;
         // it is scaled and added. That takes an instruction a weight, weights
-        // widened with their scales two.
+        // widened with their scales two. Codes are taken times 2^-7 and the scales
+        // times 2^7: 16 products of a bare code, up to 6, with the largest bf16
+        // would be past fp32's range where those of the weights are not.
         auto all_steps = [&](auto split) {
             constexpr bool SPLIT = decltype(split)::value;
             const int row = SPLIT ? r >> 2 : r & ((1 << cur.lx) - 1);
@@ -345,12 +348,12 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-                        d[b] = mma_bf16(x[2 * b], widen4<32>(c[b >> 1][2 * b & 3], 1.0f), zero);
+                        d[b] = mma_bf16(x[2 * b], widen4<32>(c[b >> 1][2 * b & 3], kCodeUnit), zero);
                     }
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
-                        d[b] = mma_bf16(x[2 * b + 1], widen4<32>(c[b >> 1][(2 * b & 3) + 1], 1.0f),
-                                        d[b]);
+                        d[b] = mma_bf16(x[2 * b + 1],
+                                        widen4<32>(c[b >> 1][(2 * b & 3) + 1], kCodeUnit), d[b]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int n = (H - k - h * 128) / 16;
@@ -361,10 +364,12 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
                         for (int e = 0; e < 4; ++e) {
                             const int v = (int)sc[2 * h + (e >> 1)];
                             // group 2 e + b of the half: byte 2 (e & 1) + b
-                            const float f0 = e & 1 ? __builtin_amdgcn_cvt_f32_fp8(v, 2)
-                                                   : __builtin_amdgcn_cvt_f32_fp8(v, 0);
-                            const float f1 = e & 1 ? __builtin_amdgcn_cvt_f32_fp8(v, 3)
-                                                   : __builtin_amdgcn_cvt_f32_fp8(v, 1);
+                            const float f0 =
+                                e & 1 ? __builtin_amdgcn_cvt_scalef32_f32_fp8(v, 1 / kCodeUnit, 2)
+                                      : __builtin_amdgcn_cvt_scalef32_f32_fp8(v, 1 / kCodeUnit, 0);
+                            const float f1 =
+                                e & 1 ? __builtin_amdgcn_cvt_scalef32_f32_fp8(v, 1 / kCodeUnit, 3)
+                                      : __builtin_amdgcn_cvt_scalef32_f32_fp8(v, 1 / kCodeUnit, 1);
                             acc[e] = __builtin_fmaf(d[2 * h][e], f0, acc[e]);
                             acc2[e] = __builtin_fmaf(d[2 * h + 1][e], f1, acc2[e]);
                         }
