@@ -34,6 +34,10 @@ const float kNothing = -__builtin_huge_valf();
 template <int V>
 constexpr int kAtOnce = V >= 16 ? 2 : 4;
 
+// Tokens of a wave of the gradient, whose picks lie in KP lanes each.
+template <int V, int KP>
+constexpr int kGradAtOnce = 64 / KP < kAtOnce<V> ? 64 / KP : kAtOnce<V>;
+
 // v of the lane that CTRL names (`none` where there is none, or in the rows
 // that ROWS leaves out).
 template <int CTRL, int ROWS>
@@ -73,6 +77,34 @@ __device__ __forceinline__ double wave_sum(double v) {
     for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
     return v;
 }
+
+// The sum of fp64 values by lane moves and not through LDS, for each token. (The
+// one above, made once a sequence, holds fewer registers: 123, not 129, of the
+// gradient of 256 sigmoid scores, where 128 leave room for one wave more.)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF,
+                                                              false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL,
+                                                              ROWS, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32);
+}
+
+__device__ __forceinline__ double token_sum(double v) {
+    v += moved<0x111, 0xF>(v);
+    v += moved<0x112, 0xF>(v);
+    v += moved<0x114, 0xF>(v);
+    v += moved<0x118, 0xF>(v);
+    v += moved<0x142, 0xA>(v);
+    v += moved<0x143, 0xC>(v);
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(
+        double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63) |
+                    (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63) << 32);
+}
+
+__device__ __forceinline__ float token_sum(float v) { return wave_sum(v); }
 
 // A logit as the scores take it: -inf for one that belongs to no expert (-inf
 // or NaN), the largest fp32 for +inf.
@@ -149,10 +181,11 @@ __device__ __forceinline__ int first_behind(const int32_t* start, int S, int64_t
 // A token's scores before their sum divides them, and 1 / sum (0 without a
 // score). For sigmoid scores also rest = 1 - sigmoid(x), and they are taken
 // times e^-m, m = min(0, the largest logit), so that a token of far negative
-// logits has scores too. top: the largest logit.
-template <int V, bool SIGMOID>
+// logits has scores too. top: the largest logit. all: the sum, and with WIDE one
+// of fp64, where the few large scores may be replaced and the others are left.
+template <int V, bool SIGMOID, bool WIDE = false>
 __device__ __forceinline__ float scores(const float (&x)[V], float (&q)[V], float (&rest)[V],
-                                        float& top) {
+                                        float& top, double& all) {
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, x[i]);
@@ -160,7 +193,7 @@ __device__ __forceinline__ float scores(const float (&x)[V], float (&q)[V], floa
     top = m;
     if (SIGMOID) m = fminf(m, 0.f);
     const float em = SIGMOID ? exp_fast(m) : 0.f;
-    float sum = 0.f;
+    std::conditional_t<WIDE, double, float> sum = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (SIGMOID) {
@@ -174,8 +207,9 @@ __device__ __forceinline__ float scores(const float (&x)[V], float (&q)[V], floa
         }
         sum += q[i];
     }
-    sum = wave_sum(sum);
-    return sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
+    sum = token_sum(sum);
+    all = sum;
+    return sum > 0 ? __builtin_amdgcn_rcpf((float)sum) : 0.f;
 }
 
 // Sums over a block of a per-thread value pair.
@@ -264,7 +298,8 @@ __global__ __launch_bounds__(kTokenThreads) void balance_kernel(const BalanceArg
                 tokens += count;
                 if (pick) atomicAdd(&hist[id[b]], 1);
                 float q[V], rest[V], top;
-                const float inv = scores<V, SIGMOID>(x[b], q, rest, top);
+                double sum;
+                const float inv = scores<V, SIGMOID>(x[b], q, rest, top, sum);
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] += q[i] * (count ? inv : 0.f);
             }
@@ -387,21 +422,96 @@ __global__ __launch_bounds__(kTokenThreads) void balance_join_kernel(const Balan
     }
 }
 
+// v of the lane whose number differs in the bits of MASK: 1 to 3 within quads, 7
+// (half rows mirrored) and 15 (rows mirrored).
+template <int MASK>
+__device__ __forceinline__ int other(int v) {
+    constexpr int ctrl = MASK == 1   ? 0xB1
+                         : MASK == 2 ? 0x4E
+                         : MASK == 3 ? 0x1B
+                         : MASK == 7 ? 0x141
+                                     : 0x140;
+    return __builtin_amdgcn_update_dpp(0, v, ctrl, 0xF, 0xF, true);
+}
+
+template <int MASK>
+__device__ __forceinline__ double other(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)other<MASK>((int)(uint32_t)u) |
+                                          (uint64_t)(uint32_t)other<MASK>((int)(u >> 32)) << 32);
+}
+
+// The sum over a token's picks in the first K of KP neighbouring lanes (the others
+// have zeros), in those lanes.
+template <int KP>
+__device__ __forceinline__ double picks_sum(double v, int K) {
+    if (K == 1) return v;
+    if (K > 16) return token_sum(v);
+    v += other<1>(v);
+    v += other<2>(v);
+    v += other<7>(v);                            // a quad's lanes have the same by now
+    if (KP > 8 && K > 8) v += other<15>(v);
+    return v;
+}
+
+// Whether one of the wave's tokens, whose picks are in groups of N neighbouring
+// lanes, has an expert twice.
+template <int N>
+__device__ __forceinline__ bool repeats(int id, bool pick) {
+    bool same = false;
+    if constexpr (N == 64) {
+        for (uint64_t m = __ballot(pick); m; m &= m - 1) {
+            const int at = __builtin_amdgcn_readlane(id, __builtin_ctzll(m));
+            const uint64_t equal = __ballot(pick && id == at);
+            same |= (equal & (equal - 1)) != 0;
+        }
+        return same;
+    }
+    // each lane against those that differ in the bits of 1 to N - 1
+    auto quads = [&](int v) {
+        same |= other<1>(v) == id || other<2>(v) == id || other<3>(v) == id;
+    };
+    auto halves = [&](int v) {
+        quads(v);
+        const int m = other<7>(v);
+        same |= m == id;
+        quads(m);
+    };
+    halves(id);
+    if constexpr (N == 16) {
+        const int m = other<15>(id);
+        same |= m == id;
+        halves(m);
+    }
+    return __ballot(pick && same) != 0;
+}
+
 // The gradient of the logits. Through the picks' weights w = scale * p[pick]
 // (renormalize: / the picks' sum) with g their gradient:
 //   softmax, renormalised    dx[pick] += w (g - sum g w / scale)
-//   softmax                  dx[e]    += sum over picks of e of w g - p[e] sum w g
+//   softmax                  dx[e]    += scale p[e] (G[e] - sum over picks of p g),
+//                            G[e] the sum of g over the picks of e
 //   sigmoid                  the first form (plain: w g) times 1 - sigmoid(x[pick])
-// The picks' part, one exponential a token, is fp64: g - sum g w cancels.
+// The picks' part, one exponential a token, is fp64: g - sum g w and G - sum p g
+// cancel where the picks have almost all of the scores (of one pick with p =
+// 1 - 4e-8, fp32 left a gradient 18 % off). A plain softmax's sum is fp64 for that
+// too, its picks' scores replaced by their fp64 ones, and picks get their
+// experts' gradient whole instead of a correction to an fp32 one.
 //
 // A wave has B tokens at once, and 64 / B lanes have the picks of each (KP), so
 // that the fp64 part is done for all of them in one go.
-template <int V, bool SIGMOID, int KP>
-__global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const RouteGradArgs a) {
-    constexpr int B = 64 / KP < kAtOnce<V> ? 64 / KP : kAtOnce<V>;
+//
+// PLAIN: a softmax's weights that are not renormalised have a gradient. (Up to 256
+// experts at many tokens it is held to the registers of five waves a SIMD: 65536
+// tokens 37.5 us, with five registers more and four waves 39.9.)
+template <int V, bool SIGMOID, bool PLAIN, int KP>
+__global__ __launch_bounds__(kGradWaves * 64, PLAIN && V == 4 && KP == 8 ? 5 : 1) void
+route_backward_kernel(const RouteGradArgs a) {
+    constexpr int B = kGradAtOnce<V, KP>;
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
     const int of = lane / KP, pk = lane % KP;    // the lane's token and pick
+    extern __shared__ __align__(16) float grad_lds[];    // PLAIN: [waves][B][E]
     float each[V] = {};                          // a[e] of the sequence at hand
     int s = -1, at_s = -1;
     Span span = {0, 0};                          // of sequence s
@@ -424,12 +534,15 @@ __global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const R
         float xp = kNothing;
         if (pick) xp = load_logit(a.logits + tp * a.logits_stride, a.bf16, id);
         const uint64_t picks = __ballot(pick);
+        uint64_t given = picks;                  // those that have their expert's gradient
 
-        float my_top = 0.f, my_inv = 0.f;        // of the lane's token
+        float my_top = 0.f;                      // of the lane's token
+        double my_all = 0.0;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             float top, left[V];
-            const float inv = scores<V, SIGMOID>(xs[b], q[b], left, top);
+            double all;
+            const float inv = scores<V, SIGMOID, PLAIN>(xs[b], q[b], left, top, all);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 q[b][i] *= inv;
@@ -437,18 +550,32 @@ __global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const R
             }
             if (of == b) {
                 my_top = top;
-                my_inv = inv;
+                my_all = all;
             }
         }
 
         float back = 0.f, backs = 0.f;           // what reaches the logit of the lane's pick
-        if (a.grad_weights) {
-            auto group_sum = [](double v) {
-#pragma unroll
-                for (int off = 1; off < KP; off <<= 1) v += __shfl_xor(v, off, 64);
-                return v;
-            };
-            const bool live = pick && xp > kNothing;
+        if (PLAIN || a.grad_weights) {
+            bool live = pick && xp > kNothing;
+            double gw = live ? (double)g : 0.0;
+            if (PLAIN && a.K > 1 &&
+                (a.K <= 8    ? repeats<8>(id, pick)
+                 : a.K <= 16 ? repeats<16>(id, pick)
+                             : repeats<64>(id, pick))) {
+                // the first of an expert's picks has the gradients of all
+                const double mine = gw;
+                bool first = true;
+                gw = 0.0;
+                for (int j = 0; j < a.K; ++j) {
+                    const int from = of * KP + j;
+                    const bool same = __shfl(id, from, 64) == id;
+                    const double v = __shfl(mine, from, 64);
+                    if (same) gw += v;
+                    if (same && j < pk) first = false;
+                }
+                live = live && first;
+                given = __ballot(pick && first);
+            }
             const double v = live ? (double)xp : 0.0;
             double w, left = 1.0;
             if (SIGMOID) {
@@ -459,23 +586,47 @@ __global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const R
                 w = exp(v - (double)my_top);     // times 1 / sum, left out of a ratio
             }
             if (!live) w = 0.0;
-            double gw = live ? (double)g : 0.0;
-            if (a.renormalize) {
-                const double all = group_sum(w);
+            if (!PLAIN && a.renormalize) {
+                const double all = picks_sum<KP>(w, a.K);
                 w = all > 0.0 ? w / all : 0.0;
-                gw -= group_sum(gw * w);
-            } else if (!SIGMOID) {
-                w *= (double)my_inv;
+                gw -= picks_sum<KP>(gw * w, a.K);
+            }
+            if constexpr (PLAIN) {
+                // the pick's score as the sum has it, from the same fp32 steps
+                const double had = live ? (double)exp_fast(xp - my_top) : 0.0;
+                const double all = my_all + picks_sum<KP>(w - had, a.K);
+                w = live ? w / all : 0.0;
+                const double through = picks_sum<KP>(gw * w, a.K);
+                backs = (float)((double)a.scale * through);
+                gw -= through;
             }
             back = live ? (float)((double)a.scale * w * gw * left) : 0.f;
-            if (!SIGMOID && !a.renormalize) backs = (float)group_sum((double)back);
+        }
+
+        // a plain softmax's part of all experts, the picks' put in their places,
+        // in LDS of the wave's own (which serves a wave in order)
+        float* const part = grad_lds + (PLAIN ? wave * B * a.E : 0);
+        if constexpr (PLAIN) {
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const float all = lane_value(backs, b * KP & 63);
+#pragma unroll
+                for (int i = 0; i < V; ++i)      // (where q = 0, `all` may be no number)
+                    if (lane + 64 * i < a.E)
+                        part[b * a.E + lane + 64 * i] = q[b][i] == 0.f ? 0.f : -(q[b][i] * all);
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (given >> lane & 1) part[of * a.E + id] = back;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
         }
 
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             if (t + b >= t1) break;
             constexpr uint64_t kGroup = KP == 64 ? ~0ull : (1ull << (KP & 63)) - 1;
-            uint64_t mask = picks >> (b * KP & 63) & kGroup;
+            uint64_t mask = picks >> (b * KP & 63) & kGroup;     // of a padding token 0
             bool aux = false;
             if (a.grad_loss && mask) {
                 if (s < 0 || span.hi <= t + b) {
@@ -510,7 +661,6 @@ __global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const R
                 for (int i = 0; i < V; ++i) through += q[b][i] * each[i];
                 through = wave_sum(through);
             }
-            if (!SIGMOID) through += lane_value(backs, b * KP & 63);
             float dx[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -518,7 +668,11 @@ __global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const R
                 if (SIGMOID) dx[i] *= rest[b][i];
                 if (q[b][i] == 0.f) dx[i] = 0.f; // also where `through` is no number
             }
-            if (a.grad_weights)
+            if constexpr (PLAIN) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (lane + 64 * i < a.E) dx[i] += part[b * a.E + lane + 64 * i];
+            } else if (a.grad_weights) {
                 for (; mask; mask &= mask - 1) {
                     const int from = b * KP + __builtin_ctzll(mask);
                     const int e = __builtin_amdgcn_readlane(id, from);
@@ -527,6 +681,7 @@ __global__ __launch_bounds__(kGradWaves * 64) void route_backward_kernel(const R
                     for (int i = 0; i < V; ++i)
                         if (e >> 6 == i) dx[i] += v;
                 }
+            }
             uint8_t* out = a.grad + (t + b) * a.grad_stride;
             if (a.grad_bf16) {
 #pragma unroll
@@ -583,19 +738,23 @@ hipError_t launch_route_backward(const RouteGradArgs& a, hipStream_t st) {
     const unsigned grid = (unsigned)((a.T + a.tile - 1) / a.tile);
     return by_width(a.E, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        auto run = [&](auto sigmoid, auto kp) {
-            route_backward_kernel<V, decltype(sigmoid)::value, decltype(kp)::value>
-                <<<grid, kGradWaves * 64, 0, st>>>(a);
+        auto run = [&](auto sigmoid, auto plain, auto kp) {
+            constexpr int KP = decltype(kp)::value;
+            constexpr bool P = decltype(plain)::value;
+            const size_t lds = P ? (size_t)kGradWaves * kGradAtOnce<V, KP> * a.E * 4 : 0;
+            route_backward_kernel<V, decltype(sigmoid)::value, P, KP>
+                <<<grid, kGradWaves * 64, lds, st>>>(a);
         };
-        auto by_picks = [&](auto sigmoid) {
+        auto by_picks = [&](auto sigmoid, auto plain) {
             // few tokens: one a wave, over more of the CUs (256 experts, 8 picks:
             // 8192 tokens 12.5 us, 20 with eight a wave; 65536 tokens 62 and 51)
-            if (a.T <= 16384 || a.K > 16) run(sigmoid, std::integral_constant<int, 64>{});
-            else if (a.K <= 8) run(sigmoid, std::integral_constant<int, 8>{});
-            else run(sigmoid, std::integral_constant<int, 16>{});
+            if (a.T <= 16384 || a.K > 16) run(sigmoid, plain, std::integral_constant<int, 64>{});
+            else if (a.K <= 8) run(sigmoid, plain, std::integral_constant<int, 8>{});
+            else run(sigmoid, plain, std::integral_constant<int, 16>{});
         };
-        if (a.score == MOE_EP_SIGMOID) by_picks(std::true_type{});
-        else by_picks(std::false_type{});
+        if (a.score == MOE_EP_SIGMOID) by_picks(std::true_type{}, std::false_type{});
+        else if (a.grad_weights && !a.renormalize) by_picks(std::false_type{}, std::true_type{});
+        else by_picks(std::false_type{}, std::false_type{});
     });
 }
 

@@ -728,7 +728,9 @@ MOE_EP_API int moe_ep_balance_loss(const void* logits, int64_t logits_stride, in
  *   grad_logits[t, e] = sum_k grad_weights[t, k] * d topk_weights[t, k] / d x[t, e]
  *                     + sum_s grad_loss[s] * d loss[s] / d x[t, e]
  * The picks and the counts are constants (so is a selection bias, which only
- * chooses). The picks' part is computed in fp64, the rest in fp32, rounded once.
+ * chooses). The picks' part is computed in fp64, its differences too (the other
+ * experts enter a softmax's sum as fp32 exponentials), the rest in fp32; rounded
+ * to grad_dtype at the end.
  * Every row is written; a token without a pick, and an expert whose logit is
  * -inf or NaN, get +0.0; picks outside [0, E) have no part, whatever their
  * gradient holds. An expert that a token picks twice counts twice.
