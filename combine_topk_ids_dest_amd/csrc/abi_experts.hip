@@ -117,11 +117,13 @@ inline int64_t w4_scale_row(int64_t H, int32_t group) { return (H / group + 15) 
 // Tokens of a block of the balance loss's sums, 0: few enough tokens for a
 // block per sequence, which ends the call in one launch (one sequence, 256
 // experts, softmax: 64 tokens 9.1 us, with tiles and the join of them 12.2; 128
-// tokens 10.5 and 12.4, 256 tokens 16.6 and 12.2).
+// tokens 10.5 and 12.4, 256 tokens 16.6 and 12.2). At most 4096, so that a wave
+// adds at most 256 scores in fp32: with 2^26 tokens alike in 256 tiles a mean score
+// was 2.4e-4 off.
 inline int64_t balance_tile(int64_t T) {
     if (T <= 128) return 0;
     const int64_t per = (T + 255) / 256;
-    return per < 32 ? 32 : per;
+    return per < 32 ? 32 : per > 4096 ? 4096 : per;
 }
 
 // Sizes of the balance loss; its slots of sums and their bytes.

@@ -10,7 +10,8 @@
 // A wave has one token at a time, lane l the experts l, l + 64, ... Exponentials
 // and sums over a token's experts are fp32 (a result is used once, in fp32: no
 // choice hangs on its last bit); sums over tokens are fp32 within a block's
-// tokens and fp64 over blocks, always in the same order. Counts are integers.
+// tokens, at most 256 to a wave, and fp64 over blocks, always in the same order.
+// Counts are integers.
 //
 // Bound by the logits' bytes only at many tokens (65536 x 256, fp32: the sums 19 us
 // at 3.6 TB/s and their join 7, the gradient 45, of some 300 instructions a token);

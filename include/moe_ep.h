@@ -699,7 +699,8 @@ MOE_EP_API int moe_ep_matmul_w4(const void* x, int64_t x_stride, const void* w, 
  *                     mean_score[s, e]: 1 where picks or scores are even.
  * A sequence without a token that counts has zeros. An expert whose logit is
  * -inf or NaN has q = 0, +inf counts as the largest fp32 value. Exponentials and
- * a token's sums are fp32; equal calls give equal bits.
+ * a token's sums are fp32, sums over tokens fp32 for at most 4096 tokens (256 a
+ * wave, then 16 waves) and fp64 from there; equal calls give equal bits.
  *
  *   logits        as for moe_ep_route_topk.   topk_ids  int32 [T, K].
  *   seq_start     int32 [S + 1] on the device, ascending, values outside [0, T]
