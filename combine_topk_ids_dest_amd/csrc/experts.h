@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "common.h"
+#include "w4_tiles.h"
 
 namespace moe_ep {
 
@@ -59,15 +60,6 @@ struct MatmulArgs {
 };
 
 hipError_t launch_matmul(const MatmulArgs& a, hipStream_t stream);
-
-// How tiles of up to 16 rows are cut: 2^lw runs of 16 rows of w each, but in the
-// grid's last, partial round 2^last, so that it is shorter where CUs would be
-// idle.
-struct FewCut {
-    int lw, last;
-    int nt;                      // tiles of a run, over all columns
-    int whole, total;            // tiles before the last round, and of all rounds
-};
 
 // The same with 4-bit weights: m.w holds E2M1 codes (m.w_stride, m.w_row bytes),
 // s one scale per `group` columns (E4M3 for 16, E8M0 for 32). m.row_bytes is

@@ -413,53 +413,6 @@ __device__ __forceinline__ void few_tiles(const W4Args& a, uint8_t* lds, int tot
     finish(old, odd ^ 1);
 }
 
-// A cut's rounds times a tile's time, in columns of 16 rows of w: a tile's own and
-// about 2048 for its start and end.
-__host__ __device__ __forceinline__ float few_columns(const FewCut& c, int H) {
-    return (float)(c.whole / kGrid) * (float)((H << c.lw) + 2048) +
-           (c.total > c.whole ? (float)((H << c.last) + 2048) : 0.f);
-}
-
-// The cut of `runs` runs of up to 16 rows that takes least. least: lw for runs
-// of more than 8 rows (a step of 2048 columns of 16 rows is no segment).
-__host__ __device__ __forceinline__ FewCut few_cut(int runs, int N, int H, int bo, int least) {
-    FewCut best = {};
-    float best_cost = 0.f;
-#pragma unroll
-    for (int lw = 3; lw >= 0; --lw) {
-        if (lw < least) break;
-        const int nt = (N + (bo << lw) - 1) / (bo << lw);
-        const int tiles = runs * nt;
-        const int whole = tiles / kGrid * kGrid, rest = tiles - whole;
-        int split = rest * 8 <= kGrid ? 3 : rest * 4 <= kGrid ? 2 : rest * 2 <= kGrid ? 1 : 0;
-        if (split > lw - least) split = lw - least;
-        const FewCut c = {lw, lw - split, nt, whole, whole + (rest << split)};
-        const float cost = few_columns(c, H);
-        if (lw == 3 || cost < best_cost) {
-            best_cost = cost;
-            best = c;
-        }
-    }
-    return best;
-}
-
-// What a product takes with tiles of a few rows, in us, and with big ones (`turns`
-// whole rounds of the grid of `rows` rows each, then one of `last`; 0: none), from
-// measured times. Both sides where the choice turns, in us, few and big: 7168 ->
-// 2 x 2048, E4M3, 64 rows 23 and 57, 256 rows 65 and 73, 512 rows 125 and 73;
-// 2048 -> 7168, 96 rows 22 and 22, 128 rows 26 and 22.
-__host__ __device__ __forceinline__ float few_time(const FewCut& c, int H, int group) {
-    return 6.f + few_columns(c, H) * (group == 16 ? 16.f / 29300.f : 16.f / 39000.f);
-}
-
-__host__ __device__ __forceinline__ float big_time(int turns, int rows, int last, int H,
-                                                   int group) {
-    const float pairs = (float)((H + 127) / 128);
-    const float start = group == 16 ? 0.55f : 0.4f, row = group == 16 ? 0.0135f : 0.0125f;
-    return 8.f + (float)turns * pairs * (start + row * (float)rows) +
-           (last ? pairs * (start + row * (float)last) : 0.f);
-}
-
 template <int GROUP, bool GATED>
 __device__ __forceinline__ void few_rows(const W4Args& a, uint8_t* lds, int rows0, int small_to,
                                          int runs) {
@@ -506,18 +459,6 @@ __device__ __forceinline__ void few_rows(const W4Args& a, uint8_t* lds, int rows
         return few_setup<GROUP, GATED>(a, at.g, (at.l - col * mt) * kSmall, at.rows,
                                        col * (BO << cut.lw) + n0, lw);
     });
-}
-
-template <int GROUP, bool GATED>
-__global__ __launch_bounds__(kThreads, 2) void w4_few_kernel(const W4Args a) {
-    __shared__ __align__(1024) uint8_t lds[kFewLds];
-    if (!a.m.counts) return few_rows<GROUP, GATED>(a, lds, 0, INT32_MAX, 0);
-    const int rows0 = lane_rows(a.m, 0);
-    int runs = 0;
-    for (int g0 = 0; g0 < a.m.groups; g0 += 64)
-        runs += __builtin_amdgcn_readlane(
-            wave_inclusive_scan(runs_of(g0 ? lane_rows(a.m, g0) : rows0, INT32_MAX, 0)), 63);
-    if (runs > 0) few_rows<GROUP, GATED>(a, lds, rows0, INT32_MAX, runs);
 }
 
 // ---------------------------------------------------------------------
@@ -918,17 +859,14 @@ __device__ __forceinline__ void w4_mid_tile(const W4Args& a, int g, int m0, int 
     finish_tile<2, GATED, FRAGS, JF, WN>(m, g, m0, left, n0, acc, lds);
 }
 
+// Tiles of each kind (n; of a few rows the runs) and of all but those, and up to how
+// many rows a group takes few-row tiles: kSmall, or all groups do, or none.
 template <int GROUP, bool GATED>
-__global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
-    __shared__ __align__(1024) uint8_t lds[kLds];
-    const MatmulArgs& m = a.m;
+__device__ __forceinline__ int plan_tiles(const MatmulArgs& m, int rows0, int (&n)[kKinds],
+                                          int& total) {
     constexpr int BB = GATED ? kCols / 2 : kCols;
-    // 64 rows: each wave all of them, so that a weight is widened once, or with
-    // powers of two, which take little of that, half of them and less of LDS
-    constexpr int MID64 = GROUP == 16 ? 8 : 4;
     const int ntb = (m.N + BB - 1) / BB;
-    const int rows0 = lane_rows(m, 0);
-    int n[kKinds], total = 0, small_to = m.counts ? kSmall : 0;
+    int small_to = m.counts ? kSmall : 0;
     for (;;) {
         count_runs(m, rows0, small_to, n);
         total = 0;
@@ -937,28 +875,44 @@ __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
             n[k] *= ntb;
             total += n[k];
         }
-        if (!small_to || small_to == INT32_MAX) break;
+        if (!small_to || small_to == INT32_MAX || total == 0) break;
         if (total > kGrid) {
             // a few rows beside so much else: in part-filled tiles
             small_to = 0;
             continue;
         }
-        if (total == 0) break;
         // one round of big tiles, in parts of these rows, or few-row tiles for all
         int most = 0, runs = 0;
 #pragma unroll
         for (int k = 1; k < kKinds; ++k)
             if (n[k]) most = k;
-        const int cut = last_parts(total);
         for (int g0 = 0; g0 < m.groups; g0 += 64)
             runs += __builtin_amdgcn_readlane(
                 wave_inclusive_scan(runs_of(g0 ? lane_rows(m, g0) : rows0, INT32_MAX, 0)), 63);
-        const int H = m.row_bytes / 2;
-        if (few_time(few_cut(runs, m.N, H, GATED ? kSmall / 2 : kSmall, 1), H, GROUP) >=
-            big_time(0, 0, (most + cut - 1) / cut * 32, H, GROUP))
+        if (!few_instead(total, most, runs, n[0], m.N, m.row_bytes / 2, GATED ? kSmall / 2 : kSmall,
+                         GROUP))
             break;
         small_to = INT32_MAX;
     }
+    return small_to;
+}
+
+// A block's share of all tiles.
+template <int GROUP, bool GATED>
+__device__ __forceinline__ void all_tiles(const W4Args& a, uint8_t* lds, int rows0) {
+    const MatmulArgs& m = a.m;
+    constexpr int BB = GATED ? kCols / 2 : kCols;
+    // 64 rows: each wave all of them, so that a weight is widened once, or with
+    // powers of two, which take little of that, half of them and less of LDS
+    constexpr int MID64 = GROUP == 16 ? 8 : 4;
+    const int ntb = (m.N + BB - 1) / BB;
+    int n[kKinds], total;
+    // (in scalar registers, which is where the tiles' loads take what follows from
+    // them: behind branches on fp32 numbers the compiler may hold them in vector ones)
+    const int small_to = uniform(plan_tiles<GROUP, GATED>(m, rows0, n, total));
+    total = uniform(total);
+#pragma unroll
+    for (int k = 0; k < kKinds; ++k) n[k] = uniform(n[k]);
     const int parts = last_parts(total);
     for (int t0 = 0; t0 < total; t0 += kGrid) {
         const Turn turn = turn_of(blockIdx.x, t0, total, parts);
@@ -991,21 +945,41 @@ __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
     if (n[0] > 0) few_rows<GROUP, GATED>(a, lds, rows0, small_to, n[0]);
 }
 
+// Few-row tiles for all groups.
+template <int GROUP, bool GATED>
+__device__ __forceinline__ void only_few_rows(const W4Args& a, uint8_t* lds, int rows0) {
+    int runs = 0;
+    for (int g0 = 0; g0 < a.m.groups; g0 += 64)
+        runs += __builtin_amdgcn_readlane(
+            wave_inclusive_scan(runs_of(g0 ? lane_rows(a.m, g0) : rows0, INT32_MAX, 0)), 63);
+    if (runs > 0) few_rows<GROUP, GATED>(a, lds, rows0, INT32_MAX, runs);
+}
+
+template <int GROUP, bool GATED>
+__global__ __launch_bounds__(kThreads, 2) void w4_few_kernel(const W4Args a) {
+    __shared__ __align__(1024) uint8_t lds[kFewLds];
+    if (!a.m.counts) return few_rows<GROUP, GATED>(a, lds, 0, INT32_MAX, 0);
+    only_few_rows<GROUP, GATED>(a, lds, lane_rows(a.m, 0));
+}
+
+template <int GROUP, bool GATED>
+__global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
+    __shared__ __align__(1024) uint8_t lds[kLds];
+    all_tiles<GROUP, GATED>(a, lds, lane_rows(a.m, 0));
+}
+
 template <int GROUP, bool GATED>
 hipError_t launch(const W4Args& a, hipStream_t st) {
     const MatmulArgs& m = a.m;
+    constexpr int BO = GATED ? kSmall / 2 : kSmall, BB = GATED ? kCols / 2 : kCols;
     const int H = m.row_bytes / 2;
-    bool few = m.rows <= 2 * kSmall;
+    bool few;
     W4Args b = a;
-    if (!m.counts) {
-        b.cut = few_cut((m.rows + kSmall - 1) / kSmall, m.N, H, GATED ? kSmall / 2 : kSmall,
-                        m.rows > 8 ? 1 : 0);
-        const Cut c = cut_rows(m.rows, 0);
-        const int tiles = c.runs * ((m.N * (GATED ? 2 : 1) + kCols - 1) / kCols);
-        const int rest = tiles % kGrid, parts = last_parts(tiles);
-        few = few_time(b.cut, H, GROUP) <
-              big_time(tiles / kGrid, c.kind * 32, rest ? (c.kind + parts - 1) / parts * 32 : 0, H,
-                       GROUP);
+    if (m.counts) {
+        few = m.rows <= 2 * kSmall;
+    } else {
+        b.cut = few_cut((m.rows + kSmall - 1) / kSmall, m.N, H, BO, m.rows > 8 ? 1 : 0);
+        few = few_over_all(b.cut, m.rows, m.N, H, BB, GROUP);
     }
     if (few) w4_few_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(b);
     else w4_big_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(b);
