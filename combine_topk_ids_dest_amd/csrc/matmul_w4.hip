@@ -897,8 +897,8 @@ __device__ __forceinline__ int plan_tiles(const MatmulArgs& m, int rows0, int (&
     return small_to;
 }
 
-// A block's share of all tiles.
-template <int GROUP, bool GATED>
+// A block's share of all tiles; TALL: of all heights, else of 32 rows.
+template <int GROUP, bool GATED, bool TALL>
 __device__ __forceinline__ void all_tiles(const W4Args& a, uint8_t* lds, int rows0) {
     const MatmulArgs& m = a.m;
     constexpr int BB = GATED ? kCols / 2 : kCols;
@@ -918,7 +918,7 @@ __device__ __forceinline__ void all_tiles(const W4Args& a, uint8_t* lds, int row
         const Turn turn = turn_of(blockIdx.x, t0, total, parts);
         if (turn.t < 0) break;
         int t = turn.t;
-        int kind = kKinds - 1;
+        int kind = TALL ? kKinds - 1 : 1;
 #pragma unroll
         for (int k = kKinds - 1; k > 1; --k)
             if (kind == k && t >= n[k]) {
@@ -933,7 +933,7 @@ __device__ __forceinline__ void all_tiles(const W4Args& a, uint8_t* lds, int row
         auto run = [&](auto bm) {
             w4_tile<GROUP, GATED, decltype(bm)::value>(a, at.g, p.m0, p.end, n0, lds);
         };
-        const int f = p.fragments;
+        const int f = TALL ? p.fragments : 1;
         if (f == 8) run(std::integral_constant<int, 256>{});
         else if (f == 7) run(std::integral_constant<int, 224>{});
         else if (f == 6) run(std::integral_constant<int, 192>{});
@@ -955,6 +955,10 @@ __device__ __forceinline__ void only_few_rows(const W4Args& a, uint8_t* lds, int
     if (runs > 0) few_rows<GROUP, GATED>(a, lds, rows0, INT32_MAX, runs);
 }
 
+// Three kernels, since beside more code few rows take longer (by expert, 32 of one
+// or two rows or none, 2048 -> 7168, powers of two: 43, 45 and 50 us): with few-row
+// tiles only; with tiles of 32 rows too, for groups of up to 32 rows (32 experts of
+// 32 rows, 7168 -> 2 x 2048, E4M3: 281 us without, 129 with); and with all.
 template <int GROUP, bool GATED>
 __global__ __launch_bounds__(kThreads, 2) void w4_few_kernel(const W4Args a) {
     __shared__ __align__(1024) uint8_t lds[kFewLds];
@@ -963,9 +967,20 @@ __global__ __launch_bounds__(kThreads, 2) void w4_few_kernel(const W4Args a) {
 }
 
 template <int GROUP, bool GATED>
+__global__ __launch_bounds__(kThreads, 2) void w4_low_kernel(const W4Args a) {
+    __shared__ __align__(1024) uint8_t lds[kLds];
+    const int rows0 = lane_rows(a.m, 0);
+    bool more = false;
+    for (int g0 = 0; g0 < a.m.groups; g0 += 64)
+        more |= __ballot((g0 ? lane_rows(a.m, g0) : rows0) > kSmall) != 0;
+    if (!more) return only_few_rows<GROUP, GATED>(a, lds, rows0);
+    all_tiles<GROUP, GATED, false>(a, lds, rows0);
+}
+
+template <int GROUP, bool GATED>
 __global__ __launch_bounds__(kThreads, 2) void w4_big_kernel(const W4Args a) {
     __shared__ __align__(1024) uint8_t lds[kLds];
-    all_tiles<GROUP, GATED>(a, lds, lane_rows(a.m, 0));
+    all_tiles<GROUP, GATED, true>(a, lds, lane_rows(a.m, 0));
 }
 
 template <int GROUP, bool GATED>
@@ -976,12 +991,14 @@ hipError_t launch(const W4Args& a, hipStream_t st) {
     bool few;
     W4Args b = a;
     if (m.counts) {
-        few = m.rows <= 2 * kSmall;
+        few = m.rows <= 2 * kSmall && few_if_full(m.groups, m.rows, m.N, H, BO, BB, GROUP);
     } else {
         b.cut = few_cut((m.rows + kSmall - 1) / kSmall, m.N, H, BO, m.rows > 8 ? 1 : 0);
         few = few_over_all(b.cut, m.rows, m.N, H, BB, GROUP);
     }
     if (few) w4_few_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(b);
+    else if (m.counts && m.rows <= 2 * kSmall)
+        w4_low_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(b);
     else w4_big_kernel<GROUP, GATED><<<kGrid, kThreads, 0, st>>>(b);
     return hipGetLastError();
 }

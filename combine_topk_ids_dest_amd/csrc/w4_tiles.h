@@ -74,6 +74,19 @@ MOE_EP_TILES bool few_over_all(const FewCut& few, int rows, int N, int H, int co
                     group);
 }
 
+// By expert, with room for `rows` rows each: whether few-row tiles take less than
+// big ones even where every group is full, so that no counts need looking at. (8
+// experts of 17 to 32 rows, 512 -> 1024, powers of two: 9.1 us, beside the code of
+// 32-row tiles 11.8; 32 of 32 rows, 7168 -> 2 x 2048, E4M3, 281 and 129.)
+MOE_EP_TILES bool few_if_full(int groups, int rows, int N, int H, int bo, int cols, int group) {
+    if (rows <= kSmall) return true;
+    const Cut c = cut_rows(rows, 0);
+    const int tiles = groups * c.runs * ((N + cols - 1) / cols);
+    const int runs = groups * ((rows + kSmall - 1) / kSmall);
+    return few_time(few_cut(runs, N, H, bo, 1), H, group) <
+           big_time(tiles / kGrid, c.kind * 32, tiles % kGrid ? c.kind * 32 : 0, H, group);
+}
+
 // By expert, where groups of more than kSmall rows are `total` big tiles, one round
 // of the grid at most, of up to 32 * most rows, with `low` runs of 16 rows of other
 // groups behind them: whether few-row tiles for all `runs` runs take less. (Each

@@ -42,3 +42,17 @@ def test_few_rows_of_most_experts_count_beside_a_big_tile(choice):
     # alone it is the other way round with eight of them
     assert choice(experts([20] * 8, 256, 7168, 2048, True, 16)) == [("big", {"32"})]
 
+
+@pytest.mark.parametrize("rows", [24, 32])
+def test_the_room_for_rows_does_not_choose_their_tiles(choice, rows):
+    """32 experts of 24 or 32 rows take 32-row tiles with room for 32 rows as with
+    more (128 and 281 us), and few-row tiles where they have few rows."""
+    for H, N, gated in ((7168, 2048, True), (2048, 7168, False)):
+        for group in (16, 32):
+            room = [choice(experts([rows] * 32, c, H, N, gated, group)) for c in (32, 33, 256)]
+            assert all(r[0][1] == {"32"} for r in room), room
+            sparse = [choice(experts([1, 2, 0, 16] * 8, c, H, N, gated, group))
+                      for c in (16, 32, 33, 256)]
+            assert all(r[0][1] == {"few"} for r in sparse), sparse
+    # where all full experts' few-row tiles take less, that kernel alone
+    assert choice(experts([32] * 8, 32, 512, 1024, False, 32)) == [("few", {"few"})]

@@ -81,8 +81,9 @@ int main() {
             total = over * ntb;
             int small_to = kSmall;
             if (room <= 2 * kSmall) {
-                kernel = "few";
-                small_to = INT_MAX;
+                const bool few = few_if_full((int)rows.size(), room, N, H, bo, cols, group);
+                kernel = few ? "few" : "low";
+                if (few) small_to = INT_MAX;
             }
             if (small_to == kSmall && total > kGrid) small_to = 0;
             else if (small_to == kSmall && total &&
