@@ -1,5 +1,5 @@
-"""Which tiles the products with 4-bit weights take, without a GPU: the choice goes by
-the rows that there are."""
+"""Which tiles the products with 4-bit weights take, without a GPU: the cases of the
+GPU tests reach every kind, and the choice goes by the rows that there are."""
 import os
 import shutil
 import subprocess
@@ -7,6 +7,7 @@ import subprocess
 import pytest
 
 from combine_topk_ids_dest_amd import build as hip_build
+from w4_cases import EXPERTS, H, TOKENS, WIDE_N
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 
@@ -31,6 +32,18 @@ def choice(tmp_path_factory):
 
 def experts(counts, rows, H, N, gated, group):
     return f"experts {rows} {H} {N} {int(gated)} {group} " + " ".join(map(str, counts))
+
+
+@pytest.mark.parametrize("group", [16, 32])
+@pytest.mark.parametrize("gated", [False, True])
+def test_the_cases_take_every_kind_of_tile(choice, gated, group):
+    got = choice(*(f"dense {T} {H} {WIDE_N[gated]} {int(gated)} {group}" for T in TOKENS))
+    for (T, want), (_, tiles) in zip(TOKENS.items(), got):
+        assert want in tiles, (T, tiles)
+    for name, (counts, rows, N, Ng, kernel, want) in EXPERTS.items():
+        for columns in (H, 544, 16 * group):
+            (k, tiles), = choice(experts(counts, rows, columns, Ng if gated else N, gated, group))
+            assert k == kernel and want <= tiles, (name, columns, k, tiles)
 
 
 def test_few_rows_of_most_experts_count_beside_a_big_tile(choice):
