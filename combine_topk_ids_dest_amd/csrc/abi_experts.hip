@@ -114,12 +114,15 @@ int check_w4(const W4Args& a, int64_t H, int64_t N, int64_t rows, int ob) {
 // Bytes of a row of 4-bit weights' scales.
 inline int64_t w4_scale_row(int64_t H, int32_t group) { return (H / group + 15) / 16 * 16; }
 
-// Tokens of a block of the balance loss's sums, 0: few enough tokens for a
-// block per sequence, which ends the call in one launch (one sequence, 256
-// experts, softmax: 64 tokens 9.1 us, with tiles and the join of them 12.2; 128
-// tokens 10.5 and 12.4, 256 tokens 16.6 and 12.2). At most 4096, so that a wave
-// adds at most 256 scores in fp32: with 2^26 tokens alike in 256 tiles a mean score
-// was 2.4e-4 off.
+// Tokens of a block of the balance loss's sums, 0: few enough tokens for a block
+// per sequence, which ends the call in one launch. Calls one by one (one sequence,
+// 256 experts, softmax): 64 tokens 9.1 us, with tiles and the join of them 12.2; 128
+// tokens 10.5 and 12.4, 256 tokens 16.6 and 12.2. Replayed from a graph, without a
+// second launch's time on the host: 64 tokens 7.9 and 9.7, 128 tokens 10.9 and 9.6
+// (8 experts 8.8 and 7.5, 1024 experts 19.4 and 14.3; in 8 sequences, which are as
+// many blocks, 7.5 and 16.8).
+// At most 4096, so that a wave adds at most 256 scores in fp32: with 2^26 tokens
+// alike in 256 tiles a mean score was 2.4e-4 off.
 inline int64_t balance_tile(int64_t T) {
     if (T <= 128) return 0;
     const int64_t per = (T + 255) / 256;

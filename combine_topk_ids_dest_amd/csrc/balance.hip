@@ -7,16 +7,16 @@
 //   dx[t,e] = q[t,e] (a[e] - sum_j q[t,j] a[j]), a[e] = g E c[e] / (sum c * n),
 //             for sigmoid scores times 1 - sigmoid(x[e])
 //
-// A wave has one token at a time, lane l the experts l, l + 64, ... Exponentials
-// and sums over a token's experts are fp32 (a result is used once, in fp32: no
-// choice hangs on its last bit); sums over tokens are fp32 within a block's
-// tokens, at most 256 to a wave, and fp64 over blocks, always in the same order.
-// Counts are integers.
+// Lane l of a wave has a token's experts l, l + 64, ..., of one to four tokens at a
+// time. Exponentials and sums over a token's experts are fp32 (a result is used
+// once, in fp32: no choice hangs on its last bit); sums over tokens are fp32 within
+// a block's tokens, at most 256 to a wave, and fp64 over blocks, always in the same
+// order. Counts are integers. Where terms of the gradient cancel they are fp64.
 //
 // Bound by the logits' bytes only at many tokens (65536 x 256, fp32: the sums 19 us
-// at 3.6 TB/s and their join 7, the gradient 45, of some 300 instructions a token);
+// at 3.6 TB/s and their join 7, the gradient 38, of some 250 instructions a token);
 // below by chains of loads and of sums over lanes, so a wave has several tokens at
-// once (8192 tokens: 15 us the loss, 11 the gradient; 128: 12 and 6).
+// once (8192 tokens: 15 us the loss, 12 the gradient; 128: 13 and 5.6).
 #include <type_traits>
 
 #include "experts.h"
@@ -746,12 +746,19 @@ hipError_t launch_route_backward(const RouteGradArgs& a, hipStream_t st) {
             route_backward_kernel<V, decltype(sigmoid)::value, P, KP>
                 <<<grid, kGradWaves * 64, lds, st>>>(a);
         };
+        // One token a wave, over more of the CUs and with fewer registers, or (of up to
+        // 16 picks) several, which share the fp64 part. Both in us, one and several:
+        // 64 experts, 4096 tokens 6.1 and 6.5, 8192 8.9 and 7.6; 256, softmax, 16384
+        // tokens 17.8 and 19.3, 32768 30 and 27; 512, 32768 tokens renormalised 41 and
+        // 45, plain 37 and 34; 1024, 65536 tokens 126 and 132.
         auto by_picks = [&](auto sigmoid, auto plain) {
-            // few tokens: one a wave, over more of the CUs (256 experts, 8 picks:
-            // 8192 tokens 12.5 us, 20 with eight a wave; 65536 tokens 62 and 51)
-            if (a.T <= 16384 || a.K > 16) run(sigmoid, plain, std::integral_constant<int, 64>{});
-            else if (a.K <= 8) run(sigmoid, plain, std::integral_constant<int, 8>{});
-            else run(sigmoid, plain, std::integral_constant<int, 16>{});
+            if constexpr (V <= 4 || (V == 8 && decltype(plain)::value))
+                if (a.T > (V <= 2 ? 8191 : 16384) && a.K <= 16) {
+                    if (a.K <= 8) run(sigmoid, plain, std::integral_constant<int, 8>{});
+                    else run(sigmoid, plain, std::integral_constant<int, 16>{});
+                    return;
+                }
+            run(sigmoid, plain, std::integral_constant<int, 64>{});
         };
         if (a.score == MOE_EP_SIGMOID) by_picks(std::true_type{}, std::false_type{});
         else if (a.grad_weights && !a.renormalize) by_picks(std::false_type{}, std::true_type{});

@@ -1,6 +1,6 @@
-"""GPU: the router's gradient where a wave has several tokens (more than 16384 of them:
-picks in 8 or 16 lanes each), in every width of its experts, and both training terms
-with more sequences than a grid has blocks."""
+"""GPU: the router's gradient of so many tokens that a wave has several (picks in 8 or 16
+lanes each; one a wave for many experts), in every width of its experts, and both
+training terms with more sequences than a grid has blocks."""
 import math
 
 import pytest
@@ -19,6 +19,8 @@ BF16, F32 = torch.bfloat16, torch.float32
 
 WAVES = [
     # T, E, K, S, dtype, grad dtype, masked, through
+    (8191, 64, 6, 2, F32, F32, 0.0, "both"),
+    (8192, 128, 6, 2, F32, F32, 0.0, "both"),
     (16385, 8, 2, 1, F32, F32, 0.0, "both"),
     (16391, 60, 8, 40, BF16, F32, 0.2, "both"),
     (17001, 64, 9, 3, F32, BF16, 0.0, "both"),
