@@ -13,8 +13,8 @@
 // a block's tokens, at most 256 to a wave, and fp64 over blocks, always in the same
 // order. Counts are integers. Where terms of the gradient cancel they are fp64.
 //
-// Bound by the logits' bytes only at many tokens (65536 x 256, fp32: the sums 19 us
-// at 3.6 TB/s and their join 7, the gradient 38, of some 250 instructions a token);
+// Bound by the logits' bytes only at many tokens (65536 x 256, fp32: the sums 18 us
+// at 3.7 TB/s and their join 7, the gradient 38, of 270 vector instructions a token);
 // below by chains of loads and of sums over lanes, so a wave has several tokens at
 // once (8192 tokens: 15 us the loss, 12 the gradient; 128: 13 and 5.6).
 #include <type_traits>

@@ -5,9 +5,9 @@
 // code times scale, is exact in bf16 (as is a code times a power of two): the
 // weights are made there in registers and multiplied in the bf16 matrix cores,
 // with fp32 sums of exact products. f, one factor for a matrix, is applied to
-// the sum. 32 experts of 15575 rows, 7168 -> 2 x 2048, E4M3: 880 to 950 us; 8 of
-// 917 rows 82; 25 of one or two rows 88 (4.7 TB/s); one token 9 (with 2048 -> 7168
-// and powers of two, 917 rows: 44).
+// the sum. 32 experts of 15575 rows, 7168 -> 2 x 2048, E4M3: 917 us one after the
+// other, 979 (919 to 1129) each by itself; 8 of 917 rows 82; 25 of one or two rows 88
+// (4.7 TB/s); one token 9 (with 2048 -> 7168 and powers of two, 917 rows: 45 and 47).
 #include "product_tiles.h"
 
 namespace moe_ep {
@@ -956,7 +956,7 @@ __device__ __forceinline__ void only_few_rows(const W4Args& a, uint8_t* lds, int
 }
 
 // Three kernels, since beside more code few rows take longer (by expert, 32 of one
-// or two rows or none, 2048 -> 7168, powers of two: 43, 45 and 50 us): with few-row
+// or two rows or none, 2048 -> 7168, powers of two: 43, 43 and 50 us): with few-row
 // tiles only; with tiles of 32 rows too, for groups of up to 32 rows (32 experts of
 // 32 rows, 7168 -> 2 x 2048, E4M3: 281 us without, 129 with); and with all.
 template <int GROUP, bool GATED>
